@@ -11,6 +11,8 @@
  *     (DeepSeek-V4.1-Flash-1017 · exlr8 page, "Stores").
  * Every bit-level rule (tile order, bit order, tail-biting windows, nibble order, rounding)
  * is the one in FORMAT.md, rules F1-F14.
+ * It also multiplies dense (unrouted) FP8 projections with one fp32 scale per 128 x 128 block
+ * (fp8b128, FORMAT F22-F26), with their gated feed-forward form and the backward passes.
  *
  * Conventions for every entry point:
  *   - Pointers marked "device" are device memory owned by the caller; the library never
@@ -57,6 +59,9 @@ extern "C" {
                        /* fp8 matrix cores with the stored E2M1 codes and their scales      */
                        /* (MXFP4), or with the T16 values rounded to E4M3 (trellis, FORMAT  */
                        /* F19); prefill mode (TQ_AUTO takes it; with TQ_GEMV an error)      */
+
+/* ---- flag of the fp8b128 products --------------------------------------------------------- */
+#define TQ_OUT_BF16 32u /* y is bf16 instead of fp32                                           */
 
 /* ---- device status bits (tq_device_status) ------------------------------------------ */
 #define TQ_STATUS_BAD_EXPERT 1u  /* an id outside [-1, E): that slot's output is NaN    */
@@ -430,6 +435,113 @@ int trellis_expert_gemm_noalloc(const tq_trellis_layer* L, const void* x, int64_
 size_t tq_workspace_bytes(int64_t T, int32_t topk, int32_t E, int32_t out, int32_t in,
                           uint32_t flags);
 
+/*
+ * A dense projection in the fp8b128 store (FORMAT F22), the layout in which block-scaled FP8
+ * checkpoints are published: E4M3 codes, HF orientation, and one fp32 scale per block of
+ * 128 outputs x 128 inputs; the last block of a row or column may be a part of one.
+ *   W[o][i] = scales[o / 128][i / 128] * E4M3[codes[o][i]]
+ */
+typedef struct tq_fp8b128_layer {
+  int32_t out;          /* output channels, a multiple of 16 up to 2^20                        */
+  int32_t in;           /* inputs, a multiple of 16 up to 2^20; out * in below 2^31            */
+  const uint8_t* codes; /* device [out][in], 16-byte aligned                                   */
+  const float* scales;  /* device [ceil(out / 128)][ceil(in / 128)]: any fp32 values           */
+} tq_fp8b128_layer;
+
+/*
+ * fp8b128_quantize — bf16 rows in 8 bits (FORMAT F23): per block of 128 consecutive inputs of
+ * a row (the last may be shorter) the scale 2^k, k the smallest integer >= -126 with
+ * max|x| <= 448 * 2^k (1 for an all-zero block), and each element's E4M3 code, the nearest
+ * (ties to even) to x * 2^-k. A block holding an infinity or NaN gets the scale NaN and zero
+ * codes. The activations of the products below, and the 8-bit form in which a training program
+ * keeps them for the backward pass.
+ *   x       device bf16 [rows][n], 16-byte aligned; n a multiple of 16 up to 2^20.
+ *   codes   device uint8 [rows][n], 16-byte aligned.
+ *   scales  device fp32 [rows][ceil(n / 128)].
+ * Here and below a call's rows times their longest width must not exceed 2^33 elements.
+ */
+int fp8b128_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, float* scales,
+                     void* stream);
+
+/*
+ * fp8b128_gemm — the 8-bit product (FORMAT F24):
+ *   y[t][o] = sum over i of X[t][i] * W[o][i],  X[t][i] = xs[t][i / 128] * E4M3[xq[t][i]]
+ * A block's products are added by the matrix cores and its two scales applied in fp32.
+ *   L      host: the projection.
+ *   xq     device uint8 [T][L->in], 16-byte aligned: E4M3 codes (fp8b128_quantize).
+ *   xs     device fp32 [T][ceil(L->in / 128)]: any fp32 values.
+ *   T      tokens (0 is a successful no-op).
+ *   y      device [T][L->out], 16-byte aligned: fp32, or bf16 with TQ_OUT_BF16.
+ *   flags  0 or TQ_OUT_BF16. The fp32 result is made of exact products added in fp32 (bf16
+ *          matrix cores, the codes converted exactly); the bf16 result comes from the fp8
+ *          matrix cores, whose sums over a block are good to about 2^-15 of the block's norm,
+ *          below half a step of bf16.
+ * NaN codes, infinite or NaN scales give NaN in the outputs they enter. The same call gives the
+ * same bits; a token's bits may depend on T, which decides how the inputs are split.
+ */
+int fp8b128_gemm(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs, int64_t T,
+                 void* y, uint32_t flags, void* stream);
+
+/*
+ * fp8b128_gated — the gated feed-forward product, both projections, the activation and the
+ * product in one kernel (FORMAT F25):
+ *   g = X Wg^T, u = X Wu^T (fp32),  h = g / (1 + e^-g) * u, rounded to bf16 once
+ *   gate_up  host: out = 2I, the gate's I channels, then the up's; I a multiple of 16.
+ *   h        device bf16 [T][I], 16-byte aligned.
+ * Other arguments as fp8b128_gemm.
+ */
+int fp8b128_gated(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const float* xs, int64_t T,
+                  void* h, void* stream);
+
+/*
+ * fp8b128_gemm_backward — the gradients of y = X W^T (FORMAT F26):
+ *   dx[t][i] = sum over o of dy[t][o] * W[o][i],   dw[o][i] = sum over t of dy[t][o] * X[t][i]
+ * with respect to the values X and W stand for (no gradient passes through the rounding to
+ * codes or to the scales), on the bf16 matrix cores in fp32, rounded to bf16 once.
+ *   dy   device bf16 [T][L->out], 16-byte aligned.
+ *   dx   device bf16 [T][L->in], 16-byte aligned, or NULL (not wanted).
+ *   dw   device bf16 [L->out][L->in], 16-byte aligned, or NULL. With T == 0 it is all zero.
+ *        X enters as bf16: exact for scales that are powers of two, as fp8b128_quantize
+ *        writes them, else rounded.
+ *   ws   device workspace of tq_fp8b128_workspace_bytes(T, L->out, L->in) bytes, 256-byte
+ *        aligned; need not be cleared. Calls that share one must be ordered on one stream.
+ * No output may overlap an input.
+ */
+int fp8b128_gemm_backward(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs,
+                          int64_t T, const void* dy, void* dx, void* dw, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * fp8b128_gated_backward — the gradients of h = silu(X Wg^T) * (X Wu^T) (FORMAT F26), from
+ * the 8-bit activations alone: g and u are computed again, with s = 1 / (1 + e^-g)
+ *   du = dh * g * s,   dg = dh * u * s * (1 + g * (1 - s))     (rounded to bf16)
+ *   dx = [dg du] W,    dw = [dg du]^T X                        as fp8b128_gemm_backward
+ *   dh   device bf16 [T][I], 16-byte aligned.
+ * Other arguments as fp8b128_gemm_backward, with gate_up in the place of L.
+ */
+int fp8b128_gated_backward(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const float* xs,
+                           int64_t T, const void* dh, void* dx, void* dw, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the two backward calls (0 for invalid sizes). */
+size_t tq_fp8b128_workspace_bytes(int64_t T, int32_t out, int32_t in);
+
+/*
+ * fp8b128_ffn — a dense gated FFN, such as a shared expert's, over two fp8b128 projections:
+ *   y = fp8b128_gemm(down, q(fp8b128_gated(gate_up, q(x)))),  q = fp8b128_quantize
+ * the same kernels on the same bits as those four calls, four launches.
+ *   gate_up  host: out = 2I, in = H.   down  host: out = H, in = I.
+ *   x        device bf16 [T][H], 16-byte aligned.
+ *   y        device [T][H], 16-byte aligned: fp32, or bf16 with TQ_OUT_BF16.
+ *   ws       device workspace of tq_fp8b128_ffn_workspace_bytes(T, H, I) bytes, 256-byte
+ *            aligned; need not be cleared. Calls that share one must be ordered on one stream.
+ */
+int fp8b128_ffn(const tq_fp8b128_layer* gate_up, const tq_fp8b128_layer* down, const void* x,
+                int64_t T, void* y, uint32_t flags, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of fp8b128_ffn (0 for invalid sizes). */
+size_t tq_fp8b128_ffn_workspace_bytes(int64_t T, int32_t H, int32_t I);
+
 /* Message of the last error on this thread ("" if none). */
 const char* tq_last_error(void);
 
@@ -438,9 +550,10 @@ int tq_device_status(void* ws, void* stream, uint32_t* flags_out);
 
 /*
  * Measurement hook, for benchmarks and profilers (not part of the computation). After this
- * call, the calling thread's next trellis_expert_gemm, mxfp4_expert_gemm or
- * trellis_expert_ffn times its main kernel (the grouped GEMV in the decode-batch mode, the
- * down projection's GEMV in the FFN, the grouped GEMM in the prefill mode): the kernel is
+ * call, the calling thread's next trellis_expert_gemm, mxfp4_expert_gemm, trellis_expert_ffn,
+ * fp8b128_gemm, fp8b128_gated or fp8b128_ffn times its main kernel (the grouped GEMV in the
+ * decode-batch mode, the down projection's GEMV or product in the FFNs, the grouped GEMM in the
+ * prefill mode): the kernel is
  * launched with hipExtLaunchKernel, which sets `start` and `stop` to the dispatch's own
  * start and end; under stream capture they are recorded on the stream right before and
  * after the launch instead (event-record nodes of the graph). The hook is then cleared.

@@ -31,6 +31,8 @@ from .routing import route_bucket
 from .gemm import expert_gemm, expert_gemm_values, expert_gemm_exact, combine_slots
 from .ffn import silu, silu_scalar, expert_ffn
 from .fp8b32 import fp8b32_unit_bytes, decode_fp8b32_unit, decode_fp8b32_weight_scalar
+from .fp8b128 import (fp8b128_blocks, fp8b128_scale, fp8b128_quantize, fp8b128_activations,
+                      fp8b128_weights, fp8b128_gated, fp8b128_gated_grads)
 from .codebooks import (MUL1_MULT, PMCGX_MULTS, mul1_value, mul1_value_array, decode_unit_mul1,
                         decode_unit_mul1_scalar, pmcgx_half_sum, pmcgx_pair_codes,
                         decode_unit_pmcgx, decode_unit_pmcgx_scalar, pmcgx_values, mul1_e4m3)

@@ -27,6 +27,7 @@ TQ_GEMM = 2
 TQ_COMBINE = 4
 TQ_ROTATE = 8
 TQ_FP8 = 16
+TQ_OUT_BF16 = 32
 TQ_CODEBOOK_T16, TQ_CODEBOOK_MUL1, TQ_CODEBOOK_PMCGX = 0, 1, 2
 
 TQ_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -63,6 +64,15 @@ class Mxfp4LayerC(ctypes.Structure):
     ]
 
 
+class Fp8b128LayerC(ctypes.Structure):
+    _fields_ = [
+        ("out", ctypes.c_int32),
+        ("in_", ctypes.c_int32),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -90,6 +100,17 @@ SIGNATURES = {
                                           _P, _I64, _P, _P, _I32, _P, _U32, _P, _SZ, _P]),
     "trellis_expert_gemm_noalloc": (ctypes.c_int, [ctypes.POINTER(TrellisLayerC), _P, _I64, _P,
                                                    _P, _I32, _P, _U32, _P]),
+    "fp8b128_quantize": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
+    "fp8b128_gemm": (ctypes.c_int, [ctypes.POINTER(Fp8b128LayerC), _P, _P, _I64, _P, _U32, _P]),
+    "fp8b128_gated": (ctypes.c_int, [ctypes.POINTER(Fp8b128LayerC), _P, _P, _I64, _P, _P]),
+    "fp8b128_gemm_backward": (ctypes.c_int, [ctypes.POINTER(Fp8b128LayerC), _P, _P, _I64, _P, _P,
+                                             _P, _P, _SZ, _P]),
+    "fp8b128_gated_backward": (ctypes.c_int, [ctypes.POINTER(Fp8b128LayerC), _P, _P, _I64, _P, _P,
+                                              _P, _P, _SZ, _P]),
+    "fp8b128_ffn": (ctypes.c_int, [ctypes.POINTER(Fp8b128LayerC), ctypes.POINTER(Fp8b128LayerC),
+                                   _P, _I64, _P, _U32, _P, _SZ, _P]),
+    "tq_fp8b128_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "tq_fp8b128_ffn_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
     "tq_ffn_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32, _I32, _U32]),
     "tq_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32, _I32, _U32]),
     "tq_last_error": (ctypes.c_char_p, []),

@@ -1256,3 +1256,295 @@ int trellis_expert_ffn(const tq_trellis_layer* gate_up, const tq_trellis_layer* 
 }
 
 }  // extern "C"
+
+// ---- the fp8b128 store ---------------------------------------------------------------------
+namespace {
+
+// Elements of one operand or result of a call: keeps every grid below 2^32 threads.
+constexpr int64_t FB_MAX_ELEMENTS = (int64_t)1 << 33;
+constexpr int FB_MAX_DIM = 1 << 20;
+
+int fb_blocks(int n) { return (n + 127) / 128; }
+
+int check_fp8b128_layer(const tq_fp8b128_layer* L) {
+  if (!L) return fail(TQ_EINVAL, "layer is NULL");
+  if (L->out <= 0 || L->out % 16 || L->out > FB_MAX_DIM)
+    return fail(TQ_EINVAL, "out = %d is not a multiple of 16 in 16..%d", L->out, FB_MAX_DIM);
+  if (L->in <= 0 || L->in % 16 || L->in > FB_MAX_DIM)
+    return fail(TQ_EINVAL, "in = %d is not a multiple of 16 in 16..%d", L->in, FB_MAX_DIM);
+  if ((int64_t)L->out * L->in >= ((int64_t)1 << 31))
+    return fail(TQ_EINVAL, "out * in must stay below 2^31");
+  if (!L->codes || !L->scales) return fail(TQ_EINVAL, "codes or scales is NULL");
+  if (!aligned(L->codes, 16)) return fail(TQ_EALIGN, "codes must be 16-byte aligned");
+  if (!aligned(L->scales, 4)) return fail(TQ_EALIGN, "scales must be 4-byte aligned");
+  return TQ_OK;
+}
+
+int check_gated(const tq_fp8b128_layer* L) {
+  if (L->out % 32)
+    return fail(TQ_EINVAL, "gate_up has I = out / 2 gate channels, a multiple of 16 (out = %d)",
+                L->out);
+  return TQ_OK;
+}
+
+int check_tokens(int64_t T, int64_t width) {
+  if (T < 0) return fail(TQ_EINVAL, "T = %lld is negative", (long long)T);
+  if (T > FB_MAX_ELEMENTS / width)
+    return fail(TQ_EINVAL, "T = %lld rows of %lld exceed 2^33 elements", (long long)T,
+                (long long)width);
+  return TQ_OK;
+}
+
+int check_activations(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs, int64_t T) {
+  int rc = check_tokens(T, std::max(L->out, L->in));
+  if (rc) return rc;
+  if (T == 0) return TQ_OK;
+  if (!xq || !xs) return fail(TQ_EINVAL, "xq or xs is NULL");
+  if (!aligned(xq, 16)) return fail(TQ_EALIGN, "xq must be 16-byte aligned");
+  if (!aligned(xs, 4)) return fail(TQ_EALIGN, "xs must be 4-byte aligned");
+  return TQ_OK;
+}
+
+int check_rows(const void* p, const char* name, int64_t T) {
+  if (T == 0) return TQ_OK;
+  if (!p) return fail(TQ_EINVAL, "%s is NULL", name);
+  if (!aligned(p, 16)) return fail(TQ_EALIGN, "%s must be 16-byte aligned", name);
+  return TQ_OK;
+}
+
+tq::Fp8b128GemmArgs forward_args(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs,
+                                 int64_t T, void* y) {
+  tq::Fp8b128GemmArgs a{};
+  a.w = L->codes;
+  a.ws = L->scales;
+  a.x = xq;
+  a.xs = xs;
+  a.y = y;
+  a.T = T;
+  a.out = L->out;
+  a.in = L->in;
+  a.nb = fb_blocks(L->in);
+  return a;
+}
+
+int timed_forward(const tq::Fp8b128GemmArgs& a, int epi, hipStream_t s, const char* what) {
+  hipError_t err = time_begin(s);
+  if (err != hipSuccess) return hip_fail(err, "hipEventRecord");
+  err = tq::launch_fp8b128_gemm(a, epi, s);
+  if (err == hipSuccess) err = time_end(s);
+  if (err != hipSuccess) return hip_fail(err, what);
+  return ok();
+}
+
+// dx and dw of y = X W^T from bf16 dy; either may be NULL.
+int backward_products(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs, int64_t T,
+                      const uint16_t* dy, void* dx, void* dw, hipStream_t s) {
+  tq::Fp8b128BackwardArgs a{};
+  a.w = L->codes;
+  a.ws = L->scales;
+  a.x = xq;
+  a.xs = xs;
+  a.dy = dy;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dw = static_cast<uint16_t*>(dw);
+  a.T = T;
+  a.out = L->out;
+  a.in = L->in;
+  a.nb = fb_blocks(L->in);
+  hipError_t err = hipSuccess;
+  if (dx) err = tq::launch_fp8b128_dx(a, s);
+  if (err == hipSuccess && dw) err = tq::launch_fp8b128_dw(a, s);
+  if (err != hipSuccess) return hip_fail(err, "fp8b128 gradient launch");
+  return ok();
+}
+
+int check_gradients(const tq_fp8b128_layer* L, void* dx, void* dw, int64_t T) {
+  if (!dx && !dw) return fail(TQ_EINVAL, "dx and dw are both NULL");
+  if (!aligned(dx, 16) || !aligned(dw, 16)) return fail(TQ_EALIGN, "dx and dw must be 16-byte aligned");
+  return TQ_OK;
+}
+
+// No tokens: dx has no rows and dw is a sum of nothing (a fill kernel, so graphs may hold it).
+int empty_gradients(const tq_fp8b128_layer* L, void* dw, hipStream_t s) {
+  if (!dw) return ok();
+  int rc = check_device();
+  if (rc) return rc;
+  hipError_t err = tq::launch_fill_i32(static_cast<int32_t*>(dw), (int64_t)L->out * L->in / 2, 0, s);
+  if (err != hipSuccess) return hip_fail(err, "dw clear launch");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8b128_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, float* scales,
+                     void* stream) {
+  if (n <= 0 || n % 16 || n > FB_MAX_DIM)
+    return fail(TQ_EINVAL, "n = %lld is not a multiple of 16 in 16..%d", (long long)n, FB_MAX_DIM);
+  int rc = check_tokens(rows, n);
+  if (rc) return rc;
+  if (rows == 0) return ok();
+  if (!x || !codes || !scales) return fail(TQ_EINVAL, "x, codes or scales is NULL");
+  if (!aligned(x, 16) || !aligned(codes, 16))
+    return fail(TQ_EALIGN, "x and codes must be 16-byte aligned");
+  if (!aligned(scales, 4)) return fail(TQ_EALIGN, "scales must be 4-byte aligned");
+  rc = check_device();
+  if (rc) return rc;
+  hipError_t err = tq::launch_fp8b128_quantize(static_cast<const uint16_t*>(x), rows, (int)n, codes,
+                                               scales, static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) return hip_fail(err, "fp8b128_quantize launch");
+  return ok();
+}
+
+int fp8b128_gemm(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs, int64_t T, void* y,
+                 uint32_t flags, void* stream) {
+  int rc = check_fp8b128_layer(L);
+  if (rc) return rc;
+  if (flags & ~TQ_OUT_BF16) return fail(TQ_EINVAL, "flags = 0x%x is not valid", flags);
+  rc = check_activations(L, xq, xs, T);
+  if (rc) return rc;
+  rc = check_rows(y, "y", T);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  rc = check_device();
+  if (rc) return rc;
+  return timed_forward(forward_args(L, xq, xs, T, y), (flags & TQ_OUT_BF16) ? tq::FB_BF16 : tq::FB_F32,
+                       static_cast<hipStream_t>(stream), "fp8b128 product launch");
+}
+
+int fp8b128_gated(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const float* xs, int64_t T,
+                  void* h, void* stream) {
+  int rc = check_fp8b128_layer(gate_up);
+  if (rc) return rc;
+  rc = check_gated(gate_up);
+  if (rc) return rc;
+  rc = check_activations(gate_up, xq, xs, T);
+  if (rc) return rc;
+  rc = check_rows(h, "h", T);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  rc = check_device();
+  if (rc) return rc;
+  return timed_forward(forward_args(gate_up, xq, xs, T, h), tq::FB_GATED,
+                       static_cast<hipStream_t>(stream), "fp8b128 gated product launch");
+}
+
+size_t tq_fp8b128_workspace_bytes(int64_t T, int32_t out, int32_t in) {
+  if (T < 0 || out < 16 || in < 16) return 0;
+  return round_up((size_t)T * out * 2, 256);  // the gradients of gate and up
+}
+
+int fp8b128_gemm_backward(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs, int64_t T,
+                          const void* dy, void* dx, void* dw, void* ws, size_t ws_bytes,
+                          void* stream) {
+  int rc = check_fp8b128_layer(L);
+  if (rc) return rc;
+  rc = check_activations(L, xq, xs, T);
+  if (rc) return rc;
+  rc = check_rows(dy, "dy", T);
+  if (rc) return rc;
+  rc = check_gradients(L, dx, dw, T);
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (T == 0) return empty_gradients(L, dw, s);
+  rc = check_ws(ws, ws_bytes, tq_fp8b128_workspace_bytes(T, L->out, L->in));
+  if (rc) return rc;
+  rc = check_device();
+  if (rc) return rc;
+  return backward_products(L, xq, xs, T, static_cast<const uint16_t*>(dy), dx, dw, s);
+}
+
+int fp8b128_gated_backward(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const float* xs,
+                           int64_t T, const void* dh, void* dx, void* dw, void* ws,
+                           size_t ws_bytes, void* stream) {
+  int rc = check_fp8b128_layer(gate_up);
+  if (rc) return rc;
+  rc = check_gated(gate_up);
+  if (rc) return rc;
+  rc = check_activations(gate_up, xq, xs, T);
+  if (rc) return rc;
+  rc = check_rows(dh, "dh", T);
+  if (rc) return rc;
+  rc = check_gradients(gate_up, dx, dw, T);
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (T == 0) return empty_gradients(gate_up, dw, s);
+  rc = check_ws(ws, ws_bytes, tq_fp8b128_workspace_bytes(T, gate_up->out, gate_up->in));
+  if (rc) return rc;
+  rc = check_device();
+  if (rc) return rc;
+  uint16_t* dgu = at<uint16_t>(ws, 0);
+  tq::Fp8b128GemmArgs a = forward_args(gate_up, xq, xs, T, dgu);
+  a.dh = static_cast<const uint16_t*>(dh);
+  hipError_t err = tq::launch_fp8b128_gemm(a, tq::FB_GATED_GRAD, s);
+  if (err != hipSuccess) return hip_fail(err, "fp8b128 gate and up gradient launch");
+  return backward_products(gate_up, xq, xs, T, dgu, dx, dw, s);
+}
+
+namespace {
+
+struct Fp8b128FfnWs {
+  size_t xq, xs, h, hq, hs, total;
+};
+
+Fp8b128FfnWs fp8b128_ffn_ws(int64_t T, int H, int I) {
+  Fp8b128FfnWs w{};
+  size_t off = 0;
+  w.xq = off;
+  off += round_up((size_t)T * H, 256);
+  w.xs = off;
+  off += round_up((size_t)T * fb_blocks(H) * 4, 256);
+  w.h = off;
+  off += round_up((size_t)T * I * 2, 256);
+  w.hq = off;
+  off += round_up((size_t)T * I, 256);
+  w.hs = off;
+  off += round_up((size_t)T * fb_blocks(I) * 4, 256);
+  w.total = off;
+  return w;
+}
+
+}  // namespace
+
+size_t tq_fp8b128_ffn_workspace_bytes(int64_t T, int32_t H, int32_t I) {
+  if (T < 0 || H < 16 || I < 16) return 0;
+  return fp8b128_ffn_ws(T, H, I).total;
+}
+
+int fp8b128_ffn(const tq_fp8b128_layer* gate_up, const tq_fp8b128_layer* down, const void* x,
+                int64_t T, void* y, uint32_t flags, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_fp8b128_layer(gate_up);
+  if (rc) return rc;
+  rc = check_gated(gate_up);
+  if (rc) return rc;
+  rc = check_fp8b128_layer(down);
+  if (rc) return rc;
+  const int H = gate_up->in, I = gate_up->out / 2;
+  if (down->in != I || down->out != H)
+    return fail(TQ_EINVAL, "down must be in = gate_up.out / 2 (%d), out = gate_up.in (%d)", I, H);
+  if (flags & ~TQ_OUT_BF16) return fail(TQ_EINVAL, "flags = 0x%x is not valid", flags);
+  rc = check_tokens(T, std::max(H, 2 * I));
+  if (rc) return rc;
+  rc = check_rows(x, "x", T);
+  if (rc) return rc;
+  rc = check_rows(y, "y", T);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  const Fp8b128FfnWs W = fp8b128_ffn_ws(T, H, I);
+  rc = check_ws(ws, ws_bytes, W.total);
+  if (rc) return rc;
+  uint8_t *xq = at<uint8_t>(ws, W.xq), *hq = at<uint8_t>(ws, W.hq);
+  float *xs = at<float>(ws, W.xs), *hs = at<float>(ws, W.hs);
+  uint16_t* h = at<uint16_t>(ws, W.h);
+  rc = fp8b128_quantize(x, T, H, xq, xs, stream);
+  if (rc) return rc;
+  hipError_t err = tq::launch_fp8b128_gemm(forward_args(gate_up, xq, xs, T, h), tq::FB_GATED,
+                                           static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) return hip_fail(err, "fp8b128 gated product launch");
+  rc = fp8b128_quantize(h, T, I, hq, hs, stream);
+  if (rc) return rc;
+  return fp8b128_gemm(down, hq, hs, T, y, flags, stream);
+}
+
+}  // extern "C"

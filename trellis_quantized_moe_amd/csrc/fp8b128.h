@@ -1,0 +1,103 @@
+// Device pieces shared by the kernels of the fp8b128 store (FORMAT F22-F25): E4M3 codes with
+// one fp32 scale per 128 x 128 block of a weight and per 128 inputs of an activation row.
+#pragma once
+
+#include "gemm_core.h"
+
+namespace tq {
+
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int FB_BLOCK = 128;         // inputs (and outputs) per scale
+constexpr uint32_t FB_OOB = 0x80000000u;  // a buffer offset past every resource: loads give 0
+
+// Four E4M3 codes as four bf16 values (exact: bf16 holds every E4M3 value).
+__device__ __forceinline__ u32x2 fb_bf16_of4(uint32_t c) {
+  u32x2 r;
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
+  return r;
+}
+// Eight E4M3 codes as one bf16 matrix-core operand.
+__device__ __forceinline__ u32x4 fb_bf16_of8(uint32_t c0, uint32_t c1) {
+  const u32x2 a = fb_bf16_of4(c0), b = fb_bf16_of4(c1);
+  return (u32x4){a.x, a.y, b.x, b.y};
+}
+
+// Two fp32 values rounded to bf16 (nearest, ties to even), packed.
+__device__ __forceinline__ uint32_t fb_pack_bf16(float lo, float hi) {
+  const bf16x2 h = __builtin_convertvector((f32x2){lo, hi}, bf16x2);
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// The sum over one block of 128 inputs of the products of two rows' codes, for a 16 x 16 tile:
+// lane (r = l % 16, q = l / 16) holds bytes 16 q .. 16 q + 15 and 64 + 16 q .. 64 + 16 q + 15
+// of row r of A and of row r of B; result element i is D[4 q + i][r].
+//
+// EXACT: the codes become bf16 (exactly) and four v_mfma_f32_16x16x32_bf16 add the exact
+// products in fp32. Else one v_mfma_f32_16x16x128_f8f6f4, at twice the rate: the fp8 matrix
+// cores align the products of an instruction to the largest one and drop bits below about
+// 2^-17 of it (measured on block-scaled normal data: 1.5e-5 to 5e-5 of a block's sum in the
+// 2-norm, unbiased, against 1e-8 with bf16), which is far below half a step of a bf16
+// result (2^-9) and is used only where the result is rounded to bf16.
+template <bool EXACT>
+__device__ __forceinline__ f32x4 fb_block_product(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1) {
+  f32x4 p = (f32x4){0.f, 0.f, 0.f, 0.f};
+  if constexpr (EXACT) {
+    p = mfma_bf16(fb_bf16_of8(a0.x, a0.y), fb_bf16_of8(b0.x, b0.y), p);
+    p = mfma_bf16(fb_bf16_of8(a0.z, a0.w), fb_bf16_of8(b0.z, b0.w), p);
+    p = mfma_bf16(fb_bf16_of8(a1.x, a1.y), fb_bf16_of8(b1.x, b1.y), p);
+    p = mfma_bf16(fb_bf16_of8(a1.z, a1.w), fb_bf16_of8(b1.z, b1.w), p);
+  } else {
+    const i32x8 a = (i32x8){(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w,
+                            (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
+    const i32x8 b = (i32x8){(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w,
+                            (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
+    // scale operands of zero select the instruction without block scales
+    p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, p, 0, 0, 0, 0, 0, 0);
+  }
+  return p;
+}
+
+// ---- epilogues ------------------------------------------------------------------------------
+// What a forward kernel does with the sums of four consecutive channels o .. o + 3 of one
+// token (gated forms: g and u are the sums of gate and up channels o .. o + 3).
+__device__ __forceinline__ float fb_sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+
+template <int EPI>
+__device__ __forceinline__ void fb_store(const Fp8b128GemmArgs& a, int64_t t, int o, f32x4 g,
+                                         f32x4 u) {
+  if constexpr (EPI == FB_F32) {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + t * a.out + o) = g;
+  } else if constexpr (EPI == FB_BF16) {
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + t * a.out + o) =
+        (u32x2){fb_pack_bf16(g[0], g[1]), fb_pack_bf16(g[2], g[3])};
+  } else if constexpr (EPI == FB_GATED) {
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = g[i] * fb_sigmoid(g[i]) * u[i];
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + t * (a.out / 2) + o) =
+        (u32x2){fb_pack_bf16(h[0], h[1]), fb_pack_bf16(h[2], h[3])};
+  } else {
+    // d silu(g) / dg = s + g s (1 - s) with s = sigmoid(g); the two gradients are rounded to
+    // bf16, the operand type of the two products that read them
+    const u32x2 d2 = *reinterpret_cast<const u32x2*>(a.dh + t * (a.out / 2) + o);
+    const float dh[4] = {bf16_lo_to_f32(d2.x), bf16_hi_to_f32(d2.x), bf16_lo_to_f32(d2.y),
+                         bf16_hi_to_f32(d2.y)};
+    float dg[4], du[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float s = fb_sigmoid(g[i]);
+      dg[i] = dh[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+      du[i] = dh[i] * g[i] * s;
+    }
+    uint16_t* row = static_cast<uint16_t*>(a.y) + t * a.out + o;
+    *reinterpret_cast<u32x2*>(row) = (u32x2){fb_pack_bf16(dg[0], dg[1]), fb_pack_bf16(dg[2], dg[3])};
+    *reinterpret_cast<u32x2*>(row + a.out / 2) =
+        (u32x2){fb_pack_bf16(du[0], du[1]), fb_pack_bf16(du[2], du[3])};
+  }
+}
+
+constexpr bool fb_gated(int epi) { return epi == FB_GATED || epi == FB_GATED_GRAD; }
+
+}  // namespace tq

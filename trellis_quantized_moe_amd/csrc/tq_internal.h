@@ -302,6 +302,40 @@ hipError_t launch_ffn_mid(const FfnMidArgs& a, bool decode, hipStream_t s);
 // The FFN's two decode-batch plans (gate/up over T tokens, down over the T * topk slots as
 // rows) and the gate/up activation prep, in one launch.
 hipError_t launch_ffn_plan(const PlanArgs& gate_up, const PlanArgs& down, hipStream_t s);
+// ---- the fp8b128 store (FORMAT F22-F26) ----------------------------------------------------
+// What a forward product writes.
+enum Fp8b128Epilogue {
+  FB_F32,         // y fp32 [T][out], from exact products
+  FB_BF16,        // y bf16 [T][out]
+  FB_GATED,       // h bf16 [T][out / 2] = silu(gate) * up
+  FB_GATED_GRAD,  // bf16 [T][out]: the gradients of gate and up, from dh
+};
+struct Fp8b128GemmArgs {
+  const uint8_t* w;    // E4M3 codes [out][in]
+  const float* ws;     // [ceil(out / 128)][nb]
+  const uint8_t* x;    // E4M3 codes [T][in]
+  const float* xs;     // [T][nb]
+  const uint16_t* dh;  // FB_GATED_GRAD: bf16 [T][out / 2]
+  void* y;
+  int64_t T;
+  int out, in, nb;     // nb = ceil(in / 128)
+};
+hipError_t launch_fp8b128_gemm(const Fp8b128GemmArgs& a, int epi, hipStream_t s);
+struct Fp8b128BackwardArgs {
+  const uint8_t* w;
+  const float* ws;
+  const uint8_t* x;
+  const float* xs;
+  const uint16_t* dy;  // bf16 [T][out]
+  uint16_t* dx;        // bf16 [T][in]
+  uint16_t* dw;        // bf16 [out][in]
+  int64_t T;
+  int out, in, nb;
+};
+hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s);
+hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& a, hipStream_t s);
+hipError_t launch_fp8b128_quantize(const uint16_t* x, int64_t rows, int n, uint8_t* codes,
+                                   float* scales, hipStream_t s);
 hipError_t launch_nvfp4_transcode(const uint8_t* units, int E, int out, int in,
                                   uint8_t* codes, uint8_t* scales, float* scale2,
                                   uint8_t* status, hipStream_t s);

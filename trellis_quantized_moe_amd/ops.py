@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from ._lib import (TQ_AUTO, TQ_COMBINE, TQ_GEMM, TQ_GEMV, TQ_LAYOUT_GEMV,  # noqa: F401
-                   TQ_LAYOUT_STORE, TQ_LAYOUT_UNIT128, TQ_ROTATE, TQ_FP8, TQ_CODEBOOK_T16,
+                   TQ_LAYOUT_STORE, TQ_LAYOUT_UNIT128, TQ_OUT_BF16, TQ_ROTATE, TQ_FP8, TQ_CODEBOOK_T16,
                    TQ_CODEBOOK_MUL1, TQ_CODEBOOK_PMCGX, check)
 
 
@@ -309,6 +309,189 @@ def mxfp4_to_nvfp4(layer, codes=None, scales=None, scale2=None, status=None):
     check(_lib.load().mxfp4_to_nvfp4(ctypes.byref(c), _ptr(codes), _ptr(scales), _ptr(scale2),
                                      _ptr(status), _stream(dev)))
     return codes, scales, scale2, status
+
+
+@dataclass
+class Fp8b128Layer:
+    """A dense projection in the fp8b128 store (see tq_fp8b128_layer in include/tq.h)."""
+    codes: torch.Tensor      # uint8 or float8_e4m3fn [out, in]
+    scales: torch.Tensor     # fp32 [ceil(out / 128), ceil(in / 128)]
+
+    def __post_init__(self):
+        _check_rows("codes", self.codes, _E4M3)
+        self.out, self.in_ = self.codes.shape
+        _check_rows("scales", self.scales, _F32, self.codes.device,
+                    (-(-self.out // 128), -(-self.in_ // 128)))
+        self._c = _lib.Fp8b128LayerC(self.out, self.in_, self.codes.data_ptr(),
+                                     self.scales.data_ptr())
+
+    @classmethod
+    def from_host(cls, layer, device="cuda"):
+        return cls(torch.from_numpy(np.ascontiguousarray(layer["codes"], dtype=np.uint8)).to(device),
+                   torch.from_numpy(np.ascontiguousarray(layer["scales"], dtype=np.float32)).to(device))
+
+    def c_struct(self):
+        return self._c
+
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_F32 = (torch.float32,)
+
+
+def _check_rows(name, t, dtypes, device=None, shape=None):
+    """The kernels read raw pointers: a tensor has to be on the GPU, contiguous, of one of
+    `dtypes` and, where they are given, on `device` and of `shape`."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if t.dtype not in dtypes:
+        raise ValueError("%s is %s, not %s" % (name, t.dtype, dtypes[0]))
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous 2-D tensor" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, not %s" % (name, t.device, device))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _call_on(device, fn, *args):
+    """fn(*args, stream) on the device's current stream, with that device current (a kernel
+    launched while another device is current would not run on it)."""
+    if torch.cuda.current_device() == device.index:
+        check(fn(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, _stream(device)))
+
+
+def _check_ws(ws, device, nbytes):
+    """The given workspace, or a new one (the fp8b128 calls need no cleared memory)."""
+    if ws is None:
+        return torch.empty(max(256, nbytes), dtype=torch.uint8, device=device)
+    if not ws.is_cuda or ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % device)
+    return ws
+
+
+def _check_fp8b128(layer, codes, scales):
+    """(T, device) of activations that fit the layer."""
+    dev = layer.codes.device
+    _check_rows("codes", codes, _E4M3, dev)
+    T = codes.shape[0]
+    if codes.shape[1] != layer.in_:
+        raise ValueError("codes have %d inputs, the layer %d" % (codes.shape[1], layer.in_))
+    _check_rows("scales", scales, _F32, dev, (T, -(-layer.in_ // 128)))
+    return T, dev
+
+
+def fp8b128_quantize(x, codes=None, scales=None):
+    """(codes uint8 [rows, n], scales fp32 [rows, ceil(n / 128)]): the 8-bit form of bf16 rows
+    with one power-of-two scale per 128 inputs (see fp8b128_quantize in include/tq.h)."""
+    _check_rows("x", x, _BF16)
+    rows, n = x.shape
+    nb = -(-n // 128)
+    if codes is None:
+        codes = torch.empty((rows, n), dtype=torch.uint8, device=x.device)
+    else:
+        _check_rows("codes", codes, _E4M3, x.device, (rows, n))
+    if scales is None:
+        scales = torch.empty((rows, nb), dtype=torch.float32, device=x.device)
+    else:
+        _check_rows("scales", scales, _F32, x.device, (rows, nb))
+    _call_on(x.device, _lib.load().fp8b128_quantize, x.data_ptr(), rows, n, codes.data_ptr(),
+             scales.data_ptr())
+    return codes, scales
+
+
+def fp8b128_gemm(layer, codes, scales, flags=0, out=None):
+    """[T, out]: quantized activations times an fp8b128 projection, fp32 or (TQ_OUT_BF16) bf16
+    (see fp8b128_gemm in include/tq.h)."""
+    T, dev = _check_fp8b128(layer, codes, scales)
+    dtype = torch.bfloat16 if flags & TQ_OUT_BF16 else torch.float32
+    if out is None:
+        out = torch.empty((T, layer.out), dtype=dtype, device=dev)
+    else:
+        _check_rows("out", out, (dtype,), dev, (T, layer.out))
+    _call_on(dev, _lib.load().fp8b128_gemm, ctypes.byref(layer.c_struct()), codes.data_ptr(),
+             scales.data_ptr(), T, out.data_ptr(), flags)
+    return out
+
+
+def fp8b128_gated(layer, codes, scales, out=None):
+    """bf16 [T, I]: silu(gate) * up of quantized activations over a fused gate/up projection
+    (out = 2I) (see fp8b128_gated in include/tq.h)."""
+    T, dev = _check_fp8b128(layer, codes, scales)
+    if out is None:
+        out = torch.empty((T, layer.out // 2), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_rows("out", out, _BF16, dev, (T, layer.out // 2))
+    _call_on(dev, _lib.load().fp8b128_gated, ctypes.byref(layer.c_struct()), codes.data_ptr(),
+             scales.data_ptr(), T, out.data_ptr())
+    return out
+
+
+def fp8b128_workspace(T, out, in_, device="cuda"):
+    """A workspace of the two backward calls (it need not be cleared)."""
+    n = int(_lib.load().tq_fp8b128_workspace_bytes(T, out, in_))
+    return torch.empty(max(256, n), dtype=torch.uint8, device=device)
+
+
+def _fp8b128_backward(fn, layer, codes, scales, dy, width, need_dx, need_dw, dx, dw, ws):
+    T, dev = _check_fp8b128(layer, codes, scales)
+    _check_rows("the output's gradient", dy, _BF16, dev, (T, width))
+    if dx is not None:
+        _check_rows("dx", dx, _BF16, dev, (T, layer.in_))
+    elif need_dx:
+        dx = torch.empty((T, layer.in_), dtype=torch.bfloat16, device=dev)
+    if dw is not None:
+        _check_rows("dw", dw, _BF16, dev, (layer.out, layer.in_))
+    elif need_dw:
+        dw = torch.empty((layer.out, layer.in_), dtype=torch.bfloat16, device=dev)
+    lib = _lib.load()
+    ws = _check_ws(ws, dev, lib.tq_fp8b128_workspace_bytes(T, layer.out, layer.in_))
+    _call_on(dev, getattr(lib, fn), ctypes.byref(layer.c_struct()), codes.data_ptr(),
+             scales.data_ptr(), T, dy.data_ptr(), None if dx is None else dx.data_ptr(),
+             None if dw is None else dw.data_ptr(), ws.data_ptr(), ws.numel())
+    return dx, dw
+
+
+def fp8b128_gemm_backward(layer, codes, scales, dy, need_dx=True, need_dw=True, dx=None, dw=None,
+                          ws=None):
+    """(dx bf16 [T, in], dw bf16 [out, in]): the gradients of fp8b128_gemm from dy [T, out];
+    None for one that is not needed (see fp8b128_gemm_backward in include/tq.h)."""
+    return _fp8b128_backward("fp8b128_gemm_backward", layer, codes, scales, dy, layer.out,
+                             need_dx, need_dw, dx, dw, ws)
+
+
+def fp8b128_gated_backward(layer, codes, scales, dh, need_dx=True, need_dw=True, dx=None, dw=None,
+                           ws=None):
+    """(dx bf16 [T, in], dw bf16 [2I, in]): the gradients of fp8b128_gated from dh [T, I] and
+    the 8-bit activations; None for one that is not needed (see fp8b128_gated_backward in
+    include/tq.h)."""
+    return _fp8b128_backward("fp8b128_gated_backward", layer, codes, scales, dh, layer.out // 2,
+                             need_dx, need_dw, dx, dw, ws)
+
+
+def fp8b128_ffn(gate_up, down, x, flags=0, out=None, ws=None):
+    """[T, H]: a dense gated FFN over two fp8b128 projections, fp32 or (TQ_OUT_BF16) bf16 (see
+    fp8b128_ffn in include/tq.h)."""
+    dev = gate_up.codes.device
+    _check_rows("x", x, _BF16, dev)
+    if down.codes.device != dev:
+        raise ValueError("the two layers are on different devices")
+    T, H = x.shape
+    if H != gate_up.in_:
+        raise ValueError("x has %d inputs, the layer %d" % (H, gate_up.in_))
+    dtype = torch.bfloat16 if flags & TQ_OUT_BF16 else torch.float32
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=dev)
+    else:
+        _check_rows("out", out, (dtype,), dev, (T, H))
+    lib = _lib.load()
+    ws = _check_ws(ws, dev, lib.tq_fp8b128_ffn_workspace_bytes(T, H, gate_up.out // 2))
+    _call_on(dev, lib.fp8b128_ffn, ctypes.byref(gate_up.c_struct()), ctypes.byref(down.c_struct()),
+             x.data_ptr(), T, out.data_ptr(), flags, ws.data_ptr(), ws.numel())
+    return out
 
 
 def device_status(ws):

@@ -19,6 +19,7 @@ layer, top-8 routing, 8,192-token prefill chunks):
   (exponents -8..-2);
 - fp8b32: codes uniform over the 254 non-NaN E4M3 bytes, E8M0 bytes uniform in
   113..119 (exponents -14..-8);
+- fp8b128: codes as fp8b32's, fp32 block scales U(0.5, 1.5) / (128 sqrt(in));
 - routes: top-k distinct experts per token, uniform or Zipf-skewed;
 - gates: softmax of topk N(0, 1) logits per token (fp32).
 """

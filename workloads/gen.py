@@ -7,6 +7,7 @@ __all__ = [
     "uniform_routes", "zipf_routes", "softmax_gates", "trellis_layer", "mxfp4_layer",
     "single_matrix", "one_unit", "mxfp4_decode_layer", "mixed_widths", "mixed_layer",
     "prefill_chunk", "mxfp4_prefill_chunk", "ffn_layers", "ffn_decode", "fp8b32_layer",
+    "fp8b128_layer",
     "shared_expert",
     "WORKLOADS",
 ]
@@ -152,6 +153,17 @@ def fp8b32_layer(workload, E, out, inputs, extra=()):
     units[:, :nc] = c + (c >= 0x7F) + (c >= 0xFE)  # skip 0x7F and 0xFF (NaN)
     units[:, nc:] = rng_for(workload, SCALES, *extra).integers(113, 120, size=(E, ns), dtype=np.uint8)
     return {"E": E, "out": out, "in": inputs, "units": units.reshape(-1)}
+
+
+def fp8b128_layer(workload, out, inputs, extra=()):
+    """A dense projection in the fp8b128 store: codes uniform over the 254 non-NaN E4M3 bytes,
+    fp32 scales U(0.5, 1.5) / (128 sqrt(in)), so that normal inputs give outputs near 1."""
+    c = rng_for(workload, CODES, *extra).integers(0, 254, size=(out, inputs), dtype=np.uint8)
+    codes = c + (c >= 0x7F) + (c >= 0xFE)  # skip 0x7F and 0xFF (NaN)
+    blocks = (-(-out // 128), -(-inputs // 128))
+    scales = rng_for(workload, SCALES, *extra).uniform(0.5, 1.5, size=blocks)
+    return {"out": out, "in": inputs, "codes": codes.astype(np.uint8),
+            "scales": (scales / (128.0 * np.sqrt(float(inputs)))).astype(np.float32)}
 
 
 def shared_expert(T=128, out=1536, inputs=5120):
