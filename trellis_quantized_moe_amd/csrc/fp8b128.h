@@ -59,6 +59,20 @@ __device__ __forceinline__ f32x4 fb_block_product(u32x4 a0, u32x4 a1, u32x4 b0, 
   return p;
 }
 
+// The tile of this workgroup: the grid is read as 8 interleaved streams, one per XCD, each a
+// contiguous range of tiles in an order that walks 4 channel tiles per token tile, so that the
+// tiles an XCD works on at one time share rows of both operands in its L2.
+__device__ inline bool fb_tile_of(int tt, int tc, int* t, int* c) {
+  const int n = tt * tc, per = (n + 7) >> 3, j = blockIdx.x >> 3;
+  const int u = (blockIdx.x & 7) * per + j;
+  if (j >= per || u >= n) return false;
+  const int band = u / (4 * tt), first = 4 * band, width = min(4, tc - first);
+  const int v = u - first * tt;
+  *c = first + v % width;
+  *t = v / width;
+  return true;
+}
+
 // ---- epilogues ------------------------------------------------------------------------------
 // What a forward kernel does with the sums of four consecutive channels o .. o + 3 of one
 // token (gated forms: g and u are the sums of gate and up channels o .. o + 3).

@@ -125,14 +125,176 @@ hipError_t launch_strips(const Fp8b128GemmArgs& a, hipStream_t s) {
   return launch_timed(fp8b128_strip_kernel<EPI, 4>, dim3(grid), dim3(FS_THREADS), s, a);
 }
 
+// ---- many tokens: tiles of both operands in LDS ----------------------------------------------
+//
+// A workgroup of 2 x WT waves owns 64 * WT tokens and 32 * SW weight rows (gated: the gate rows
+// of 16 * SW channels, then their up rows), wave (wc, wt) SW strips of 16 channels (gated: half
+// of them gate strips, half the up strips of the same channels, so that both sums of a channel
+// end in one lane) and 4 tiles of 16 tokens. Per block of 128 inputs the rows' 128 bytes go
+// straight to LDS (16-byte chunk c of row r at position c ^ (r % 8), so that eight lanes reading
+// one chunk of eight rows meet eight different banks' worth of LDS), one block ahead of the
+// products: two stages, one barrier per block.
+template <int SW, int WT>
+struct FbTile {
+  static constexpr int WAVES = 2 * WT, THREADS = 64 * WAVES, BC = 32 * SW, BT = 64 * WT;
+  alignas(16) uint8_t w[2][BC * 128];
+  alignas(16) uint8_t x[2][BT * 128];
+  alignas(16) float sx[2][BT];
+};
+
+template <int EPI, int SW, int WT>
+__device__ void fb_tile(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tile_t, int tile_c) {
+  using S = FbTile<SW, WT>;
+  constexpr bool GATED = fb_gated(EPI), EXACT = EPI == FB_F32;
+  constexpr int NX = S::BT / S::WAVES / 8, NW = S::BC / S::WAVES / 8;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wc = w & 1, wt = w >> 1;
+  const int64_t t0 = (int64_t)tile_t * S::BT;
+  const int rows = (int)min((int64_t)S::BT, a.T - t0);
+  const int half = a.out / 2;
+  const int c0 = tile_c * (GATED ? S::BC / 2 : S::BC);  // first channel (gated: of either half)
+  const int width = GATED ? half : a.out;
+
+  // weight row k of the tile: channel and validity
+  auto channel = [&](int k) {
+    if (!GATED) return c0 + k;
+    return k < S::BC / 2 ? c0 + k : half + c0 + k - S::BC / 2;
+  };
+  auto valid = [&](int k) { return c0 + (GATED && k >= S::BC / 2 ? k - S::BC / 2 : k) < width; };
+
+  const GemmRsrc rw = gemm_rsrc(a.w, (uint32_t)a.out * (uint32_t)a.in);
+  const GemmRsrc rws = gemm_rsrc(a.ws, (uint32_t)(((a.out + 127) / 128) * a.nb) * 4u);
+  const GemmRsrc rx = gemm_rsrc(a.x + t0 * a.in, (uint32_t)rows * (uint32_t)a.in);
+  const GemmRsrc rxs = gemm_rsrc(a.xs + t0 * a.nb, (uint32_t)(rows * a.nb) * 4u);
+  // an instruction fills 8 rows: lane l writes position l % 8 of row l / 8
+  const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
+  uint32_t wo[NW], xo[NX];
+#pragma unroll
+  for (int j = 0; j < NW; ++j) {
+    const int k = 8 * (NW * w + j) + (lane >> 3);
+    wo[j] = valid(k) ? (uint32_t)channel(k) * (uint32_t)a.in + chunk : FB_OOB;
+  }
+#pragma unroll
+  for (int j = 0; j < NX; ++j) {
+    const int k = 8 * (NX * w + j) + (lane >> 3);
+    xo[j] = k < rows ? (uint32_t)k * (uint32_t)a.in + chunk : FB_OOB;
+  }
+  const uint32_t xso = 64 * w + lane < rows ? (uint32_t)((64 * w + lane) * a.nb) * 4u : FB_OOB;
+  // the wave's strip s is tile rows strip_row(s) ..; lane s loads its scale
+  auto strip_row = [&](int s) {
+    if (!GATED) return 16 * (SW * wc + s);
+    return (s < SW / 2 ? 0 : S::BC / 2) + 16 * (SW / 2 * wc + s % (SW / 2));
+  };
+  const uint32_t wso = valid(strip_row(lane % SW))
+                           ? (uint32_t)(channel(strip_row(lane % SW)) / 128 * a.nb) * 4u : FB_OOB;
+
+  float sw_next;
+  auto load = [&](int kb) {
+    const int st = kb & 1;
+    const bool in = 128 * kb + chunk < a.in;  // chunks past the row's end are zeros
+    sw_next = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, wso, 4u * kb, 0));
+#pragma unroll
+    for (int j = 0; j < NW; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][1024 * (NW * w + j)]), 16,
+                                               in ? wo[j] : FB_OOB, 128u * kb, 0, 0);
+#pragma unroll
+    for (int j = 0; j < NX; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(&sh.x[st][1024 * (NX * w + j)]), 16,
+                                               in ? xo[j] : FB_OOB, 128u * kb, 0, 0);
+    if (w < WT)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&sh.sx[st][64 * w]), 4, xso, 4u * kb,
+                                               0, 0);
+  };
+
+  f32x4 acc[SW][4];
+#pragma unroll
+  for (int s = 0; s < SW; ++s)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  const int at0 = 128 * r + 16 * (q ^ (r & 7)), at1 = 128 * r + 16 * ((4 + q) ^ (r & 7));
+
+  load(0);
+  for (int kb = 0; kb < a.nb; ++kb) {
+    wait_vmcnt<0>();  // this wave's part of block kb is in LDS
+    const float sw = sw_next;
+    bare_barrier();   // everyone's is, and nobody reads the other stage any more
+    if (kb + 1 < a.nb) load(kb + 1);
+    const uint8_t* xl = sh.x[kb & 1] + 128 * 64 * wt;
+    const uint8_t* wl = sh.w[kb & 1];
+    u32x4 b[4][2];
+    float sx[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      b[t][0] = *reinterpret_cast<const u32x4*>(xl + 2048 * t + at0);
+      b[t][1] = *reinterpret_cast<const u32x4*>(xl + 2048 * t + at1);
+      sx[t] = sh.sx[kb & 1][64 * wt + 16 * t + r];
+    }
+#pragma unroll
+    for (int s = 0; s < SW; ++s) {
+      const u32x4 a0 = *reinterpret_cast<const u32x4*>(wl + 128 * strip_row(s) + at0);
+      const u32x4 a1 = *reinterpret_cast<const u32x4*>(wl + 128 * strip_row(s) + at1);
+      const float ss = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw), s));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f32x4 p = fb_block_product<EXACT>(a0, a1, b[t][0], b[t][1]);
+        const float m = sx[t] * ss;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[s][t][i] = __builtin_fmaf(p[i], m, acc[s][t][i]);
+      }
+    }
+  }
+  wait_vmcnt<0>();
+
+  constexpr int NO = GATED ? SW / 2 : SW;
+#pragma unroll
+  for (int s = 0; s < NO; ++s) {
+    const int o = c0 + strip_row(s) + 4 * q;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int row = 64 * wt + 16 * t + r;
+      if (row < rows && o < width) fb_store<EPI>(a, t0 + row, o, acc[s][t], acc[s + SW - NO][t]);
+    }
+  }
+}
+
+template <int EPI, int SW, int WT>
+__global__ __launch_bounds__(128 * WT) void fp8b128_tile_kernel(Fp8b128GemmArgs a, int tt, int tc) {
+  __shared__ FbTile<SW, WT> sh;
+  int t, c;
+  if (fb_tile_of(tt, tc, &t, &c)) fb_tile<EPI, SW, WT>(a, sh, t, c);
+}
+
+template <int EPI, int SW, int WT>
+hipError_t launch_tiles(const Fp8b128GemmArgs& a, hipStream_t s) {
+  using S = FbTile<SW, WT>;
+  const int width = fb_gated(EPI) ? a.out / 2 : a.out, bc = fb_gated(EPI) ? S::BC / 2 : S::BC;
+  const int tt = (int)((a.T + S::BT - 1) / S::BT), tc = (width + bc - 1) / bc;
+  return launch_timed(fp8b128_tile_kernel<EPI, SW, WT>, dim3((unsigned)((tt * tc + 7) & ~7)),
+                      dim3(S::THREADS), s, a, tt, tc);
+}
+
+template <int EPI>
+hipError_t launch_forward(const Fp8b128GemmArgs& a, hipStream_t s) {
+  // By the number of 256 x 256 tiles: from half the compute units on they are the fastest
+  // (8,192 x 5,120 x 7,168: 359 us, against 439 us with 128 x 128); below it smaller tiles
+  // spread the work wider (1,024 x 5,120 x 5,120, 80 tiles: 61 against 80 us; 512 x 5,120 x
+  // 1,536: 46 against 79 us), and up to 256 tokens strips wider still (128 x 5,120 x 1,536: 23
+  // against 46 us).
+  const int64_t big = (a.T + 255) / 256 * ((a.out + 255) / 256);
+  if (big >= 128) return launch_tiles<EPI, EPI == FB_F32 ? 4 : 8, 4>(a, s);
+  if (a.T > 256) return launch_tiles<EPI, 4, 2>(a, s);
+  return launch_strips<EPI>(a, s);
+}
+
 }  // namespace
 
 hipError_t launch_fp8b128_gemm(const Fp8b128GemmArgs& a, int epi, hipStream_t s) {
   switch (epi) {
-    case FB_F32: return launch_strips<FB_F32>(a, s);
-    case FB_BF16: return launch_strips<FB_BF16>(a, s);
-    case FB_GATED: return launch_strips<FB_GATED>(a, s);
-    default: return launch_strips<FB_GATED_GRAD>(a, s);
+    case FB_F32: return launch_forward<FB_F32>(a, s);
+    case FB_BF16: return launch_forward<FB_BF16>(a, s);
+    case FB_GATED: return launch_forward<FB_GATED>(a, s);
+    default: return launch_forward<FB_GATED_GRAD>(a, s);
   }
 }
 
