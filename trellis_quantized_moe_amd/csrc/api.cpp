@@ -1336,15 +1336,30 @@ int timed_forward(const tq::Fp8b128GemmArgs& a, int epi, hipStream_t s, const ch
   return ok();
 }
 
+// The workspace of the backward calls: the gradients of gate and up (bf16 [T][out], the gated
+// call only) and X as bf16 [T][in] (dw).
+struct Fp8b128Ws {
+  size_t dgu, xw, total;
+};
+
+Fp8b128Ws fp8b128_ws(int64_t T, int out, int in) {
+  Fp8b128Ws w{};
+  w.dgu = 0;
+  w.xw = round_up((size_t)T * out * 2, 256);
+  w.total = w.xw + round_up((size_t)T * in * 2, 256);
+  return w;
+}
+
 // dx and dw of y = X W^T from bf16 dy; either may be NULL.
 int backward_products(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs, int64_t T,
-                      const uint16_t* dy, void* dx, void* dw, hipStream_t s) {
+                      const uint16_t* dy, void* dx, void* dw, void* ws, hipStream_t s) {
   tq::Fp8b128BackwardArgs a{};
   a.w = L->codes;
   a.ws = L->scales;
   a.x = xq;
   a.xs = xs;
   a.dy = dy;
+  a.xw = at<uint16_t>(ws, fp8b128_ws(T, L->out, L->in).xw);
   a.dx = static_cast<uint16_t*>(dx);
   a.dw = static_cast<uint16_t*>(dw);
   a.T = T;
@@ -1432,7 +1447,7 @@ int fp8b128_gated(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const floa
 
 size_t tq_fp8b128_workspace_bytes(int64_t T, int32_t out, int32_t in) {
   if (T < 0 || out < 16 || in < 16) return 0;
-  return round_up((size_t)T * out * 2, 256);  // the gradients of gate and up
+  return fp8b128_ws(T, out, in).total;
 }
 
 int fp8b128_gemm_backward(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs, int64_t T,
@@ -1452,7 +1467,7 @@ int fp8b128_gemm_backward(const tq_fp8b128_layer* L, const uint8_t* xq, const fl
   if (rc) return rc;
   rc = check_device();
   if (rc) return rc;
-  return backward_products(L, xq, xs, T, static_cast<const uint16_t*>(dy), dx, dw, s);
+  return backward_products(L, xq, xs, T, static_cast<const uint16_t*>(dy), dx, dw, ws, s);
 }
 
 int fp8b128_gated_backward(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const float* xs,
@@ -1474,12 +1489,12 @@ int fp8b128_gated_backward(const tq_fp8b128_layer* gate_up, const uint8_t* xq, c
   if (rc) return rc;
   rc = check_device();
   if (rc) return rc;
-  uint16_t* dgu = at<uint16_t>(ws, 0);
+  uint16_t* dgu = at<uint16_t>(ws, fp8b128_ws(T, gate_up->out, gate_up->in).dgu);
   tq::Fp8b128GemmArgs a = forward_args(gate_up, xq, xs, T, dgu);
   a.dh = static_cast<const uint16_t*>(dh);
   hipError_t err = tq::launch_fp8b128_gemm(a, tq::FB_GATED_GRAD, s);
   if (err != hipSuccess) return hip_fail(err, "fp8b128 gate and up gradient launch");
-  return backward_products(gate_up, xq, xs, T, dgu, dx, dw, s);
+  return backward_products(gate_up, xq, xs, T, dgu, dx, dw, ws, s);
 }
 
 namespace {

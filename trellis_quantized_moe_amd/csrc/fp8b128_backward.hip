@@ -1,6 +1,11 @@
 // The gradients of a product over the fp8b128 store (FORMAT F26), on the bf16 matrix cores:
 //   dx[t][i] = sum over o of dy[t][o] * W[o][i],    W = scale of the block * code
 //   dw[o][i] = sum over t of dy[t][o] * X[t][i],    X = scale of the token's block * code
+// Both contract over the rows of a row-major operand, so a lane's eight operand values lie in
+// eight (bf16: twice four) rows: the LDS transpose reads fetch them. ds_read_b64_tr_b8: of each
+// 16 lanes, lanes 2k and 2k + 1 address the two halves of 16 bytes of row k (k = 0..7), and
+// lane j gets byte j of the eight rows. ds_read_b64_tr_b16: lanes 4k .. 4k + 3 address the
+// quarters of 32 bytes of row k (k = 0..3), and lane j gets half-word j of the four rows.
 // Inputs are the A operand, so a lane ends with four consecutive inputs of a token or channel.
 #include "fp8b128.h"
 
@@ -8,79 +13,414 @@ namespace tq {
 
 namespace {
 
-__device__ __forceinline__ u32x4 pack8(const uint16_t v[8]) {
-  return (u32x4){(uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16,
-                 (uint32_t)v[4] | (uint32_t)v[5] << 16, (uint32_t)v[6] | (uint32_t)v[7] << 16};
+typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i32x2* LdsI32x2;
+typedef __attribute__((address_space(3))) s16x4* LdsS16x4;
+
+__device__ __forceinline__ u32x2 read_tr8(const uint8_t* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((LdsI32x2)(p)));
+}
+__device__ __forceinline__ u32x2 read_tr16(const uint8_t* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4)(p)));
 }
 
-// One 16 x 16 tile per wave; the sums over each 128 outputs are scaled by their block's scale.
-__global__ __launch_bounds__(256) void fp8b128_dx_kernel(Fp8b128BackwardArgs a) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int cols = a.in / 16;
-  const int64_t t = tile / cols * 16 + r;
-  const int i0 = (int)(tile % cols) * 16;
-  if (tile / cols * 16 >= a.T) return;
-  f32x4 acc = (f32x4){0.f, 0.f, 0.f, 0.f};
-  for (int ob = 0; ob * 128 < a.out; ++ob) {
-    f32x4 p = (f32x4){0.f, 0.f, 0.f, 0.f};
-    for (int o0 = ob * 128; o0 < min(ob * 128 + 128, a.out); o0 += 32) {
-      const int o = o0 + 8 * q;
-      uint32_t c[2] = {0, 0};
-      u32x4 b = (u32x4){0, 0, 0, 0};
-      if (o < a.out) {
-        for (int j = 0; j < 8; ++j)
-          c[j / 4] |= (uint32_t)a.w[(int64_t)(o + j) * a.in + i0 + r] << (8 * (j % 4));
-        if (t < a.T) b = *reinterpret_cast<const u32x4*>(a.dy + t * a.out + o);
-      }
-      p = mfma_bf16(fb_bf16_of8(c[0], c[1]), b, p);
-    }
-    const float s = a.ws[(int64_t)ob * a.nb + i0 / 128];
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(p[i], s, acc[i]);
-  }
-  if (t < a.T)
-    *reinterpret_cast<u32x2*>(a.dx + t * a.in + i0 + 4 * q) =
-        (u32x2){fb_pack_bf16(acc[0], acc[1]), fb_pack_bf16(acc[2], acc[3])};
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+  *reinterpret_cast<u32x2*>(p) = (u32x2){fb_pack_bf16(v[0], v[1]), fb_pack_bf16(v[2], v[3])};
 }
 
-// One 16 x 16 tile per wave. X is rounded to bf16 (exact for scales that are powers of two,
-// which fp8b128_quantize writes).
-__global__ __launch_bounds__(256) void fp8b128_dw_kernel(Fp8b128BackwardArgs a) {
+// ---- dx, few tokens: 32 inputs of up to 16 * TT tokens per workgroup ------------------------
+//
+// The eight waves take the blocks of 128 outputs in turn, each with LDS of its own (no barrier
+// until the end), one block ahead: the block's 128 x 32 codes straight to LDS, the tokens' dy
+// to registers in operand order. A block's sums are scaled by its weight scale; the waves'
+// sums are added in wave order.
+constexpr int DS_WAVES = 8;
+constexpr int DS_THREADS = 64 * DS_WAVES;
+
+template <int TT>
+struct DxStripShared {
+  alignas(16) uint8_t w[DS_WAVES][2][128 * 32];
+  f32x4 red[DS_WAVES][TT * 2][64];
+};
+
+template <int TT>
+__device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStripShared<TT>& sh) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int cols = a.in / 16;
-  const int o = (int)(tile / cols) * 16 + r;
-  const int i0 = (int)(tile % cols) * 16;
-  if (tile / cols * 16 >= a.out) return;
-  f32x4 acc = (f32x4){0.f, 0.f, 0.f, 0.f};
-  for (int64_t t0 = 0; t0 < a.T; t0 += 32) {
-    uint16_t x[8], d[8];
-    for (int j = 0; j < 8; ++j) {
-      const int64_t t = t0 + 8 * q + j;
-      x[j] = d[j] = 0;
-      if (t < a.T) {
-        const uint32_t c = a.x[t * a.in + i0 + r];
-        const float v = bf16_lo_to_f32(fb_bf16_of4(c).x) * a.xs[t * a.nb + i0 / 128];
-        x[j] = (uint16_t)fb_pack_bf16(v, 0.0f);
-        d[j] = a.dy[t * a.out + o];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cols = (a.in + 31) / 32;
+  const int i0 = (int)(blockIdx.x % cols) * 32;
+  const int64_t t0 = (int64_t)(blockIdx.x / cols) * (16 * TT);
+  const int rows = (int)min((int64_t)(16 * TT), a.T - t0);
+  const int nob = (a.out + 127) / 128;
+
+  const GemmRsrc rd = gemm_rsrc(a.dy + t0 * a.out, (uint32_t)rows * (uint32_t)a.out * 2u);
+  const GemmRsrc rs = gemm_rsrc(a.ws, (uint32_t)(nob * a.nb) * 4u);
+  // codes: instruction j fills rows 32 j .. + 31; lane l half l % 2 of row l / 2, which holds
+  // the row's half (l % 2) ^ (row / 4 % 2), so that a transpose read's eight rows meet
+  // different banks
+  const int wrow = lane >> 1, wcol = 16 * ((lane & 1) ^ ((wrow >> 2) & 1));
+  const uint32_t wo = i0 + wcol < a.in ? (uint32_t)wrow * (uint32_t)a.in + i0 + wcol : FB_OOB;
+  uint32_t dof[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+    dof[t] = 16 * t + r < rows ? (uint32_t)(16 * t + r) * (uint32_t)a.out * 2u + 16u * q : FB_OOB;
+
+  constexpr int LOADS = 5 + 4 * TT;
+  u32x4 d[2][TT][4];
+  float sc[2];
+  auto load = [&](int k, int ob) {  // blocks past the last are read as zeros
+    const int left = min(128, a.out - 128 * ob);
+    const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 128 * ob : 0) * a.in,
+                                  left > 0 ? (uint32_t)left * (uint32_t)a.in : 0u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[w][k][1024 * j]), 16,
+                                               wo == FB_OOB ? FB_OOB : wo + 32u * j * (uint32_t)a.in,
+                                               0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = 128 * ob + 32 * j + 8 * q < a.out && dof[t] != FB_OOB;
+        d[k][t][j] = __builtin_amdgcn_raw_buffer_load_b128(rd, in ? dof[t] + 256u * ob + 64u * j : FB_OOB, 0, 0);
+      }
+    sc[k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        rs, ob < nob ? (uint32_t)(ob * a.nb + i0 / 128) * 4u : FB_OOB, 0, 0));
+  };
+  f32x4 acc[TT][2];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) acc[t][0] = acc[t][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  // lane (j = l % 16, q) of a transpose read: row 8 q + j / 2, half j % 2 of 16-byte column c
+  auto compute = [&](int k) {
+    f32x4 p[TT][2];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) p[t][0] = p[t][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = 32 * j + 8 * q + (r >> 1);
+        const u32x2 v = read_tr8(&sh.w[w][k][32 * row + 16 * (c ^ ((row >> 2) & 1)) + 8 * (r & 1)]);
+        const u32x4 av = fb_bf16_of8(v.x, v.y);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) p[t][c] = mfma_bf16(av, d[k][t][j], p[t][c]);
+      }
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][c][i] = __builtin_fmaf(p[t][c][i], sc[k], acc[t][c][i]);
+  };
+  // one step: the next block's loads, then this block's data (all but those loads have landed)
+  auto step = [&](int k, int ob) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the stage is outstanding
+    __builtin_amdgcn_sched_barrier(0);
+    load(k ^ 1, ob + DS_WAVES);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<LOADS>();
+    __builtin_amdgcn_sched_barrier(0);
+    compute(k);
+  };
+  load(0, w);
+  for (int ob = w; ob < nob; ob += 2 * DS_WAVES) {
+    step(0, ob);
+    if (ob + DS_WAVES < nob) step(1, ob + DS_WAVES);
+  }
+  wait_vmcnt<0>();  // no load may still be writing this workgroup's LDS when it ends
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) sh.red[w][2 * t + c][lane] = acc[t][c];
+  __syncthreads();
+  const int v = threadIdx.x >> 6;  // wave v finishes tile v
+  if (v < 2 * TT) {
+    f32x4 sum = sh.red[0][v][lane];
+#pragma unroll
+    for (int u = 1; u < DS_WAVES; ++u) sum += sh.red[u][v][lane];
+    const int row = 16 * (v >> 1) + r, i = i0 + 16 * (v & 1) + 4 * q;
+    if (row < rows && i < a.in) store4(a.dx + (t0 + row) * a.in + i, sum);
+  }
+}
+
+template <int TT>
+__global__ __launch_bounds__(DS_THREADS) void fp8b128_dx_strip_kernel(Fp8b128BackwardArgs a) {
+  __shared__ DxStripShared<TT> sh;
+  dx_strip<TT>(a, sh);
+}
+
+// ---- dx, many tokens ------------------------------------------------------------------------
+//
+// A workgroup of eight waves owns 256 inputs of 128 tokens, wave (wi, wt) 64 inputs of 64
+// tokens. Steps of 64 outputs: 64 rows of 256 code bytes and 128 rows of 128 bytes of dy go
+// straight to a ring of four LDS stages, two steps ahead. The products of two steps (one block
+// of 128 outputs) are added from zero and then scaled into the sums.
+struct DxShared {
+  alignas(16) uint8_t w[4][64 * 256];
+  alignas(16) uint8_t d[4][128 * 128];
+};
+
+__device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, int tile_i) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = w & 3, wt = w >> 2;
+  const int64_t t0 = (int64_t)tile_t * 128;
+  const int rows = (int)min((int64_t)128, a.T - t0);
+  const int i0 = tile_i * 256;
+  const int nsteps = (a.out + 63) / 64;
+
+  const GemmRsrc rd = gemm_rsrc(a.dy + t0 * a.out, (uint32_t)rows * (uint32_t)a.out * 2u);
+  const GemmRsrc rs = gemm_rsrc(a.ws, (uint32_t)((a.out + 127) / 128 * a.nb) * 4u);
+  // codes: an instruction fills 4 rows; lane l position l % 16 of row l / 16, which holds the
+  // row's 16-byte chunk (l % 16) ^ (row % 16). dy: 8 rows; position l % 8 of row l / 8 holds
+  // chunk (l % 8) ^ (row % 8).
+  uint32_t wo[2], dof[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = 8 * w + 4 * j + (lane >> 4), col = i0 + 16 * ((lane & 15) ^ (row & 15));
+    wo[j] = col < a.in ? (uint32_t)row * (uint32_t)a.in + col : FB_OOB;
+    const int tok = 16 * w + 8 * j + (lane >> 3);
+    dof[j] = tok < rows ? (uint32_t)tok * (uint32_t)a.out * 2u + 16u * ((lane & 7) ^ (lane >> 3)) : FB_OOB;
+  }
+  const int dcol = 8 * ((lane & 7) ^ (lane >> 3));  // this lane's first output of a step
+  const int ib = min((i0 + 64 * wi) / 128, a.nb - 1);
+  constexpr int LOADS = 5;
+  float sc[4];
+  auto load = [&](int st, int k) {  // steps past the last are read as zeros
+    const int left = min(64, a.out - 64 * k);
+    const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 64 * k : 0) * a.in,
+                                  left > 0 ? (uint32_t)left * (uint32_t)a.in : 0u);
+    const bool in = dcol < left;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][256 * (8 * w + 4 * j)]), 16,
+                                               wo[j], 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][128 * (16 * w + 8 * j)]), 16,
+                                               in ? dof[j] : FB_OOB, 128u * k, 0, 0);
+    sc[st] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        rs, 64 * (k & ~1) < a.out ? (uint32_t)(k / 2 * a.nb + ib) * 4u : FB_OOB, 0, 0));
+  };
+
+  f32x4 acc[4][4], p[4][4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[c][t] = p[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  load(0, 0);
+  load(1, 1);
+  auto step = [&](int st, int k) {
+    wait_vmcnt<LOADS>();  // this wave's part of step k has landed, step k + 1's may be in flight
+    bare_barrier();
+    load((st + 2) & 3, k + 2);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x4 b[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        b[t] = *reinterpret_cast<const u32x4*>(
+            &sh.d[st][128 * (64 * wt + 16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int row = 32 * j + 8 * q + (r >> 1);
+        const u32x2 v = read_tr8(&sh.w[st][256 * row + 16 * ((4 * wi + c) ^ (row & 15)) + 8 * (r & 1)]);
+        const u32x4 av = fb_bf16_of8(v.x, v.y);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) p[c][t] = mfma_bf16(av, b[t], p[c][t]);
       }
     }
-    acc = mfma_bf16(pack8(x), pack8(d), acc);
+    if (st & 1) {  // the block of 128 outputs is complete
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[c][t][i] = __builtin_fmaf(p[c][t][i], sc[st], acc[c][t][i]);
+          p[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        }
+    }
+  };
+  // whole blocks (a step past the last adds zeros)
+  for (int k = 0; k < nsteps; k += 4) {
+    step(0, k);
+    step(1, k + 1);
+    if (k + 2 < nsteps) {
+      step(2, k + 2);
+      step(3, k + 3);
+    }
   }
-  *reinterpret_cast<u32x2*>(a.dw + (int64_t)o * a.in + i0 + 4 * q) =
-      (u32x2){fb_pack_bf16(acc[0], acc[1]), fb_pack_bf16(acc[2], acc[3])};
+  wait_vmcnt<0>();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int i = i0 + 64 * wi + 16 * c + 4 * q;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int row = 64 * wt + 16 * t + r;
+      if (row < rows && i < a.in) store4(a.dx + (t0 + row) * a.in + i, acc[c][t]);
+    }
+  }
+}
+
+__global__ __launch_bounds__(512) void fp8b128_dx_kernel(Fp8b128BackwardArgs a, int tt, int ti) {
+  __shared__ DxShared sh;
+  int t, i;
+  if (fb_tile_of(tt, ti, &t, &i)) dx_tile(a, sh, t, i);
+}
+
+// ---- dw -------------------------------------------------------------------------------------
+//
+// X as bf16 [T][in] (exact for scales that are powers of two), once per call: every channel
+// tile of the product reads it.
+__global__ __launch_bounds__(256) void fp8b128_widen_kernel(const uint8_t* __restrict__ x,
+                                                            const float* __restrict__ xs, int64_t n16,
+                                                            int in, int nb, u32x4* __restrict__ y) {
+  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 16 inputs of a row
+  if (k >= n16) return;
+  const int per = in / 16;
+  const int64_t t = k / per;
+  const float s = xs[t * nb + (int)(k % per) / 8];
+  const u32x4 c = *reinterpret_cast<const u32x4*>(x + 16 * k);
+  u32x4 out[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const u32x2 v = fb_bf16_of4(c[j]);
+    out[j / 2][j % 2 * 2] = fb_pack_bf16(bf16_lo_to_f32(v.x) * s, bf16_hi_to_f32(v.x) * s);
+    out[j / 2][j % 2 * 2 + 1] = fb_pack_bf16(bf16_lo_to_f32(v.y) * s, bf16_hi_to_f32(v.y) * s);
+  }
+  y[2 * k] = out[0];
+  y[2 * k + 1] = out[1];
+}
+
+// A workgroup of eight waves owns 256 inputs of 128 channels, wave (wi, wo) 64 inputs of 64
+// channels; steps of 64 tokens through a ring of three LDS stages, two steps ahead. A row's
+// 32-byte chunk c lies at position c ^ (row % 16) (dy: row % 8), so that the four rows of a
+// transpose read meet different banks.
+struct DwShared {
+  alignas(16) uint8_t x[3][64 * 512];
+  alignas(16) uint8_t d[3][64 * 256];
+};
+
+__device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, int tile_i) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = w & 3, wo = w >> 2;
+  const int i0 = tile_i * 256, o0 = tile_o * 128;
+  const int nsteps = (int)((a.T + 63) / 64);
+  uint32_t xo[4], dof[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // two rows of 512 bytes per instruction
+    const int row = 8 * w + 2 * j + (lane >> 5), pos = lane & 31;
+    const int i = i0 + 16 * ((pos >> 1) ^ (row & 15)) + 8 * (pos & 1);
+    xo[j] = i < a.in ? ((uint32_t)row * (uint32_t)a.in + i) * 2u : FB_OOB;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {  // four rows of 256 bytes
+    const int row = 8 * w + 4 * j + (lane >> 4), pos = lane & 15;
+    const int o = o0 + 16 * ((pos >> 1) ^ (row & 7)) + 8 * (pos & 1);
+    dof[j] = o < a.out ? ((uint32_t)row * (uint32_t)a.out + o) * 2u : FB_OOB;
+  }
+  constexpr int LOADS = 6;
+  auto load = [&](int st, int k) {  // rows past the last token are read as zeros
+    const int64_t t = (int64_t)64 * k;
+    const int left = (int)min((int64_t)64, a.T - t);
+    const int64_t at = left > 0 ? t : 0;
+    const GemmRsrc rx = gemm_rsrc(a.xw + at * a.in, left > 0 ? (uint32_t)left * (uint32_t)a.in * 2u : 0u);
+    const GemmRsrc rd = gemm_rsrc(a.dy + at * a.out, left > 0 ? (uint32_t)left * (uint32_t)a.out * 2u : 0u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(&sh.x[st][512 * (8 * w + 2 * j)]), 16,
+                                               xo[j], 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][256 * (8 * w + 4 * j)]), 16,
+                                               dof[j], 0, 0, 0);
+  };
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  load(0, 0);
+  load(1, 1);
+  auto step = [&](int st, int k) {
+    wait_vmcnt<LOADS>();
+    bare_barrier();
+    load((st + 2) % 3, k + 2);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      // lane (r, q) of half h: row 32 j + 8 q + 4 h + r / 4, quarter r % 4 of a 32-byte chunk
+      const int row = 32 * j + 8 * q + (r >> 2);
+      u32x4 b[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int ch = 4 * wo + c;
+        const u32x2 lo = read_tr16(&sh.d[st][256 * row + 32 * (ch ^ (row & 7)) + 8 * (r & 3)]);
+        const u32x2 hi = read_tr16(&sh.d[st][256 * (row + 4) + 32 * (ch ^ ((row + 4) & 7)) + 8 * (r & 3)]);
+        b[c] = (u32x4){lo.x, lo.y, hi.x, hi.y};
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int ch = 4 * wi + c;
+        const u32x2 lo = read_tr16(&sh.x[st][512 * row + 32 * (ch ^ (row & 15)) + 8 * (r & 3)]);
+        const u32x2 hi = read_tr16(&sh.x[st][512 * (row + 4) + 32 * (ch ^ ((row + 4) & 15)) + 8 * (r & 3)]);
+        const u32x4 av = (u32x4){lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[c][t] = mfma_bf16(av, b[t], acc[c][t]);
+      }
+    }
+  };
+  for (int k = 0; k < nsteps; k += 3) {
+    step(0, k);
+    if (k + 1 < nsteps) step(1, k + 1);
+    if (k + 2 < nsteps) step(2, k + 2);
+  }
+  wait_vmcnt<0>();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int i = i0 + 64 * wi + 16 * c + 4 * q;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int o = o0 + 64 * wo + 16 * t + r;
+      if (o < a.out && i < a.in) store4(a.dw + (int64_t)o * a.in + i, acc[c][t]);
+    }
+  }
+}
+
+__global__ __launch_bounds__(512) void fp8b128_dw_kernel(Fp8b128BackwardArgs a, int to, int ti) {
+  __shared__ DwShared sh;
+  int o, i;
+  if (fb_tile_of(to, ti, &o, &i)) dw_tile(a, sh, o, i);
 }
 
 }  // namespace
 
 hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s) {
-  const int64_t tiles = (a.T + 15) / 16 * (a.in / 16);
-  return launch_timed(fp8b128_dx_kernel, dim3((unsigned)((tiles + 3) / 4)), dim3(256), s, a);
+  // strips spread few tokens wider; tiles move less data once they fill half the GPU
+  const int64_t tiles = (a.T + 127) / 128 * ((a.in + 255) / 256);
+  if (tiles >= 128) {
+    const int tt = (int)((a.T + 127) / 128), ti = (a.in + 255) / 256;
+    hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)((tt * ti + 7) & ~7)), dim3(512), 0, s, a, tt, ti);
+    return hipGetLastError();
+  }
+  const int tt = a.T <= 16 ? 1 : 2;
+  const unsigned grid = (unsigned)((a.in + 31) / 32 * ((a.T + 16 * tt - 1) / (16 * tt)));
+  if (tt == 1)
+    hipLaunchKernelGGL(fp8b128_dx_strip_kernel<1>, dim3(grid), dim3(DS_THREADS), 0, s, a);
+  else
+    hipLaunchKernelGGL(fp8b128_dx_strip_kernel<2>, dim3(grid), dim3(DS_THREADS), 0, s, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& a, hipStream_t s) {
-  const int64_t tiles = (int64_t)(a.out / 16) * (a.in / 16);
-  hipLaunchKernelGGL(fp8b128_dw_kernel, dim3((unsigned)((tiles + 3) / 4)), dim3(256), 0, s, a);
+  const int64_t n16 = a.T * (a.in / 16);
+  hipLaunchKernelGGL(fp8b128_widen_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, s, a.x,
+                     a.xs, n16, a.in, a.nb, reinterpret_cast<u32x4*>(a.xw));
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int to = (a.out + 127) / 128, ti = (a.in + 255) / 256;
+  hipLaunchKernelGGL(fp8b128_dw_kernel, dim3((unsigned)((to * ti + 7) & ~7)), dim3(512), 0, s, a, to, ti);
   return hipGetLastError();
 }
 

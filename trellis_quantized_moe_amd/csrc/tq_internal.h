@@ -327,6 +327,7 @@ struct Fp8b128BackwardArgs {
   const uint8_t* x;
   const float* xs;
   const uint16_t* dy;  // bf16 [T][out]
+  uint16_t* xw;        // workspace of dw: X as bf16 [T][in]
   uint16_t* dx;        // bf16 [T][in]
   uint16_t* dw;        // bf16 [out][in]
   int64_t T;
