@@ -26,11 +26,11 @@ FP8_SUM = 2.0 ** -12
 # tile and a 16-byte chunk pair; fewer blocks than waves, and more
 FORWARD = [(1, 16, 16), (1, 1536, 5120), (2, 48, 112), (5, 160, 128), (16, 32, 144), (17, 128, 256),
            (33, 272, 400), (64, 144, 1040), (65, 96, 2064), (100, 64, 1168), (129, 256, 128),
-           (200, 400, 272), (257, 528, 640), (300, 1040, 96), (513, 288, 1296), (1030, 784, 528)]
+           (200, 400, 272), (257, 528, 640), (300, 1040, 96), (513, 288, 1296), (1030, 784, 528), (3000, 2832, 144)]
 GATED = [(1, 32, 16), (1, 1536, 5120), (3, 96, 144), (16, 288, 272), (31, 64, 400), (64, 1440, 528),
-         (130, 160, 1040), (257, 544, 256), (300, 800, 400), (700, 1056, 272)]
+         (130, 160, 1040), (257, 544, 256), (300, 800, 400), (700, 1056, 272), (2900, 2848, 272)]
 BACKWARD = [(1, 32, 16), (1, 288, 400), (2, 64, 128), (17, 32, 272), (40, 288, 144), (64, 96, 1040),
-            (129, 256, 256), (200, 544, 400), (257, 160, 656), (333, 1056, 272), (600, 288, 784)]
+            (129, 256, 256), (200, 544, 400), (257, 160, 656), (333, 1056, 272), (600, 288, 784), (2100, 352, 2064)]
 
 
 def bits_of(t):

@@ -18,10 +18,13 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i32x2* LdsI32x2;
 typedef __attribute__((address_space(3))) s16x4* LdsS16x4;
 
-__device__ __forceinline__ u32x2 read_tr8(const uint8_t* p) {
+// The pointers are __restrict__ for the compiler's wait insertion: it makes an LDS read that it
+// knows nothing about wait for every load in flight that writes LDS, the ones meant to stay in
+// flight across the read included; the kernels' own waits and barriers order the two.
+__device__ __forceinline__ u32x2 read_tr8(const uint8_t* __restrict__ p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((LdsI32x2)(p)));
 }
-__device__ __forceinline__ u32x2 read_tr16(const uint8_t* p) {
+__device__ __forceinline__ u32x2 read_tr16(const uint8_t* __restrict__ p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4)(p)));
 }
 
@@ -154,7 +157,7 @@ __global__ __launch_bounds__(DS_THREADS) void fp8b128_dx_strip_kernel(Fp8b128Bac
 //
 // A workgroup of eight waves owns 256 inputs of 128 tokens, wave (wi, wt) 64 inputs of 64
 // tokens. Steps of 64 outputs: 64 rows of 256 code bytes and 128 rows of 128 bytes of dy go
-// straight to a ring of four LDS stages, two steps ahead. The products of two steps (one block
+// straight to a ring of four LDS stages, three steps ahead. The products of two steps (one block
 // of 128 outputs) are added from zero and then scaled into the sums.
 struct DxShared {
   alignas(16) uint8_t w[4][64 * 256];
@@ -208,38 +211,55 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) acc[c][t] = p[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  load(0, 0);
-  load(1, 1);
-  auto step = [&](int st, int k) {
-    wait_vmcnt<LOADS>();  // this wave's part of step k has landed, step k + 1's may be in flight
-    bare_barrier();
-    load((st + 2) & 3, k + 2);
+    for (int t = 0; t < 4; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  // operands of 32 outputs (half j of a step)
+  u32x2 av[2][4];
+  u32x4 bv[2][4];
+  auto read = [&](int st, int j) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      u32x4 b[4];
+    for (int t = 0; t < 4; ++t)
+      bv[j][t] = *reinterpret_cast<const u32x4*>(
+          &sh.d[st][128 * (64 * wt + 16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int row = 32 * j + 8 * q + (r >> 1);
+      av[j][c] = read_tr8(&sh.w[st][256 * row + 16 * ((4 * wi + c) ^ (row & 15)) + 8 * (r & 1)]);
+    }
+  };
+  auto multiply = [&](int j, bool first) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const u32x4 a8 = fb_bf16_of8(av[j][c].x, av[j][c].y);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        b[t] = *reinterpret_cast<const u32x4*>(
-            &sh.d[st][128 * (64 * wt + 16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int row = 32 * j + 8 * q + (r >> 1);
-        const u32x2 v = read_tr8(&sh.w[st][256 * row + 16 * ((4 * wi + c) ^ (row & 15)) + 8 * (r & 1)]);
-        const u32x4 av = fb_bf16_of8(v.x, v.y);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) p[c][t] = mfma_bf16(av, b[t], p[c][t]);
-      }
+        p[c][t] = mfma_bf16(a8, bv[j][t], first ? (f32x4){0.f, 0.f, 0.f, 0.f} : p[c][t]);
     }
+  };
+#pragma unroll
+  for (int k = 0; k < 4; ++k) load(k, k);
+  wait_vmcnt<3 * LOADS>();
+  bare_barrier();
+  read(0, 0);
+  // A step's second half is read while its first half is multiplied, and the next step's first
+  // half while its second is: between the two, the next step's data have landed everywhere,
+  // and this step's stage is no longer read.
+  auto step = [&](int st, int k) {
+    read(st, 1);
+    multiply(0, (st & 1) == 0);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<2 * LOADS>();
+    bare_barrier();
+    const float s = sc[st];
+    read((st + 1) & 3, 0);
+    load(st, k + 4);
+    multiply(1, false);
     if (st & 1) {  // the block of 128 outputs is complete
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[c][t][i] = __builtin_fmaf(p[c][t][i], sc[st], acc[c][t][i]);
-          p[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        }
+          for (int i = 0; i < 4; ++i) acc[c][t][i] = __builtin_fmaf(p[c][t][i], s, acc[c][t][i]);
     }
   };
   // whole blocks (a step past the last adds zeros)
@@ -295,8 +315,11 @@ __global__ __launch_bounds__(256) void fp8b128_widen_kernel(const uint8_t* __res
 
 // A workgroup of eight waves owns 256 inputs of 128 channels, wave (wi, wo) 64 inputs of 64
 // channels; steps of 64 tokens through a ring of three LDS stages, two steps ahead. A row's
-// 32-byte chunk c lies at position c ^ (row % 16) (dy: row % 8), so that the four rows of a
-// transpose read meet different banks.
+// 32-byte chunk c lies at position c ^ swizzle(row): the LDS serves 32 lanes at a time, which
+// read one chunk of rows 8 q + 0..3 and 8 (q + 1) + 0..3 (or + 4..7), and those eight rows get
+// eight different positions.
+__device__ __forceinline__ int dw_swizzle(int row) { return (row & 3) | (row >> 1 & 4); }
+
 struct DwShared {
   alignas(16) uint8_t x[3][64 * 512];
   alignas(16) uint8_t d[3][64 * 256];
@@ -312,13 +335,13 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
 #pragma unroll
   for (int j = 0; j < 4; ++j) {  // two rows of 512 bytes per instruction
     const int row = 8 * w + 2 * j + (lane >> 5), pos = lane & 31;
-    const int i = i0 + 16 * ((pos >> 1) ^ (row & 15)) + 8 * (pos & 1);
+    const int i = i0 + 16 * ((pos >> 1) ^ dw_swizzle(row)) + 8 * (pos & 1);
     xo[j] = i < a.in ? ((uint32_t)row * (uint32_t)a.in + i) * 2u : FB_OOB;
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {  // four rows of 256 bytes
     const int row = 8 * w + 4 * j + (lane >> 4), pos = lane & 15;
-    const int o = o0 + 16 * ((pos >> 1) ^ (row & 7)) + 8 * (pos & 1);
+    const int o = o0 + 16 * ((pos >> 1) ^ dw_swizzle(row)) + 8 * (pos & 1);
     dof[j] = o < a.out ? ((uint32_t)row * (uint32_t)a.out + o) * 2u : FB_OOB;
   }
   constexpr int LOADS = 6;
@@ -342,34 +365,44 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  load(0, 0);
-  load(1, 1);
-  auto step = [&](int st, int k) {
+  // operands of 32 tokens (half j of a step). Lane (r, q) of half h: row 32 j + 8 q + 4 h + r / 4,
+  // quarter r % 4 of a 32-byte chunk
+  u32x4 av[2][4], bv[2][4];
+  auto read = [&](int st, int j) {
+    const int row = 32 * j + 8 * q + (r >> 2), sw = dw_swizzle(row);  // the same for row + 4
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint8_t* p = &sh.d[st][256 * row + 32 * ((4 * wo + c) ^ sw) + 8 * (r & 3)];
+      const u32x2 lo = read_tr16(p), hi = read_tr16(p + 4 * 256);
+      bv[j][c] = (u32x4){lo.x, lo.y, hi.x, hi.y};
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint8_t* p = &sh.x[st][512 * row + 32 * ((4 * wi + c) ^ sw) + 8 * (r & 3)];
+      const u32x2 lo = read_tr16(p), hi = read_tr16(p + 4 * 512);
+      av[j][c] = (u32x4){lo.x, lo.y, hi.x, hi.y};
+    }
+  };
+  auto multiply = [&](int j) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[c][t] = mfma_bf16(av[j][c], bv[j][t], acc[c][t]);
+  };
+#pragma unroll
+  for (int k = 0; k < 3; ++k) load(k, k);
+  wait_vmcnt<2 * LOADS>();
+  bare_barrier();
+  read(0, 0);
+  auto step = [&](int st, int k) {  // as in dx_tile
+    read(st, 1);
+    multiply(0);
+    __builtin_amdgcn_sched_barrier(0);
     wait_vmcnt<LOADS>();
     bare_barrier();
-    load((st + 2) % 3, k + 2);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      // lane (r, q) of half h: row 32 j + 8 q + 4 h + r / 4, quarter r % 4 of a 32-byte chunk
-      const int row = 32 * j + 8 * q + (r >> 2);
-      u32x4 b[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int ch = 4 * wo + c;
-        const u32x2 lo = read_tr16(&sh.d[st][256 * row + 32 * (ch ^ (row & 7)) + 8 * (r & 3)]);
-        const u32x2 hi = read_tr16(&sh.d[st][256 * (row + 4) + 32 * (ch ^ ((row + 4) & 7)) + 8 * (r & 3)]);
-        b[c] = (u32x4){lo.x, lo.y, hi.x, hi.y};
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int ch = 4 * wi + c;
-        const u32x2 lo = read_tr16(&sh.x[st][512 * row + 32 * (ch ^ (row & 15)) + 8 * (r & 3)]);
-        const u32x2 hi = read_tr16(&sh.x[st][512 * (row + 4) + 32 * (ch ^ ((row + 4) & 15)) + 8 * (r & 3)]);
-        const u32x4 av = (u32x4){lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[c][t] = mfma_bf16(av, b[t], acc[c][t]);
-      }
-    }
+    read((st + 1) % 3, 0);
+    load(st, k + 3);
+    multiply(1);
   };
   for (int k = 0; k < nsteps; k += 3) {
     step(0, k);
