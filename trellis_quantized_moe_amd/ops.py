@@ -356,12 +356,14 @@ def _check_rows(name, t, dtypes, device=None, shape=None):
 
 def _call_on(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with that device current (a kernel
-    launched while another device is current would not run on it)."""
+    launched while another device is current would not run on it). The stream's handle is read
+    without making a Stream object: 0.1 us instead of 1.8, in calls of a few microseconds."""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
-        check(fn(*args, _stream(device)))
+        check(fn(*args, stream))
     else:
         with torch.cuda.device(device):
-            check(fn(*args, _stream(device)))
+            check(fn(*args, stream))
 
 
 def _check_ws(ws, device, nbytes):
