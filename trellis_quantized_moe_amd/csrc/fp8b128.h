@@ -41,22 +41,35 @@ __device__ __forceinline__ uint32_t fb_pack_bf16(float lo, float hi) {
 // 2-norm, unbiased, against 1e-8 with bf16), which is far below half a step of a bf16
 // result (2^-9) and is used only where the result is rounded to bf16.
 template <bool EXACT>
-__device__ __forceinline__ f32x4 fb_block_product(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1) {
-  f32x4 p = (f32x4){0.f, 0.f, 0.f, 0.f};
-  if constexpr (EXACT) {
-    p = mfma_bf16(fb_bf16_of8(a0.x, a0.y), fb_bf16_of8(b0.x, b0.y), p);
-    p = mfma_bf16(fb_bf16_of8(a0.z, a0.w), fb_bf16_of8(b0.z, b0.w), p);
-    p = mfma_bf16(fb_bf16_of8(a1.x, a1.y), fb_bf16_of8(b1.x, b1.y), p);
-    p = mfma_bf16(fb_bf16_of8(a1.z, a1.w), fb_bf16_of8(b1.z, b1.w), p);
-  } else {
-    const i32x8 a = (i32x8){(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w,
-                            (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-    const i32x8 b = (i32x8){(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w,
-                            (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
-    // scale operands of zero select the instruction without block scales
-    p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, p, 0, 0, 0, 0, 0, 0);
+struct FbOperand;  // 32 codes of a row, as the matrix cores take them
+template <>
+struct FbOperand<true> {
+  u32x4 v[4];
+  __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+    v[0] = fb_bf16_of8(lo.x, lo.y);
+    v[1] = fb_bf16_of8(lo.z, lo.w);
+    v[2] = fb_bf16_of8(hi.x, hi.y);
+    v[3] = fb_bf16_of8(hi.z, hi.w);
   }
+};
+template <>
+struct FbOperand<false> {
+  i32x8 v;
+  __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+    v = __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+
+__device__ __forceinline__ f32x4 fb_block_product(const FbOperand<true>& a, const FbOperand<true>& b) {
+  f32x4 p = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p = mfma_bf16(a.v[j], b.v[j], p);
   return p;
+}
+__device__ __forceinline__ f32x4 fb_block_product(const FbOperand<false>& a, const FbOperand<false>& b) {
+  // scale operands of zero select the instruction without block scales
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, (f32x4){0.f, 0.f, 0.f, 0.f}, 0,
+                                                          0, 0, 0, 0, 0);
 }
 
 // The tile of this workgroup: the grid is read as 8 interleaved streams, one per XCD, each a

@@ -82,15 +82,21 @@ __global__ __launch_bounds__(FS_THREADS) void fp8b128_strip_kernel(Fp8b128GemmAr
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       if (kb + FS_WAVES * d < a.nb) {
+        FbOperand<EXACT> wv[NS];
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+        for (int s = 0; s < NS; ++s) wv[s].set(wf[d][s][0], wf[d][s][1]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          FbOperand<EXACT> xv;
+          xv.set(xf[d][t][0], xf[d][t][1]);
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            const f32x4 p = fb_block_product<EXACT>(wf[d][s][0], wf[d][s][1], xf[d][t][0], xf[d][t][1]);
+            const f32x4 p = fb_block_product(wv[s], xv);
             const float m = sx[d][t] * ss[d][s];
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[t][s][i] = __builtin_fmaf(p[i], m, acc[t][s][i]);
           }
+        }
       }
       load(d, kb + FS_WAVES * (D + d));
     }
@@ -132,8 +138,8 @@ hipError_t launch_strips(const Fp8b128GemmArgs& a, hipStream_t s) {
 // of them gate strips, half the up strips of the same channels, so that both sums of a channel
 // end in one lane) and 4 tiles of 16 tokens. Per block of 128 inputs the rows' 128 bytes go
 // straight to LDS (16-byte chunk c of row r at position c ^ (r % 8), so that eight lanes reading
-// one chunk of eight rows meet eight different banks' worth of LDS), one block ahead of the
-// products: two stages, one barrier per block.
+// one chunk of eight rows meet eight different banks' worth of LDS), in two stages with one
+// barrier per block.
 template <int SW, int WT>
 struct FbTile {
   static constexpr int WAVES = 2 * WT, THREADS = 64 * WAVES, BC = 32 * SW, BT = 64 * WT;
@@ -189,62 +195,109 @@ __device__ void fb_tile(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tile_t
   const uint32_t wso = valid(strip_row(lane % SW))
                            ? (uint32_t)(channel(strip_row(lane % SW)) / 128 * a.nb) * 4u : FB_OOB;
 
-  float sw_next;
-  auto load = [&](int kb) {
-    const int st = kb & 1;
+  // The loads of one block, in LOADS parts: a wave cannot go on while the memory unit's queue is
+  // full, so they are issued a few at a time between the products.
+  constexpr int LOADS = 1 + NW + NX, PER = SW == 8 ? 2 : 3;
+  float sw_after = 0.0f;  // the wave's weight scales of the block, strip s in lane s
+  auto load = [&](int n, int st, int kb) {
     const bool in = 128 * kb + chunk < a.in;  // chunks past the row's end are zeros
-    sw_next = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, wso, 4u * kb, 0));
-#pragma unroll
-    for (int j = 0; j < NW; ++j)
+    if (n == 0) {
+      sw_after = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, kb < a.nb ? wso : FB_OOB, 4u * kb, 0));
+      if (w < WT)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&sh.sx[st][64 * w]), 4,
+                                                 kb < a.nb ? xso : FB_OOB, 4u * kb, 0, 0);
+    } else if (n <= NW) {
+      const int j = n - 1;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][1024 * (NW * w + j)]), 16,
                                                in ? wo[j] : FB_OOB, 128u * kb, 0, 0);
-#pragma unroll
-    for (int j = 0; j < NX; ++j)
+    } else if (n < LOADS) {
+      const int j = n - 1 - NW;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(&sh.x[st][1024 * (NX * w + j)]), 16,
                                                in ? xo[j] : FB_OOB, 128u * kb, 0, 0);
-    if (w < WT)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&sh.sx[st][64 * w]), 4, xso, 4u * kb,
-                                               0, 0);
+    }
   };
 
-  f32x4 acc[SW][4];
+  f32x4 acc[SW][4], p[4];
+  float m[4];
 #pragma unroll
-  for (int s = 0; s < SW; ++s)
+  for (int t = 0; t < 4; ++t) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < SW; ++s) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    p[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    m[t] = 0.0f;
+  }
   const int at0 = 128 * r + 16 * (q ^ (r & 7)), at1 = 128 * r + 16 * ((4 + q) ^ (r & 7));
-
-  load(0);
-  for (int kb = 0; kb < a.nb; ++kb) {
-    wait_vmcnt<0>();  // this wave's part of block kb is in LDS
-    const float sw = sw_next;
-    bare_barrier();   // everyone's is, and nobody reads the other stage any more
-    if (kb + 1 < a.nb) load(kb + 1);
-    const uint8_t* xl = sh.x[kb & 1] + 128 * 64 * wt;
-    const uint8_t* wl = sh.w[kb & 1];
-    u32x4 b[4][2];
-    float sx[4];
+  FbOperand<EXACT> av[2], bv[4];
+  float sx[4];
+  auto read_a = [&](int st, int s) {
+    const uint8_t* l = sh.w[st] + 128 * strip_row(s);
+    av[s & 1].set(*reinterpret_cast<const u32x4*>(l + at0), *reinterpret_cast<const u32x4*>(l + at1));
+  };
+  auto read_b = [&](int st, int t) {
+    const uint8_t* l = sh.x[st] + 128 * (64 * wt + 16 * t);
+    bv[t].set(*reinterpret_cast<const u32x4*>(l + at0), *reinterpret_cast<const u32x4*>(l + at1));
+  };
+  auto read_sx = [&](int st, int t) { sx[t] = sh.sx[st][64 * wt + 16 * t + r]; };
+  // Adds the last product of token tile t to the sum of strip s (the strip before the one
+  // whose product comes next, so that it has had three products' time to finish).
+  auto add = [&](int s, int t) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      b[t][0] = *reinterpret_cast<const u32x4*>(xl + 2048 * t + at0);
-      b[t][1] = *reinterpret_cast<const u32x4*>(xl + 2048 * t + at1);
-      sx[t] = sh.sx[kb & 1][64 * wt + 16 * t + r];
-    }
+    for (int i = 0; i < 4; ++i) acc[s][t][i] = __builtin_fmaf(p[t][i], m[t], acc[s][t][i]);
+    asm volatile("" : "+v"(acc[s][t]));  // done here, not where the compiler would gather them
+  };
+
+#pragma unroll
+  for (int n = 0; n < LOADS; ++n) load(n, 0, 0);
+  float sw = sw_after;
+#pragma unroll
+  for (int n = 0; n < PER; ++n) load(n, 1, 1);
+  wait_vmcnt<PER>();
+  bare_barrier();
+  read_a(0, 0);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    read_b(0, t);
+    read_sx(0, t);
+  }
+  // One block. Before its last strip, whose operands are in registers, the next block has
+  // landed everywhere and this stage is no longer read: its refill starts, and the next block's
+  // operands are read as the last strip's products release the registers.
+  for (int kb = 0; kb < a.nb; ++kb) {
+    const int st = kb & 1;
+    float sw_next = 0.0f;
 #pragma unroll
     for (int s = 0; s < SW; ++s) {
-      const u32x4 a0 = *reinterpret_cast<const u32x4*>(wl + 128 * strip_row(s) + at0);
-      const u32x4 a1 = *reinterpret_cast<const u32x4*>(wl + 128 * strip_row(s) + at1);
+      const bool last = s == SW - 1;
+      __builtin_amdgcn_sched_barrier(0);
+      if (last) {
+        wait_vmcnt<0>();
+        bare_barrier();
+        read_a(st ^ 1, 0);
+      } else {
+        read_a(st, s + 1);
+      }
+      if (last) sw_next = sw_after;
+#pragma unroll
+      for (int n = 0; n < PER; ++n)
+        load(n + (last ? 0 : PER * (s + 1)), last ? st : st ^ 1, kb + (last ? 2 : 1));
       const float ss = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw), s));
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const f32x4 p = fb_block_product<EXACT>(a0, a1, b[t][0], b[t][1]);
-        const float m = sx[t] * ss;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[s][t][i] = __builtin_fmaf(p[i], m, acc[s][t][i]);
+        add((s + SW - 1) % SW, t);
+        p[t] = fb_block_product(av[s & 1], bv[t]);
+        m[t] = sx[t] * ss;
+        if (last) {
+          __builtin_amdgcn_sched_barrier(0);
+          read_b(st ^ 1, t);
+          read_sx(st ^ 1, t);
+        }
       }
     }
+    sw = sw_next;
   }
-  wait_vmcnt<0>();
+#pragma unroll
+  for (int t = 0; t < 4; ++t) add(SW - 1, t);
+  wait_vmcnt<0>();  // no load may still be writing this workgroup's LDS when it ends
 
   constexpr int NO = GATED ? SW / 2 : SW;
 #pragma unroll
