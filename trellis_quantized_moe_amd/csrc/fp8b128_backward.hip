@@ -153,6 +153,27 @@ __global__ __launch_bounds__(DS_THREADS) void fp8b128_dx_strip_kernel(Fp8b128Bac
   dx_strip<TT>(a, sh);
 }
 
+// The 64 x 64 results of each wave of a tile (row 16 t + lane % 16, inputs 16 c + 4 (lane / 16) ..
+// + 3 in acc[c][t]) to its rows at dst, of which `rows` exist and `bytes` of each, by whole rows
+// through LDS, which no wave needs any more.
+__device__ __forceinline__ void store_tile(void* lds, int w, const f32x4 (&acc)[4][4], uint8_t* dst,
+                                           int64_t stride, int rows, int bytes) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  __syncthreads();
+  FbRows<128> out{static_cast<uint8_t*>(lds) + w * (32 * 128)};
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const f32x4 x = acc[c][2 * hf + v];
+        out.put(16 * v + r, 2 * (16 * c + 4 * q), (u32x2){fb_pack_bf16(x[0], x[1]), fb_pack_bf16(x[2], x[3])});
+      }
+    out.store(dst + 32 * hf * stride, stride, rows - 32 * hf, bytes);
+  }
+}
+
 // ---- dx, many tokens ------------------------------------------------------------------------
 //
 // A workgroup of eight waves owns 256 inputs of 128 tokens, wave (wi, wt) 64 inputs of 64
@@ -190,21 +211,22 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
   const int ib = min((i0 + 64 * wi) / 128, a.nb - 1);
   constexpr int LOADS = 5;
   float sc[4];
-  auto load = [&](int st, int k) {  // steps past the last are read as zeros
+  // A step's loads, in four parts (a wave cannot go on while the memory unit's queue is full, so
+  // they are issued between the products); steps past the last are read as zeros.
+  auto load = [&](int n, int st, int k) {
     const int left = min(64, a.out - 64 * k);
-    const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 64 * k : 0) * a.in,
-                                  left > 0 ? (uint32_t)left * (uint32_t)a.in : 0u);
-    const bool in = dcol < left;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][256 * (8 * w + 4 * j)]), 16,
-                                               wo[j], 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][128 * (16 * w + 8 * j)]), 16,
-                                               in ? dof[j] : FB_OOB, 128u * k, 0, 0);
-    sc[st] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-        rs, 64 * (k & ~1) < a.out ? (uint32_t)(k / 2 * a.nb + ib) * 4u : FB_OOB, 0, 0));
+    if (n < 2) {
+      const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 64 * k : 0) * a.in,
+                                    left > 0 ? (uint32_t)left * (uint32_t)a.in : 0u);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][256 * (8 * w + 4 * n)]), 16,
+                                               wo[n], 0, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][128 * (16 * w + 8 * (n - 2))]), 16,
+                                               dcol < left ? dof[n - 2] : FB_OOB, 128u * k, 0, 0);
+    }
+    if (n == 3)
+      sc[st] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          rs, 64 * (k & ~1) < a.out ? (uint32_t)(k / 2 * a.nb + ib) * 4u : FB_OOB, 0, 0));
   };
 
   f32x4 acc[4][4], p[4][4];
@@ -226,9 +248,13 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
       av[j][c] = read_tr8(&sh.w[st][256 * row + 16 * ((4 * wi + c) ^ (row & 15)) + 8 * (r & 1)]);
     }
   };
-  auto multiply = [&](int j, bool first) {
+  auto multiply = [&](int j, bool first, int st, int k) {  // with the loads of step k, if k >= 0
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      if (k >= 0) {
+        __builtin_amdgcn_sched_barrier(0);
+        load(c, st, k);
+      }
       const u32x4 a8 = fb_bf16_of8(av[j][c].x, av[j][c].y);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -236,7 +262,9 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
     }
   };
 #pragma unroll
-  for (int k = 0; k < 4; ++k) load(k, k);
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) load(n, k, k);
   wait_vmcnt<3 * LOADS>();
   bare_barrier();
   read(0, 0);
@@ -245,14 +273,13 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
   // and this step's stage is no longer read.
   auto step = [&](int st, int k) {
     read(st, 1);
-    multiply(0, (st & 1) == 0);
+    multiply(0, (st & 1) == 0, 0, -1);
     __builtin_amdgcn_sched_barrier(0);
     wait_vmcnt<2 * LOADS>();
     bare_barrier();
     const float s = sc[st];
     read((st + 1) & 3, 0);
-    load(st, k + 4);
-    multiply(1, false);
+    multiply(1, false, st, k + 4);
     if (st & 1) {  // the block of 128 outputs is complete
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -272,15 +299,8 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
     }
   }
   wait_vmcnt<0>();
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int i = i0 + 64 * wi + 16 * c + 4 * q;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int row = 64 * wt + 16 * t + r;
-      if (row < rows && i < a.in) store4(a.dx + (t0 + row) * a.in + i, acc[c][t]);
-    }
-  }
+  store_tile(&sh, w, acc, reinterpret_cast<uint8_t*>(a.dx + (t0 + 64 * wt) * a.in + i0 + 64 * wi),
+             (int64_t)a.in * 2, rows - 64 * wt, (a.in - i0 - 64 * wi) * 2);
 }
 
 __global__ __launch_bounds__(512) void fp8b128_dx_kernel(Fp8b128BackwardArgs a, int tt, int ti) {
@@ -345,20 +365,24 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
     dof[j] = o < a.out ? ((uint32_t)row * (uint32_t)a.out + o) * 2u : FB_OOB;
   }
   constexpr int LOADS = 6;
-  auto load = [&](int st, int k) {  // rows past the last token are read as zeros
+  // A step's loads, in three parts, as in dx_tile; rows past the last token are read as zeros.
+  auto load = [&](int n, int st, int k) {
     const int64_t t = (int64_t)64 * k;
     const int left = (int)min((int64_t)64, a.T - t);
     const int64_t at = left > 0 ? t : 0;
-    const GemmRsrc rx = gemm_rsrc(a.xw + at * a.in, left > 0 ? (uint32_t)left * (uint32_t)a.in * 2u : 0u);
-    const GemmRsrc rd = gemm_rsrc(a.dy + at * a.out, left > 0 ? (uint32_t)left * (uint32_t)a.out * 2u : 0u);
+    if (n < 2) {
+      const GemmRsrc rx = gemm_rsrc(a.xw + at * a.in, left > 0 ? (uint32_t)left * (uint32_t)a.in * 2u : 0u);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(&sh.x[st][512 * (8 * w + 2 * j)]), 16,
-                                               xo[j], 0, 0, 0);
+      for (int j = 2 * n; j < 2 * n + 2; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(&sh.x[st][512 * (8 * w + 2 * j)]), 16,
+                                                 xo[j], 0, 0, 0);
+    } else {
+      const GemmRsrc rd = gemm_rsrc(a.dy + at * a.out, left > 0 ? (uint32_t)left * (uint32_t)a.out * 2u : 0u);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][256 * (8 * w + 4 * j)]), 16,
-                                               dof[j], 0, 0, 0);
+      for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][256 * (8 * w + 4 * j)]), 16,
+                                                 dof[j], 0, 0, 0);
+    }
   };
   f32x4 acc[4][4];
 #pragma unroll
@@ -383,26 +407,32 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
       av[j][c] = (u32x4){lo.x, lo.y, hi.x, hi.y};
     }
   };
-  auto multiply = [&](int j) {
+  auto multiply = [&](int j, int st, int k) {  // with the loads of step k, if k >= 0
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 4; ++c) {
+      if (k >= 0) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (c < 3) load(c, st, k);
+      }
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[c][t] = mfma_bf16(av[j][c], bv[j][t], acc[c][t]);
+    }
   };
 #pragma unroll
-  for (int k = 0; k < 3; ++k) load(k, k);
+  for (int k = 0; k < 3; ++k)
+#pragma unroll
+    for (int n = 0; n < 3; ++n) load(n, k, k);
   wait_vmcnt<2 * LOADS>();
   bare_barrier();
   read(0, 0);
   auto step = [&](int st, int k) {  // as in dx_tile
     read(st, 1);
-    multiply(0);
+    multiply(0, 0, -1);
     __builtin_amdgcn_sched_barrier(0);
     wait_vmcnt<LOADS>();
     bare_barrier();
     read((st + 1) % 3, 0);
-    load(st, k + 3);
-    multiply(1);
+    multiply(1, st, k + 3);
   };
   for (int k = 0; k < nsteps; k += 3) {
     step(0, k);
@@ -410,15 +440,8 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
     if (k + 2 < nsteps) step(2, k + 2);
   }
   wait_vmcnt<0>();
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int i = i0 + 64 * wi + 16 * c + 4 * q;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int o = o0 + 64 * wo + 16 * t + r;
-      if (o < a.out && i < a.in) store4(a.dw + (int64_t)o * a.in + i, acc[c][t]);
-    }
-  }
+  store_tile(&sh, w, acc, reinterpret_cast<uint8_t*>(a.dw + (int64_t)(o0 + 64 * wo) * a.in + i0 + 64 * wi),
+             (int64_t)a.in * 2, a.out - o0 - 64 * wo, (a.in - i0 - 64 * wi) * 2);
 }
 
 __global__ __launch_bounds__(512) void fp8b128_dw_kernel(Fp8b128BackwardArgs a, int to, int ti) {
