@@ -30,7 +30,7 @@ FORWARD = [(1, 16, 16), (1, 1536, 5120), (2, 48, 112), (5, 160, 128), (16, 32, 1
 GATED = [(1, 32, 16), (1, 1536, 5120), (3, 96, 144), (16, 288, 272), (31, 64, 400), (64, 1440, 528),
          (130, 160, 1040), (257, 544, 256), (300, 800, 400), (700, 1056, 272), (2900, 2848, 272)]
 BACKWARD = [(1, 32, 16), (1, 288, 400), (2, 64, 128), (17, 32, 272), (40, 288, 144), (64, 96, 1040),
-            (129, 256, 256), (200, 544, 400), (257, 160, 656), (333, 1056, 272), (600, 288, 784), (2100, 352, 2064)]
+            (129, 256, 256), (200, 544, 400), (257, 160, 656), (333, 1056, 272), (600, 288, 784), (2100, 352, 2064), (4200, 64, 2320)]
 
 
 def bits_of(t):

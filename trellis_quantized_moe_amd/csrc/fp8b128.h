@@ -11,6 +11,13 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 constexpr int FB_BLOCK = 128;         // inputs (and outputs) per scale
 constexpr uint32_t FB_OOB = 0x80000000u;  // a buffer offset past every resource: loads give 0
 
+// A value at the same address for the whole wave, that the kernel does not write, through the
+// scalar cache.
+__device__ __forceinline__ float fb_uniform_load(const float* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) float*>(
+      reinterpret_cast<uintptr_t>(p));
+}
+
 // Four E4M3 codes as four bf16 values (exact: bf16 holds every E4M3 value).
 __device__ __forceinline__ u32x2 fb_bf16_of4(uint32_t c) {
   u32x2 r;
@@ -72,11 +79,14 @@ __device__ __forceinline__ f32x4 fb_block_product(const FbOperand<false>& a, con
                                                           0, 0, 0, 0, 0);
 }
 
-// The tile of this workgroup: the grid is read as 8 interleaved streams, one per XCD, each a
-// contiguous range of tiles in an order that walks 4 channel tiles per token tile, so that the
-// tiles an XCD works on at one time share rows of both operands in its L2.
-__device__ inline bool fb_tile_of(int tt, int tc, int* t, int* c) {
-  const int n = tt * tc, per = (n + 7) >> 3, j = blockIdx.x >> 3;
+constexpr int FB_CUS = 256;  // compute units: workgroups of a grid that walks its tiles
+
+// Tile j of this workgroup's stream (a workgroup starts with j = blockIdx.x / 8 and, in a grid
+// smaller than the tiles, goes on by gridDim.x / 8): the grid is read as 8 interleaved streams,
+// one per XCD, each a contiguous range of tiles in an order that walks 4 channel tiles per token
+// tile, so that the tiles an XCD works on at one time share rows of both operands in its L2.
+__device__ inline bool fb_tile_of(int tt, int tc, int j, int* t, int* c) {
+  const int n = tt * tc, per = (n + 7) >> 3;
   const int u = (blockIdx.x & 7) * per + j;
   if (j >= per || u >= n) return false;
   const int band = u / (4 * tt), first = 4 * band, width = min(4, tc - first);
@@ -141,22 +151,30 @@ __device__ __forceinline__ void fb_store(const Fp8b128GemmArgs& a, int64_t t, in
   }
 }
 
-// A wave's rows of ROW bytes (64, 128 or 256) on their way to memory: written to LDS by pieces of a
+// The lane, as a value that the compiler does not know to be the same in every tile: what a kernel
+// that walks tiles derives from it between two tiles would otherwise be computed once and held
+// in registers through the products.
+__device__ __forceinline__ int fb_fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+// N of a wave's rows of ROW bytes (64, 128 or 256) on their way to memory: written to LDS by pieces of a
 // row, 16-byte chunk c of row k at position c ^ (k % chunks) so that the rows of one piece meet
 // different banks, and stored by whole rows, 16 bytes a lane.
-template <int ROW>
+template <int ROW, int N>
 struct FbRows {
   static constexpr int CHUNKS = ROW / 16;
-  uint8_t* lds;  // of this wave: 32 rows
+  uint8_t* lds;  // N * ROW bytes of this wave's own
   template <class V>
   __device__ __forceinline__ void put(int k, int byte, V v) {
     *reinterpret_cast<V*>(lds + k * ROW + 16 * ((byte >> 4) ^ (k & (CHUNKS - 1))) + (byte & 15)) = v;
   }
   // rows 0 .. rows - 1 to dst + row * stride, their first `bytes` bytes
-  __device__ __forceinline__ void store(uint8_t* dst, int64_t stride, int rows, int bytes) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ void store(uint8_t* dst, int64_t stride, int rows, int bytes, int lane) {
 #pragma unroll
-    for (int j = 0; j < 32 * CHUNKS / 64; ++j) {
+    for (int j = 0; j < N * CHUNKS / 64; ++j) {
       const int k = j * (64 / CHUNKS) + lane / CHUNKS;
       const int c = (lane & (CHUNKS - 1)) ^ (k & (CHUNKS - 1));
       const u32x4 v = *reinterpret_cast<const u32x4*>(lds + k * ROW + 16 * (lane & (CHUNKS - 1)));

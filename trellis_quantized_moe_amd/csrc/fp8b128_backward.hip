@@ -9,6 +9,8 @@
 // Inputs are the A operand, so a lane ends with four consecutive inputs of a token or channel.
 #include "fp8b128.h"
 
+#include <algorithm>
+
 namespace tq {
 
 namespace {
@@ -69,7 +71,9 @@ __device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStripShared<TT>& sh) {
   for (int t = 0; t < TT; ++t)
     dof[t] = 16 * t + r < rows ? (uint32_t)(16 * t + r) * (uint32_t)a.out * 2u + 16u * q : FB_OOB;
 
-  constexpr int LOADS = 5 + 4 * TT;
+  // Loads of one block that the waits count: the compiler could move the scale's across a wait,
+  // so it is not one of them.
+  constexpr int LOADS = 4 + 4 * TT;
   u32x4 d[2][TT][4];
   float sc[2];
   auto load = [&](int k, int ob) {  // blocks past the last are read as zeros
@@ -155,12 +159,11 @@ __global__ __launch_bounds__(DS_THREADS) void fp8b128_dx_strip_kernel(Fp8b128Bac
 
 // The 64 x 64 results of each wave of a tile (row 16 t + lane % 16, inputs 16 c + 4 (lane / 16) ..
 // + 3 in acc[c][t]) to its rows at dst, of which `rows` exist and `bytes` of each, by whole rows
-// through LDS, which no wave needs any more.
-__device__ __forceinline__ void store_tile(void* lds, int w, const f32x4 (&acc)[4][4], uint8_t* dst,
+// through 4096 bytes of LDS of the wave's own.
+__device__ __forceinline__ void store_tile(uint8_t* lds, const f32x4 (&acc)[4][4], uint8_t* dst,
                                            int64_t stride, int rows, int bytes) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  __syncthreads();
-  FbRows<128> out{static_cast<uint8_t*>(lds) + w * (32 * 128)};
+  const int lane = fb_fresh_lane(), r = lane & 15, q = lane >> 4;
+  FbRows<128, 32> out{lds};
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
@@ -170,7 +173,7 @@ __device__ __forceinline__ void store_tile(void* lds, int w, const f32x4 (&acc)[
         const f32x4 x = acc[c][2 * hf + v];
         out.put(16 * v + r, 2 * (16 * c + 4 * q), (u32x2){fb_pack_bf16(x[0], x[1]), fb_pack_bf16(x[2], x[3])});
       }
-    out.store(dst + 32 * hf * stride, stride, rows - 32 * hf, bytes);
+    out.store(dst + 32 * hf * stride, stride, rows - 32 * hf, bytes, lane);
   }
 }
 
@@ -185,32 +188,42 @@ struct DxShared {
   alignas(16) uint8_t d[4][128 * 128];
 };
 
-__device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, int tile_i) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wi = w & 3, wt = w >> 2;
-  const int64_t t0 = (int64_t)tile_t * 128;
-  const int rows = (int)min((int64_t)128, a.T - t0);
-  const int i0 = tile_i * 256;
-  const int nsteps = (a.out + 63) / 64;
+// One workgroup per compute unit takes tile after tile: the first steps of the next tile are
+// loading while a tile's results are stored.
+struct DxTile {
+  int64_t t0;
+  int rows, i0, ib;
+  uint32_t wo[2], dof[2];
+};
 
-  const GemmRsrc rd = gemm_rsrc(a.dy + t0 * a.out, (uint32_t)rows * (uint32_t)a.out * 2u);
-  const GemmRsrc rs = gemm_rsrc(a.ws, (uint32_t)((a.out + 127) / 128 * a.nb) * 4u);
+__device__ __forceinline__ DxTile dx_tile_at(const Fp8b128BackwardArgs& a, int tile_t, int tile_i, int w) {
+  const int lane = fb_fresh_lane();
+  DxTile d;
+  d.t0 = (int64_t)tile_t * 128;
+  d.rows = (int)min((int64_t)128, a.T - d.t0);
+  d.i0 = tile_i * 256;
+  d.ib = min((d.i0 + 64 * (w & 3)) / 128, a.nb - 1);
   // codes: an instruction fills 4 rows; lane l position l % 16 of row l / 16, which holds the
   // row's 16-byte chunk (l % 16) ^ (row % 16). dy: 8 rows; position l % 8 of row l / 8 holds
   // chunk (l % 8) ^ (row % 8).
-  uint32_t wo[2], dof[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int row = 8 * w + 4 * j + (lane >> 4), col = i0 + 16 * ((lane & 15) ^ (row & 15));
-    wo[j] = col < a.in ? (uint32_t)row * (uint32_t)a.in + col : FB_OOB;
+    const int row = 8 * w + 4 * j + (lane >> 4), col = d.i0 + 16 * ((lane & 15) ^ (row & 15));
+    d.wo[j] = col < a.in ? (uint32_t)row * (uint32_t)a.in + col : FB_OOB;
     const int tok = 16 * w + 8 * j + (lane >> 3);
-    dof[j] = tok < rows ? (uint32_t)tok * (uint32_t)a.out * 2u + 16u * ((lane & 7) ^ (lane >> 3)) : FB_OOB;
+    d.dof[j] = tok < d.rows ? (uint32_t)tok * (uint32_t)a.out * 2u + 16u * ((lane & 7) ^ (lane >> 3)) : FB_OOB;
   }
+  return d;
+}
+
+__device__ void dx_tiles(const Fp8b128BackwardArgs& a, DxShared& sh, int tt, int ti) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = w & 3, wt = w >> 2;
+  const int nsteps = (a.out + 63) / 64;
   const int dcol = 8 * ((lane & 7) ^ (lane >> 3));  // this lane's first output of a step
-  const int ib = min((i0 + 64 * wi) / 128, a.nb - 1);
-  constexpr int LOADS = 5;
-  float sc[4];
+  constexpr int LOADS = 4;  // of one step; the scales come through the scalar cache
+  DxTile d;
   // A step's loads, in four parts (a wave cannot go on while the memory unit's queue is full, so
   // they are issued between the products); steps past the last are read as zeros.
   auto load = [&](int n, int st, int k) {
@@ -219,21 +232,15 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
       const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 64 * k : 0) * a.in,
                                     left > 0 ? (uint32_t)left * (uint32_t)a.in : 0u);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][256 * (8 * w + 4 * n)]), 16,
-                                               wo[n], 0, 0, 0);
+                                               d.wo[n], 0, 0, 0);
     } else {
+      const GemmRsrc rd = gemm_rsrc(a.dy + d.t0 * a.out, (uint32_t)d.rows * (uint32_t)a.out * 2u);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][128 * (16 * w + 8 * (n - 2))]), 16,
-                                               dcol < left ? dof[n - 2] : FB_OOB, 128u * k, 0, 0);
+                                               dcol < left ? d.dof[n - 2] : FB_OOB, 128u * k, 0, 0);
     }
-    if (n == 3)
-      sc[st] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-          rs, 64 * (k & ~1) < a.out ? (uint32_t)(k / 2 * a.nb + ib) * 4u : FB_OOB, 0, 0));
   };
 
   f32x4 acc[4][4], p[4][4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int t = 0; t < 4; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
   // operands of 32 outputs (half j of a step)
   u32x2 av[2][4];
   u32x4 bv[2][4];
@@ -261,23 +268,17 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
         p[c][t] = mfma_bf16(a8, bv[j][t], first ? (f32x4){0.f, 0.f, 0.f, 0.f} : p[c][t]);
     }
   };
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) load(n, k, k);
-  wait_vmcnt<3 * LOADS>();
-  bare_barrier();
-  read(0, 0);
   // A step's second half is read while its first half is multiplied, and the next step's first
   // half while its second is: between the two, the next step's data have landed everywhere,
   // and this step's stage is no longer read.
   auto step = [&](int st, int k) {
+    float s = 0.0f;
+    if (st & 1) s = fb_uniform_load(a.ws + (int64_t)(k / 2) * a.nb + d.ib);
     read(st, 1);
     multiply(0, (st & 1) == 0, 0, -1);
     __builtin_amdgcn_sched_barrier(0);
     wait_vmcnt<2 * LOADS>();
     bare_barrier();
-    const float s = sc[st];
     read((st + 1) & 3, 0);
     multiply(1, false, st, k + 4);
     if (st & 1) {  // the block of 128 outputs is complete
@@ -289,24 +290,57 @@ __device__ void dx_tile(const Fp8b128BackwardArgs& a, DxShared& sh, int tile_t, 
           for (int i = 0; i < 4; ++i) acc[c][t][i] = __builtin_fmaf(p[c][t][i], s, acc[c][t][i]);
     }
   };
-  // whole blocks (a step past the last adds zeros)
-  for (int k = 0; k < nsteps; k += 4) {
-    step(0, k);
-    step(1, k + 1);
-    if (k + 2 < nsteps) {
-      step(2, k + 2);
-      step(3, k + 3);
+  auto load_steps = [&](int first, int last) {
+#pragma unroll
+    for (int k = first; k < last; ++k)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) load(n, k, k);
+  };
+
+  int tile_t, tile_i;
+  int j = blockIdx.x >> 3;
+  if (!fb_tile_of(tt, ti, j, &tile_t, &tile_i)) return;
+  d = dx_tile_at(a, tile_t, tile_i, w);
+  load_steps(0, 3);
+  for (bool more = true; more;) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    load_steps(3, 4);
+    wait_vmcnt<3 * LOADS>();
+    bare_barrier();
+    read(0, 0);
+    // whole blocks (a step past the last adds zeros)
+    for (int k = 0; k < nsteps; k += 4) {
+      step(0, k);
+      step(1, k + 1);
+      if (k + 2 < nsteps) {
+        step(2, k + 2);
+        step(3, k + 3);
+      }
     }
+    // the loads past the last step have landed, and no wave reads a stage any more
+    wait_vmcnt<0>();
+    bare_barrier();
+    uint8_t* dst = reinterpret_cast<uint8_t*>(a.dx + (d.t0 + 64 * wt) * a.in + d.i0 + 64 * wi);
+    const int rows = d.rows - 64 * wt, bytes = (a.in - d.i0 - 64 * wi) * 2;
+    j += gridDim.x >> 3;
+    more = fb_tile_of(tt, ti, j, &tile_t, &tile_i);
+    if (more) {
+      d = dx_tile_at(a, tile_t, tile_i, w);
+      load_steps(0, 3);
+    }
+    // through the last stage, which the next tile fills after the barrier
+    store_tile(w < 4 ? sh.w[3] + 4096 * w : sh.d[3] + 4096 * (w - 4), acc, dst, (int64_t)a.in * 2, rows, bytes);
+    bare_barrier();
   }
   wait_vmcnt<0>();
-  store_tile(&sh, w, acc, reinterpret_cast<uint8_t*>(a.dx + (t0 + 64 * wt) * a.in + i0 + 64 * wi),
-             (int64_t)a.in * 2, rows - 64 * wt, (a.in - i0 - 64 * wi) * 2);
 }
 
 __global__ __launch_bounds__(512) void fp8b128_dx_kernel(Fp8b128BackwardArgs a, int tt, int ti) {
   __shared__ DxShared sh;
-  int t, i;
-  if (fb_tile_of(tt, ti, &t, &i)) dx_tile(a, sh, t, i);
+  dx_tiles(a, sh, tt, ti);
 }
 
 // ---- dw -------------------------------------------------------------------------------------
@@ -440,14 +474,15 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
     if (k + 2 < nsteps) step(2, k + 2);
   }
   wait_vmcnt<0>();
-  store_tile(&sh, w, acc, reinterpret_cast<uint8_t*>(a.dw + (int64_t)(o0 + 64 * wo) * a.in + i0 + 64 * wi),
+  __syncthreads();
+  store_tile(sh.x[0] + 4096 * w, acc, reinterpret_cast<uint8_t*>(a.dw + (int64_t)(o0 + 64 * wo) * a.in + i0 + 64 * wi),
              (int64_t)a.in * 2, a.out - o0 - 64 * wo, (a.in - i0 - 64 * wi) * 2);
 }
 
 __global__ __launch_bounds__(512) void fp8b128_dw_kernel(Fp8b128BackwardArgs a, int to, int ti) {
   __shared__ DwShared sh;
   int o, i;
-  if (fb_tile_of(to, ti, &o, &i)) dw_tile(a, sh, o, i);
+  if (fb_tile_of(to, ti, blockIdx.x >> 3, &o, &i)) dw_tile(a, sh, o, i);
 }
 
 }  // namespace
@@ -457,7 +492,8 @@ hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s) {
   const int64_t tiles = (a.T + 127) / 128 * ((a.in + 255) / 256);
   if (tiles >= 128) {
     const int tt = (int)((a.T + 127) / 128), ti = (a.in + 255) / 256;
-    hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)((tt * ti + 7) & ~7)), dim3(512), 0, s, a, tt, ti);
+    hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)std::min((tt * ti + 7) & ~7, FB_CUS)), dim3(512), 0,
+                       s, a, tt, ti);
     return hipGetLastError();
   }
   const int tt = a.T <= 16 ? 1 : 2;

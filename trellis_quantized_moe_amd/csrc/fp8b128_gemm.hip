@@ -6,6 +6,8 @@
 // lane ends with four consecutive channels of one token.
 #include "fp8b128.h"
 
+#include <algorithm>
+
 namespace tq {
 
 namespace {
@@ -148,54 +150,59 @@ struct FbTile {
   alignas(16) float sx[2][BT];
 };
 
+// One workgroup per compute unit takes tile after tile: the first block of the next tile is
+// loading while a tile's results are stored.
+//
 // SAME: the wave's strips (gated: its gate strips, and its up strips) lie in one block of 128
 // channels, so that a block of inputs has one scale for them.
 template <int EPI, int SW, int WT, bool SAME>
-__device__ void fb_tile(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tile_t, int tile_c) {
+__device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, int tc) {
   using S = FbTile<SW, WT>;
   constexpr bool GATED = fb_gated(EPI), EXACT = EPI == FB_F32;
   constexpr int NX = S::BT / S::WAVES / 8, NW = S::BC / S::WAVES / 8;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wc = w & 1, wt = w >> 1;
-  const int64_t t0 = (int64_t)tile_t * S::BT;
-  const int rows = (int)min((int64_t)S::BT, a.T - t0);
-  const int half = a.out / 2;
-  const int c0 = tile_c * (GATED ? S::BC / 2 : S::BC);  // first channel (gated: of either half)
-  const int width = GATED ? half : a.out;
-
-  // weight row k of the tile: channel and validity
-  auto channel = [&](int k) {
-    if (!GATED) return c0 + k;
-    return k < S::BC / 2 ? c0 + k : half + c0 + k - S::BC / 2;
-  };
-  auto valid = [&](int k) { return c0 + (GATED && k >= S::BC / 2 ? k - S::BC / 2 : k) < width; };
-
+  const int half = a.out / 2, width = GATED ? half : a.out;
   const GemmRsrc rw = gemm_rsrc(a.w, (uint32_t)a.out * (uint32_t)a.in);
   const GemmRsrc rws = gemm_rsrc(a.ws, (uint32_t)(((a.out + 127) / 128) * a.nb) * 4u);
-  const GemmRsrc rx = gemm_rsrc(a.x + t0 * a.in, (uint32_t)rows * (uint32_t)a.in);
-  const GemmRsrc rxs = gemm_rsrc(a.xs + t0 * a.nb, (uint32_t)(rows * a.nb) * 4u);
   // an instruction fills 8 rows: lane l writes position l % 8 of row l / 8
   const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
-  uint32_t wo[NW], xo[NX];
-#pragma unroll
-  for (int j = 0; j < NW; ++j) {
-    const int k = 8 * (NW * w + j) + (lane >> 3);
-    wo[j] = valid(k) ? (uint32_t)channel(k) * (uint32_t)a.in + chunk : FB_OOB;
-  }
-#pragma unroll
-  for (int j = 0; j < NX; ++j) {
-    const int k = 8 * (NX * w + j) + (lane >> 3);
-    xo[j] = k < rows ? (uint32_t)k * (uint32_t)a.in + chunk : FB_OOB;
-  }
-  const uint32_t xso = 64 * w + lane < rows ? (uint32_t)((64 * w + lane) * a.nb) * 4u : FB_OOB;
-  // the wave's strip s is tile rows strip_row(s) ..; lane s loads its scale
+  // the wave's strip s is tile rows strip_row(s) ..
   auto strip_row = [&](int s) {
     if (!GATED) return 16 * (SW * wc + s);
     return (s < SW / 2 ? 0 : S::BC / 2) + 16 * (SW / 2 * wc + s % (SW / 2));
   };
-  const uint32_t wso = valid(strip_row(lane % SW))
-                           ? (uint32_t)(channel(strip_row(lane % SW)) / 128 * a.nb) * 4u : FB_OOB;
+
+  // the tile: its first token, tokens, first channel (gated: of either half), load offsets
+  int64_t t0;
+  int rows, c0;
+  uint32_t wo[NW], xo[NX], xso, wso;
+  auto set_tile = [&](int tile_t, int tile_c) {
+    const int lane = fb_fresh_lane(), chunk = 16 * ((lane & 7) ^ (lane >> 3));
+    t0 = (int64_t)tile_t * S::BT;
+    rows = (int)min((int64_t)S::BT, a.T - t0);
+    c0 = tile_c * (GATED ? S::BC / 2 : S::BC);
+    // weight row k of the tile: channel and validity
+    auto channel = [&](int k) {
+      if (!GATED) return c0 + k;
+      return k < S::BC / 2 ? c0 + k : half + c0 + k - S::BC / 2;
+    };
+    auto valid = [&](int k) { return c0 + (GATED && k >= S::BC / 2 ? k - S::BC / 2 : k) < width; };
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      const int k = 8 * (NW * w + j) + (lane >> 3);
+      wo[j] = valid(k) ? (uint32_t)channel(k) * (uint32_t)a.in + chunk : FB_OOB;
+    }
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+      const int k = 8 * (NX * w + j) + (lane >> 3);
+      xo[j] = k < rows ? (uint32_t)k * (uint32_t)a.in + chunk : FB_OOB;
+    }
+    xso = 64 * w + lane < rows ? (uint32_t)((64 * w + lane) * a.nb) * 4u : FB_OOB;
+    const int k = strip_row(lane % SW);  // lane s loads strip s's scale
+    wso = valid(k) ? (uint32_t)(channel(k) / 128 * a.nb) * 4u : FB_OOB;
+  };
 
   // The loads of one block, in LOADS parts: a wave cannot go on while the memory unit's queue is
   // full, so they are issued a few at a time between the products.
@@ -205,6 +212,7 @@ __device__ void fb_tile(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tile_t
     const bool in = 128 * kb + chunk < a.in;  // chunks past the row's end are zeros
     if (n == 0) {
       sw_after = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, kb < a.nb ? wso : FB_OOB, 4u * kb, 0));
+      const GemmRsrc rxs = gemm_rsrc(a.xs + t0 * a.nb, (uint32_t)(rows * a.nb) * 4u);
       if (w < WT)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&sh.sx[st][64 * w]), 4,
                                                  kb < a.nb ? xso : FB_OOB, 4u * kb, 0, 0);
@@ -214,6 +222,7 @@ __device__ void fb_tile(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tile_t
                                                in ? wo[j] : FB_OOB, 128u * kb, 0, 0);
     } else if (n < LOADS) {
       const int j = n - 1 - NW;
+      const GemmRsrc rx = gemm_rsrc(a.x + t0 * a.in, (uint32_t)rows * (uint32_t)a.in);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(&sh.x[st][1024 * (NX * w + j)]), 16,
                                                in ? xo[j] : FB_OOB, 128u * kb, 0, 0);
     }
@@ -221,13 +230,6 @@ __device__ void fb_tile(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tile_t
 
   f32x4 acc[SW][4], p[4];
   float m[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-#pragma unroll
-    for (int s = 0; s < SW; ++s) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    p[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    m[t] = 0.0f;
-  }
   const int at0 = 128 * r + 16 * (q ^ (r & 7)), at1 = 128 * r + 16 * ((4 + q) ^ (r & 7));
   FbOperand<EXACT> av[2], bv[4];
   float sx[4];
@@ -248,109 +250,138 @@ __device__ void fb_tile(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tile_t
     asm volatile("" : "+v"(acc[s][t]));  // done here, not where the compiler would gather them
   };
 
+  // The results leave through LDS (the second stage: its refill waits for the barrier after), 32
+  // (fp32: 16) tokens of the wave at a time: stored straight from registers, by 32 bytes of 16 rows an
+  // instruction, the bf16 tile took 30,000 cycles beside the 114,000 of its products at 5,120
+  // inputs.
+  constexpr int NO = GATED ? SW / 2 : SW, ESIZE = EPI == FB_F32 ? 4 : 2, ROW = 16 * NO * ESIZE;
+  constexpr int N = EPI == FB_F32 ? 16 : 32;
+  static_assert(N * ROW * S::WAVES <= sizeof(sh.w[1]) + sizeof(sh.x[1]), "results' way out");
+  auto store_results = [&](int64_t token, int tokens, int channel0) {
+    const int lane = fb_fresh_lane(), r = lane & 15, q = lane >> 4;
+    constexpr int IN_W = sizeof(sh.w[1]) / (N * ROW);  // waves whose rows fit the weights' part
+    FbRows<ROW, N> out{w < IN_W ? sh.w[1] + w * (N * ROW) : sh.x[1] + (w - IN_W) * (N * ROW)};
+    const int bytes = min(16 * NO, width - channel0) * ESIZE;
+    const int64_t stride = (int64_t)(EPI == FB_GATED ? half : a.out) * ESIZE;
 #pragma unroll
-  for (int n = 0; n < LOADS; ++n) load(n, 0, 0);
-  float sw = sw_after;
-#pragma unroll
-  for (int n = 0; n < PER; ++n) load(n, 1, 1);
-  wait_vmcnt<PER>();
-  bare_barrier();
-  read_a(0, 0);
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    read_b(0, t);
-    read_sx(0, t);
-  }
-  // One block. Before its last strip, whose operands are in registers, the next block has
-  // landed everywhere and this stage is no longer read: its refill starts, and the next block's
-  // operands are read as the last strip's products release the registers.
-  for (int kb = 0; kb < a.nb; ++kb) {
-    const int st = kb & 1;
-    float sw_next = 0.0f;
-#pragma unroll
-    for (int s = 0; s < SW; ++s) {
-      const bool last = s == SW - 1;
-      __builtin_amdgcn_sched_barrier(0);
-      if (last) {
-        wait_vmcnt<0>();
-        bare_barrier();
-        read_a(st ^ 1, 0);
-      } else {
-        read_a(st, s + 1);
-      }
-      if (last) sw_next = sw_after;
-#pragma unroll
-      for (int n = 0; n < PER; ++n)
-        load(n + (last ? 0 : PER * (s + 1)), last ? st : st ^ 1, kb + (last ? 2 : 1));
-      const float ss = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw), s));
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        add((s + SW - 1) % SW, t);
-        p[t] = fb_block_product(av[s & 1], bv[t]);
-        if (!SAME || s % (GATED ? SW / 2 : SW) == 0) m[t] = sx[t] * ss;
-        if (last) {
-          __builtin_amdgcn_sched_barrier(0);
-          read_b(st ^ 1, t);
-          read_sx(st ^ 1, t);
-        }
-      }
-    }
-    sw = sw_next;
-  }
-#pragma unroll
-  for (int t = 0; t < 4; ++t) add(SW - 1, t);
-  wait_vmcnt<0>();  // no load may still be writing this workgroup's LDS when it ends
-
-  // The results leave through LDS (every wave is done with the stages), 32 tokens of the wave at
-  // a time: stored straight from registers, by 32 bytes of 16 rows an instruction, the bf16 tile
-  // took 30,000 cycles beside the 114,000 of its products at 5,120 inputs.
-  constexpr int NO = GATED ? SW / 2 : SW, ROW = 16 * NO * (EPI == FB_F32 ? 4 : 2);
-  __syncthreads();
-  FbRows<ROW> out{reinterpret_cast<uint8_t*>(&sh) + w * (32 * ROW)};
-  const int first = c0 + strip_row(0);  // the wave's first channel
-  const int bytes = min(16 * NO, width - first) * (EPI == FB_F32 ? 4 : 2);
-  const int64_t stride = (int64_t)(EPI == FB_GATED ? half : a.out) * (EPI == FB_F32 ? 4 : 2);
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    const int tok = 64 * wt + 32 * hf;
-    uint8_t* dst = static_cast<uint8_t*>(a.y) + (t0 + tok) * stride + first * (EPI == FB_F32 ? 4 : 2);
-    u32x2 du[NO][2];
-#pragma unroll
-    for (int s = 0; s < NO; ++s)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int t = 2 * hf + v, k = 16 * v + r, o = 16 * s + 4 * q;
-        const f32x4 g = acc[s][t], u = acc[s + SW - NO][t];
-        if constexpr (EPI == FB_F32) {
-          out.put(k, 4 * o, g);
-        } else if constexpr (EPI == FB_BF16) {
-          out.put(k, 2 * o, (u32x2){fb_pack_bf16(g[0], g[1]), fb_pack_bf16(g[2], g[3])});
-        } else if constexpr (EPI == FB_GATED) {
-          out.put(k, 2 * o, fb_gate4(g, u));
-        } else {
-          u32x2 dh = (u32x2){0, 0}, dg;
-          if (tok + k < rows && first + o < width)
-            dh = *reinterpret_cast<const u32x2*>(a.dh + (t0 + tok + k) * half + first + o);
-          fb_gate_grad4(g, u, dh, &dg, &du[s][v]);
-          out.put(k, 2 * o, dg);
-        }
-      }
-    out.store(dst, stride, rows - tok, bytes);
-    if constexpr (EPI == FB_GATED_GRAD) {
+    for (int f = 0; f < 64; f += N) {
+      uint8_t* dst = static_cast<uint8_t*>(a.y) + (token + f) * stride + (int64_t)channel0 * ESIZE;
+      u32x2 du[NO][N / 16];
 #pragma unroll
       for (int s = 0; s < NO; ++s)
 #pragma unroll
-        for (int v = 0; v < 2; ++v) out.put(16 * v + r, 2 * (16 * s + 4 * q), du[s][v]);
-      out.store(dst + half * 2, stride, rows - tok, bytes);
+        for (int v = 0; v < N / 16; ++v) {
+          const int t = f / 16 + v, k = 16 * v + r, o = 16 * s + 4 * q;
+          const f32x4 g = acc[s][t], u = acc[s + SW - NO][t];
+          if constexpr (EPI == FB_F32) {
+            out.put(k, 4 * o, g);
+          } else if constexpr (EPI == FB_BF16) {
+            out.put(k, 2 * o, (u32x2){fb_pack_bf16(g[0], g[1]), fb_pack_bf16(g[2], g[3])});
+          } else if constexpr (EPI == FB_GATED) {
+            out.put(k, 2 * o, fb_gate4(g, u));
+          } else {
+            u32x2 dh = (u32x2){0, 0}, dg;
+            if (f + k < tokens && channel0 + o < width)
+              dh = *reinterpret_cast<const u32x2*>(a.dh + (token + f + k) * half + channel0 + o);
+            fb_gate_grad4(g, u, dh, &dg, &du[s][v]);
+            out.put(k, 2 * o, dg);
+          }
+        }
+      out.store(dst, stride, tokens - f, bytes, lane);
+      if constexpr (EPI == FB_GATED_GRAD) {
+#pragma unroll
+        for (int s = 0; s < NO; ++s)
+#pragma unroll
+          for (int v = 0; v < N / 16; ++v) out.put(16 * v + r, 2 * (16 * s + 4 * q), du[s][v]);
+        out.store(dst + half * 2, stride, tokens - f, bytes, lane);
+      }
     }
+  };
+
+  int tile_t, tile_c, j = blockIdx.x >> 3;
+  if (!fb_tile_of(tt, tc, j, &tile_t, &tile_c)) return;
+  set_tile(tile_t, tile_c);
+#pragma unroll
+  for (int n = 0; n < LOADS; ++n) load(n, 0, 0);
+  for (bool more = true; more;) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int s = 0; s < SW; ++s) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      p[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      m[t] = 0.0f;
+    }
+    float sw = sw_after;
+#pragma unroll
+    for (int n = 0; n < PER; ++n) load(n, 1, 1);
+    wait_vmcnt<PER - 1>();  // part 0 may have no load that writes LDS, and no other is counted on
+    bare_barrier();
+    read_a(0, 0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      read_b(0, t);
+      read_sx(0, t);
+    }
+    // One block. Before its last strip, whose operands are in registers, the next block has
+    // landed everywhere and this stage is no longer read: its refill starts, and the next block's
+    // operands are read as the last strip's products release the registers.
+    for (int kb = 0; kb < a.nb; ++kb) {
+      const int st = kb & 1;
+      float sw_next = 0.0f;
+#pragma unroll
+      for (int s = 0; s < SW; ++s) {
+        const bool last = s == SW - 1;
+        __builtin_amdgcn_sched_barrier(0);
+        if (last) {
+          wait_vmcnt<0>();
+          bare_barrier();
+          read_a(st ^ 1, 0);
+        } else {
+          read_a(st, s + 1);
+        }
+        if (last) sw_next = sw_after;
+#pragma unroll
+        for (int n = 0; n < PER; ++n)
+          load(n + (last ? 0 : PER * (s + 1)), last ? st : st ^ 1, kb + (last ? 2 : 1));
+        const float ss = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw), s));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          add((s + SW - 1) % SW, t);
+          p[t] = fb_block_product(av[s & 1], bv[t]);
+          if (!SAME || s % (GATED ? SW / 2 : SW) == 0) m[t] = sx[t] * ss;
+          if (last) {
+            __builtin_amdgcn_sched_barrier(0);
+            read_b(st ^ 1, t);
+            read_sx(st ^ 1, t);
+          }
+        }
+      }
+      sw = sw_next;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) add(SW - 1, t);
+    // the loads past the last block have landed, and no wave reads a stage any more
+    wait_vmcnt<0>();
+    bare_barrier();
+    const int64_t first_token = t0 + 64 * wt;
+    const int tokens = rows - 64 * wt, channel0 = c0 + strip_row(0);
+    j += gridDim.x >> 3;
+    more = fb_tile_of(tt, tc, j, &tile_t, &tile_c);
+    if (more) {
+      set_tile(tile_t, tile_c);
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n) load(n, 0, 0);
+    }
+    store_results(first_token, tokens, channel0);
+    bare_barrier();
   }
+  wait_vmcnt<0>();  // no load may still be writing this workgroup's LDS when it ends
 }
 
 template <int EPI, int SW, int WT, bool SAME>
 __global__ __launch_bounds__(128 * WT) void fp8b128_tile_kernel(Fp8b128GemmArgs a, int tt, int tc) {
   __shared__ FbTile<SW, WT> sh;
-  int t, c;
-  if (fb_tile_of(tt, tc, &t, &c)) fb_tile<EPI, SW, WT, SAME>(a, sh, t, c);
+  fb_tiles<EPI, SW, WT, SAME>(a, sh, tt, tc);
 }
 
 template <int EPI, int SW, int WT>
@@ -358,7 +389,9 @@ hipError_t launch_tiles(const Fp8b128GemmArgs& a, hipStream_t s) {
   using S = FbTile<SW, WT>;
   const int width = fb_gated(EPI) ? a.out / 2 : a.out, bc = fb_gated(EPI) ? S::BC / 2 : S::BC;
   const int tt = (int)((a.T + S::BT - 1) / S::BT), tc = (width + bc - 1) / bc;
-  const dim3 grid((unsigned)((tt * tc + 7) & ~7)), block(S::THREADS);
+  // two workgroups of the smaller tile share a compute unit
+  const dim3 grid((unsigned)std::min((tt * tc + 7) & ~7, S::WAVES == 4 ? 2 * FB_CUS : FB_CUS));
+  const dim3 block(S::THREADS);
   // tiles start at multiples of 64 channels, the up half at channel I = width
   if (!fb_gated(EPI) || width % 64 == 0)
     return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, true>, grid, block, s, a, tt, tc);
