@@ -7,70 +7,201 @@
 #include "fp8b128.h"
 
 #include <algorithm>
+#include <cstdint>
 
 namespace tq {
 
 namespace {
 
-// ---- few tokens: one strip of 16 channels per workgroup, the inputs split over its waves ----
+// ---- one or two tokens: a channel per wave ---------------------------------------------------
 //
-// A workgroup owns 16 channels (gated: 16 gate and 16 up channels) of up to 16 * TT tokens.
-// Its eight waves take the blocks of 128 inputs in turn, each straight from memory to
-// registers, D blocks ahead, and their sums are added through LDS in wave order (so the result
-// does not depend on timing). One launch, no workspace.
-constexpr int FS_WAVES = 8;
-constexpr int FS_THREADS = 64 * FS_WAVES;
+// A wave owns one channel (gated: its gate and up rows) and reads the rows 1,024 inputs at a time,
+// 16 bytes a lane, D such steps ahead; the products are fp32 multiply-adds of the decoded codes
+// (exact products), a lane's 16 are scaled once, and the lanes are added at the end. Bound by
+// latency: the waves of all channels read their few kilobytes at once.
+constexpr int FR_WAVES = 4;
 
-template <int EPI, int TT>
-__global__ __launch_bounds__(FS_THREADS) void fp8b128_strip_kernel(Fp8b128GemmArgs a) {
-  constexpr int NS = fb_gated(EPI) ? 2 : 1;
-  constexpr bool EXACT = EPI == FB_F32;
-  constexpr int D = TT == 1 ? 4 : 2;
-  __shared__ f32x4 red[FS_WAVES][TT * NS][64];
+// Adds v over the 64 lanes (every lane gets the sum; the order is fixed).
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+__device__ __forceinline__ void fb_f32_of16(u32x4 c, float (&f)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], true);
+    f[4 * j] = lo.x;
+    f[4 * j + 1] = lo.y;
+    f[4 * j + 2] = hi.x;
+    f[4 * j + 3] = hi.y;
+  }
+}
+
+template <int EPI, int NT>
+__global__ __launch_bounds__(64 * FR_WAVES) void fp8b128_row_kernel(Fp8b128GemmArgs a) {
+  constexpr int NS = fb_gated(EPI) ? 2 : 1, D = 4;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int o = blockIdx.x * FR_WAVES + w, T = (int)a.T;
+  const int width = a.out / NS;
+  if (o >= width) return;
+  const GemmRsrc rx = gemm_rsrc(a.x, (uint32_t)T * (uint32_t)a.in);
+  const GemmRsrc rxs = gemm_rsrc(a.xs, (uint32_t)(T * a.nb) * 4u);
+  GemmRsrc rw[NS], rws[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    rw[s] = gemm_rsrc(a.w + (int64_t)(o + s * width) * a.in, (uint32_t)a.in);
+    rws[s] = gemm_rsrc(a.ws + (int64_t)((o + s * width) / 128) * a.nb, (uint32_t)a.nb * 4u);
+  }
+  u32x4 wf[D][NS], xf[D][NT];
+  float ss[D][NS], sx[D][NT];
+  auto load = [&](int d, int k) {  // past the rows' end: zeros
+    const uint32_t at = 1024u * k + 16u * lane;
+    const bool in = at < (uint32_t)a.in;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      wf[d][s] = __builtin_amdgcn_raw_buffer_load_b128(rw[s], in ? at : FB_OOB, 0, 0);
+      ss[d][s] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws[s], in ? at / 128 * 4 : FB_OOB, 0, 0));
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {  // tokens past the last: outside the resource
+      xf[d][t] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? t * (uint32_t)a.in + at : FB_OOB, 0, 0);
+      sx[d][t] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          rxs, in ? (uint32_t)(t * a.nb + at / 128) * 4u : FB_OOB, 0, 0));
+    }
+  };
+  float acc[NT][NS];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) acc[t][s] = 0.0f;
+  const int steps = (a.in + 1023) / 1024;
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  for (int k = 0; k < steps; k += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (k + d < steps) {
+        float wv[NS][16];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) fb_f32_of16(wf[d][s], wv[s]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float xv[16];
+          fb_f32_of16(xf[d][t], xv);
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            float p = xv[0] * wv[s][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) p = __builtin_fmaf(xv[i], wv[s][i], p);
+            acc[t][s] = __builtin_fmaf(p, sx[d][t] * ss[d][s], acc[t][s]);
+          }
+        }
+      }
+      load(d, k + D + d);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (t >= T) break;
+    const float g = wave_sum(acc[t][0]), u = wave_sum(acc[t][NS - 1]);
+    if (lane != 0) continue;
+    uint16_t* y = static_cast<uint16_t*>(a.y);
+    if constexpr (EPI == FB_F32) {
+      static_cast<float*>(a.y)[(int64_t)t * a.out + o] = g;
+    } else if constexpr (EPI == FB_BF16) {
+      y[(int64_t)t * a.out + o] = (uint16_t)fb_pack_bf16(g, 0.0f);
+    } else if constexpr (EPI == FB_GATED) {
+      y[(int64_t)t * width + o] = (uint16_t)fb_gate4((f32x4){g, 0.f, 0.f, 0.f}, (f32x4){u, 0.f, 0.f, 0.f}).x;
+    } else {
+      u32x2 dg, du;
+      fb_gate_grad4((f32x4){g, 0.f, 0.f, 0.f}, (f32x4){u, 0.f, 0.f, 0.f},
+                    (u32x2){a.dh[(int64_t)t * width + o], 0u}, &dg, &du);
+      y[(int64_t)t * a.out + o] = (uint16_t)dg.x;
+      y[(int64_t)t * a.out + width + o] = (uint16_t)du.x;
+    }
+  }
+}
+
+template <int EPI>
+hipError_t launch_rows(const Fp8b128GemmArgs& a, hipStream_t s) {
+  const unsigned width = a.out / (fb_gated(EPI) ? 2 : 1);
+  const dim3 grid((width + FR_WAVES - 1) / FR_WAVES), block(64 * FR_WAVES);
+  if (a.T == 1) return launch_timed(fp8b128_row_kernel<EPI, 1>, grid, block, s, a);
+  return launch_timed(fp8b128_row_kernel<EPI, 2>, grid, block, s, a);
+}
+
+// ---- few tokens: strips of 16 channels, the inputs split over a workgroup's waves ------------
+//
+// A workgroup owns NS strips of 16 channels (gated: half of them gate strips, half the up strips
+// of the same channels) of up to 16 * TT tokens. Its W waves take the blocks of 128 inputs in
+// turn, each with D stages of LDS of its own that its loads fill D - 1 blocks ahead (no barrier
+// until the end), and their sums are added in wave order, so the result does not depend on
+// timing. One launch, no workspace. The rows come through LDS because a load in operand order
+// has consecutive lanes in different rows, which the memory unit takes one by one: strips of
+// 16 channels and tokens loaded that way took 9.9 us at 32 x 5,120 x 1,536.
+template <int NS, int TT>
+struct FbStrip {
+  static constexpr int ROWS = 16 * (NS + TT);
+  static constexpr int W = NS + TT <= 4 ? 8 : 4, D = NS + TT <= 3 ? 3 : NS + TT == 6 ? 3 : 2;
+  static constexpr int LOADS = ROWS / 8 + 1;  // per block
+  union {
+    struct {
+      alignas(16) uint8_t rows[ROWS * 128];  // strips, then tokens
+      alignas(16) float sx[64];
+    } stage[W][D];
+    f32x4 red[W][TT * NS][64];
+  };
+};
+
+template <int EPI, int NS, int TT>
+__device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
+  using S = FbStrip<NS, TT>;
+  constexpr bool GATED = fb_gated(EPI), EXACT = EPI == FB_F32;
+  constexpr int NO = GATED ? NS / 2 : NS;  // strips of results
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int strips = a.out / 16 / NS;
-  const int strip = blockIdx.x % strips;
-  const int64_t t0 = (int64_t)(blockIdx.x / strips) * (16 * TT);
+  const int width = GATED ? a.out / 2 : a.out;
+  const int groups = (width + 16 * NO - 1) / (16 * NO);
+  const int c0 = (int)(blockIdx.x % groups) * (16 * NO);
+  const int64_t t0 = (int64_t)(blockIdx.x / groups) * (16 * TT);
   const int rows = (int)min((int64_t)(16 * TT), a.T - t0);
 
   const GemmRsrc rw = gemm_rsrc(a.w, (uint32_t)a.out * (uint32_t)a.in);
-  const GemmRsrc rws = gemm_rsrc(a.ws, (uint32_t)(((a.out + 127) / 128) * a.nb) * 4u);
   const GemmRsrc rx = gemm_rsrc(a.x + t0 * a.in, (uint32_t)rows * (uint32_t)a.in);
   const GemmRsrc rxs = gemm_rsrc(a.xs + t0 * a.nb, (uint32_t)(rows * a.nb) * 4u);
-  uint32_t wo[NS], wso[NS], xo[TT], xso[TT];
+  // an instruction fills 8 rows: lane l writes position l % 8 of row l / 8, chunk
+  // (l % 8) ^ (row % 8), as in the tiles
+  const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
+  uint32_t ro[2 * (NS + TT)];
+  const float* ws[NS];
 #pragma unroll
-  for (int s = 0; s < NS; ++s) {
-    const int o = 16 * strip + s * (a.out / 2);
-    wo[s] = (uint32_t)(o + r) * (uint32_t)a.in + 16u * q;
-    wso[s] = (uint32_t)(o / 128) * (uint32_t)a.nb * 4u;
+  for (int j = 0; j < 2 * (NS + TT); ++j) {
+    const int k = 8 * j + (lane >> 3), t = k - 16 * NS;
+    if (j < 2 * NS) {
+      const int c = c0 + k % (16 * NO);
+      ro[j] = c < width ? (uint32_t)(c + k / (16 * NO) * width) * (uint32_t)a.in + chunk : FB_OOB;
+    } else {
+      ro[j] = t < rows ? (uint32_t)t * (uint32_t)a.in + chunk : FB_OOB;
+    }
   }
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int row = 16 * t + r;
-    xo[t] = row < rows ? (uint32_t)row * (uint32_t)a.in + 16u * q : FB_OOB;
-    xso[t] = row < rows ? (uint32_t)(row * a.nb) * 4u : FB_OOB;
-  }
+  for (int s = 0; s < NS; ++s)  // a strip past the last channel takes the last one's scale
+    ws[s] = a.ws + (int64_t)((min(c0 + 16 * (s % NO), width - 16) + s / NO * width) / 128) * a.nb;
+  const uint32_t xso = lane < rows ? (uint32_t)(lane * a.nb) * 4u : FB_OOB;
 
-  u32x4 wf[D][NS][2], xf[D][TT][2];
-  float ss[D][NS], sx[D][TT];
-  auto load = [&](int d, int kb) {
-    // chunks past the row's end (and blocks past the last) are read as zeros on both sides
-    const bool c0 = kb * 128 + 16 * q < a.in, c1 = kb * 128 + 64 + 16 * q < a.in;
-    const bool in = kb < a.nb;
+  auto load = [&](int d, int kb) {  // chunks past the row's end, blocks past the last: zeros
+    auto& st = sh.stage[w][d];
+    const bool in = 128 * kb + chunk < a.in;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      wf[d][s][0] = __builtin_amdgcn_raw_buffer_load_b128(rw, c0 ? wo[s] + 128u * kb : FB_OOB, 0, 0);
-      wf[d][s][1] = __builtin_amdgcn_raw_buffer_load_b128(rw, c1 ? wo[s] + 128u * kb + 64u : FB_OOB, 0, 0);
-      ss[d][s] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, in ? wso[s] + 4u * kb : FB_OOB, 0, 0));
-    }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const bool row = xo[t] != FB_OOB;
-      xf[d][t][0] = __builtin_amdgcn_raw_buffer_load_b128(rx, row && c0 ? xo[t] + 128u * kb : FB_OOB, 0, 0);
-      xf[d][t][1] = __builtin_amdgcn_raw_buffer_load_b128(rx, row && c1 ? xo[t] + 128u * kb + 64u : FB_OOB, 0, 0);
-      sx[d][t] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rxs, row && in ? xso[t] + 4u * kb : FB_OOB, 0, 0));
-    }
+    for (int j = 0; j < 2 * (NS + TT); ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 2 * NS ? rw : rx, (LdsPtr)(&st.rows[1024 * j]), 16,
+                                               in ? ro[j] : FB_OOB, 128u * kb, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&st.sx[0]), 4, kb < a.nb ? xso : FB_OOB,
+                                             4u * kb, 0, 0);
   };
 
   f32x4 acc[TT][NS];
@@ -78,59 +209,83 @@ __global__ __launch_bounds__(FS_THREADS) void fp8b128_strip_kernel(Fp8b128GemmAr
   for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int s = 0; s < NS; ++s) acc[t][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  const int at0 = 128 * r + 16 * (q ^ (r & 7)), at1 = 128 * r + 16 * ((4 + q) ^ (r & 7));
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(d, w + FS_WAVES * d);
-  for (int kb = w; kb < a.nb; kb += FS_WAVES * D) {
+  for (int d = 0; d < S::D - 1; ++d) load(d, w + S::W * d);
+  auto step = [&](int d, int kb) {
+    float ss[NS];
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (kb + FS_WAVES * d < a.nb) {
-        FbOperand<EXACT> wv[NS];
+    for (int s = 0; s < NS; ++s) ss[s] = fb_uniform_load(ws[s] + kb);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the refilled stage is outstanding
+    __builtin_amdgcn_sched_barrier(0);
+    load((d + S::D - 1) % S::D, kb + S::W * (S::D - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<S::LOADS * (S::D - 1)>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const auto& st = sh.stage[w][d];
+    FbOperand<EXACT> wv[NS];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) wv[s].set(wf[d][s][0], wf[d][s][1]);
+    for (int s = 0; s < NS; ++s)
+      wv[s].set(*reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at0),
+                *reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at1));
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          FbOperand<EXACT> xv;
-          xv.set(xf[d][t][0], xf[d][t][1]);
+    for (int t = 0; t < TT; ++t) {
+      FbOperand<EXACT> xv;
+      xv.set(*reinterpret_cast<const u32x4*>(st.rows + 2048 * (NS + t) + at0),
+             *reinterpret_cast<const u32x4*>(st.rows + 2048 * (NS + t) + at1));
+      const float sx = st.sx[16 * t + r];
 #pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            const f32x4 p = fb_block_product(wv[s], xv);
-            const float m = sx[d][t] * ss[d][s];
+      for (int s = 0; s < NS; ++s) {
+        const f32x4 p = fb_block_product(wv[s], xv);
+        const float m = sx * ss[s];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][s][i] = __builtin_fmaf(p[i], m, acc[t][s][i]);
-          }
-        }
+        for (int i = 0; i < 4; ++i) acc[t][s][i] = __builtin_fmaf(p[i], m, acc[t][s][i]);
       }
-      load(d, kb + FS_WAVES * (D + d));
     }
+  };
+  for (int kb = w; kb < a.nb; kb += S::W * S::D) {
+#pragma unroll
+    for (int d = 0; d < S::D; ++d)
+      if (kb + S::W * d < a.nb) step(d, kb + S::W * d);
   }
+  wait_vmcnt<0>();
+  __syncthreads();  // no load of this workgroup is writing its LDS, and no wave reads a stage
 #pragma unroll
   for (int t = 0; t < TT; ++t)
 #pragma unroll
-    for (int s = 0; s < NS; ++s) red[w][t * NS + s][lane] = acc[t][s];
+    for (int s = 0; s < NS; ++s) sh.red[w][t * NS + s][lane] = acc[t][s];
   __syncthreads();
-  const int t = threadIdx.x >> 6;  // wave t finishes token tile t
-  if (t < TT && 16 * t + r < rows) {
-    f32x4 sum[NS];
+  for (int v = w; v < TT * NO; v += S::W) {  // the tiles of results, one after the other
+    const int t = v / NO, s = v % NO;
+    f32x4 g = sh.red[0][t * NS + s][lane], u = sh.red[0][t * NS + s + NS - NO][lane];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      sum[s] = red[0][t * NS + s][lane];
-#pragma unroll
-      for (int v = 1; v < FS_WAVES; ++v) sum[s] += red[v][t * NS + s][lane];
+    for (int k = 1; k < S::W; ++k) {
+      g += sh.red[k][t * NS + s][lane];
+      u += sh.red[k][t * NS + s + NS - NO][lane];
     }
-    fb_store<EPI>(a, t0 + 16 * t + r, 16 * strip + 4 * q, sum[0], sum[NS - 1]);
+    const int o = c0 + 16 * s + 4 * q;
+    if (16 * t + r < rows && o < width) fb_store<EPI>(a, t0 + 16 * t + r, o, g, u);
   }
 }
 
-template <int EPI>
-hipError_t launch_strips(const Fp8b128GemmArgs& a, hipStream_t s) {
-  const int64_t strips = a.out / (fb_gated(EPI) ? 32 : 16);
-  const int tt = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
-  const unsigned grid = (unsigned)(strips * ((a.T + 16 * tt - 1) / (16 * tt)));
-  if (tt == 1)
-    return launch_timed(fp8b128_strip_kernel<EPI, 1>, dim3(grid), dim3(FS_THREADS), s, a);
-  if (tt == 2)
-    return launch_timed(fp8b128_strip_kernel<EPI, 2>, dim3(grid), dim3(FS_THREADS), s, a);
-  return launch_timed(fp8b128_strip_kernel<EPI, 4>, dim3(grid), dim3(FS_THREADS), s, a);
+template <int EPI, int NS, int TT>
+__global__ __launch_bounds__((64 * FbStrip<NS, TT>::W)) void fp8b128_strip_kernel(Fp8b128GemmArgs a) {
+  __shared__ FbStrip<NS, TT> sh;
+  fb_strip<EPI, NS, TT>(a, sh);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int EPI, int NS, int TT>
+int64_t strip_groups(const Fp8b128GemmArgs& a) {  // workgroups
+  constexpr int NO = fb_gated(EPI) ? NS / 2 : NS;
+  return ceil_div(fb_gated(EPI) ? a.out / 2 : a.out, 16 * NO) * ceil_div(a.T, 16 * TT);
+}
+template <int EPI, int NS, int TT>
+hipError_t launch_strip(const Fp8b128GemmArgs& a, hipStream_t s) {
+  return launch_timed(fp8b128_strip_kernel<EPI, NS, TT>, dim3((unsigned)strip_groups<EPI, NS, TT>(a)),
+                      dim3(64 * FbStrip<NS, TT>::W), s, a);
 }
 
 // ---- many tokens: tiles of both operands in LDS ----------------------------------------------
@@ -142,12 +297,12 @@ hipError_t launch_strips(const Fp8b128GemmArgs& a, hipStream_t s) {
 // straight to LDS (16-byte chunk c of row r at position c ^ (r % 8), so that eight lanes reading
 // one chunk of eight rows meet eight different banks' worth of LDS), in two stages with one
 // barrier per block.
-template <int SW, int WT>
+template <int SW, int WT, int ST>
 struct FbTile {
   static constexpr int WAVES = 2 * WT, THREADS = 64 * WAVES, BC = 32 * SW, BT = 64 * WT;
-  alignas(16) uint8_t w[2][BC * 128];
-  alignas(16) uint8_t x[2][BT * 128];
-  alignas(16) float sx[2][BT];
+  alignas(16) uint8_t w[ST][BC * 128];
+  alignas(16) uint8_t x[ST][BT * 128];
+  alignas(16) float sx[ST][BT];
 };
 
 // One workgroup per compute unit takes tile after tile: the first block of the next tile is
@@ -155,9 +310,9 @@ struct FbTile {
 //
 // SAME: the wave's strips (gated: its gate strips, and its up strips) lie in one block of 128
 // channels, so that a block of inputs has one scale for them.
-template <int EPI, int SW, int WT, bool SAME>
-__device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, int tc) {
-  using S = FbTile<SW, WT>;
+template <int EPI, int SW, int WT, int ST, bool SAME>
+__device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT, ST>& sh, int tt, int tc) {
+  using S = FbTile<SW, WT, ST>;
   constexpr bool GATED = fb_gated(EPI), EXACT = EPI == FB_F32;
   constexpr int NX = S::BT / S::WAVES / 8, NW = S::BC / S::WAVES / 8;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -165,7 +320,6 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
   const int wc = w & 1, wt = w >> 1;
   const int half = a.out / 2, width = GATED ? half : a.out;
   const GemmRsrc rw = gemm_rsrc(a.w, (uint32_t)a.out * (uint32_t)a.in);
-  const GemmRsrc rws = gemm_rsrc(a.ws, (uint32_t)(((a.out + 127) / 128) * a.nb) * 4u);
   // an instruction fills 8 rows: lane l writes position l % 8 of row l / 8
   const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
   // the wave's strip s is tile rows strip_row(s) ..
@@ -177,7 +331,10 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
   // the tile: its first token, tokens, first channel (gated: of either half), load offsets
   int64_t t0;
   int rows, c0;
-  uint32_t wo[NW], xo[NX], xso, wso;
+  uint32_t wo[NW], xo[NX], xso;
+  // the scales of the wave's strips: one for each, or (SAME) for each half, block by block
+  constexpr int NG = !SAME ? SW : GATED ? 2 : 1, PER_GROUP = SW / NG;
+  const float* ws[NG];
   auto set_tile = [&](int tile_t, int tile_c) {
     const int lane = fb_fresh_lane(), chunk = 16 * ((lane & 7) ^ (lane >> 3));
     t0 = (int64_t)tile_t * S::BT;
@@ -200,32 +357,37 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
       xo[j] = k < rows ? (uint32_t)k * (uint32_t)a.in + chunk : FB_OOB;
     }
     xso = 64 * w + lane < rows ? (uint32_t)((64 * w + lane) * a.nb) * 4u : FB_OOB;
-    const int k = strip_row(lane % SW);  // lane s loads strip s's scale
-    wso = valid(k) ? (uint32_t)(channel(k) / 128 * a.nb) * 4u : FB_OOB;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {  // a strip past the last channel takes a scale that exists
+      const int k = strip_row(g * PER_GROUP);
+      ws[g] = a.ws + (int64_t)((valid(k) ? channel(k) : 0) / 128) * a.nb;
+    }
   };
 
   // The loads of one block, in LOADS parts: a wave cannot go on while the memory unit's queue is
   // full, so they are issued a few at a time between the products.
-  constexpr int LOADS = 1 + NW + NX, PER = SW == 8 ? 2 : 3;
-  float sw_after = 0.0f;  // the wave's weight scales of the block, strip s in lane s
+  constexpr int LOADS = NW + NX, PER = (LOADS + SW - 2) / (SW - 1);
   auto load = [&](int n, int st, int kb) {
     const bool in = 128 * kb + chunk < a.in;  // chunks past the row's end are zeros
-    if (n == 0) {
-      sw_after = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, kb < a.nb ? wso : FB_OOB, 4u * kb, 0));
-      const GemmRsrc rxs = gemm_rsrc(a.xs + t0 * a.nb, (uint32_t)(rows * a.nb) * 4u);
-      if (w < WT)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&sh.sx[st][64 * w]), 4,
-                                                 kb < a.nb ? xso : FB_OOB, 4u * kb, 0, 0);
-    } else if (n <= NW) {
-      const int j = n - 1;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][1024 * (NW * w + j)]), 16,
-                                               in ? wo[j] : FB_OOB, 128u * kb, 0, 0);
+    if (n < NW) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][1024 * (NW * w + n)]), 16,
+                                               in ? wo[n] : FB_OOB, 128u * kb, 0, 0);
     } else if (n < LOADS) {
-      const int j = n - 1 - NW;
       const GemmRsrc rx = gemm_rsrc(a.x + t0 * a.in, (uint32_t)rows * (uint32_t)a.in);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(&sh.x[st][1024 * (NX * w + j)]), 16,
-                                               in ? xo[j] : FB_OOB, 128u * kb, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(&sh.x[st][1024 * (NX * w + n - NW)]), 16,
+                                               in ? xo[n - NW] : FB_OOB, 128u * kb, 0, 0);
     }
+    if (n == 0 && w < WT) {
+      const GemmRsrc rxs = gemm_rsrc(a.xs + t0 * a.nb, (uint32_t)(rows * a.nb) * 4u);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&sh.sx[st][64 * w]), 4,
+                                               kb < a.nb ? xso : FB_OOB, 4u * kb, 0, 0);
+    }
+  };
+  auto load_blocks = [&](int first, int last) {
+#pragma unroll
+    for (int kb = first; kb < last; ++kb)
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n) load(n, kb, kb);
   };
 
   f32x4 acc[SW][4], p[4];
@@ -250,17 +412,17 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
     asm volatile("" : "+v"(acc[s][t]));  // done here, not where the compiler would gather them
   };
 
-  // The results leave through LDS (the second stage: its refill waits for the barrier after), 32
+  // The results leave through LDS (the last stage: its refill waits for the barrier after), 32
   // (fp32: 16) tokens of the wave at a time: stored straight from registers, by 32 bytes of 16 rows an
   // instruction, the bf16 tile took 30,000 cycles beside the 114,000 of its products at 5,120
   // inputs.
   constexpr int NO = GATED ? SW / 2 : SW, ESIZE = EPI == FB_F32 ? 4 : 2, ROW = 16 * NO * ESIZE;
   constexpr int N = EPI == FB_F32 ? 16 : 32;
-  static_assert(N * ROW * S::WAVES <= sizeof(sh.w[1]) + sizeof(sh.x[1]), "results' way out");
+  static_assert(N * ROW * S::WAVES <= sizeof(sh.w[0]) + sizeof(sh.x[0]), "results' way out");
   auto store_results = [&](int64_t token, int tokens, int channel0) {
     const int lane = fb_fresh_lane(), r = lane & 15, q = lane >> 4;
-    constexpr int IN_W = sizeof(sh.w[1]) / (N * ROW);  // waves whose rows fit the weights' part
-    FbRows<ROW, N> out{w < IN_W ? sh.w[1] + w * (N * ROW) : sh.x[1] + (w - IN_W) * (N * ROW)};
+    constexpr int IN_W = sizeof(sh.w[0]) / (N * ROW);  // waves whose rows fit the weights' part
+    FbRows<ROW, N> out{w < IN_W ? sh.w[ST - 1] + w * (N * ROW) : sh.x[ST - 1] + (w - IN_W) * (N * ROW)};
     const int bytes = min(16 * NO, width - channel0) * ESIZE;
     const int64_t stride = (int64_t)(EPI == FB_GATED ? half : a.out) * ESIZE;
 #pragma unroll
@@ -301,8 +463,7 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
   int tile_t, tile_c, j = blockIdx.x >> 3;
   if (!fb_tile_of(tt, tc, j, &tile_t, &tile_c)) return;
   set_tile(tile_t, tile_c);
-#pragma unroll
-  for (int n = 0; n < LOADS; ++n) load(n, 0, 0);
+  load_blocks(0, ST - 1);
   for (bool more = true; more;) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -311,10 +472,11 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
       p[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
       m[t] = 0.0f;
     }
-    float sw = sw_after;
 #pragma unroll
-    for (int n = 0; n < PER; ++n) load(n, 1, 1);
-    wait_vmcnt<PER - 1>();  // part 0 may have no load that writes LDS, and no other is counted on
+    for (int n = 0; n < PER; ++n) load(n, ST - 1, ST - 1);
+    // block 0 has landed: later blocks' loads (the token scales' not counted: not every wave has
+    // one) may be in flight
+    wait_vmcnt<(ST - 2) * LOADS + PER>();
     bare_barrier();
     read_a(0, 0);
 #pragma unroll
@@ -322,41 +484,47 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
       read_b(0, t);
       read_sx(0, t);
     }
+    float ss[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) ss[g] = fb_uniform_load(ws[g]);
     // One block. Before its last strip, whose operands are in registers, the next block has
     // landed everywhere and this stage is no longer read: its refill starts, and the next block's
     // operands are read as the last strip's products release the registers.
+    int st = 0;
     for (int kb = 0; kb < a.nb; ++kb) {
-      const int st = kb & 1;
-      float sw_next = 0.0f;
+      const int next = st + 1 == ST ? 0 : st + 1, before = st == 0 ? ST - 1 : st - 1;
+      float sn[NG];
 #pragma unroll
       for (int s = 0; s < SW; ++s) {
         const bool last = s == SW - 1;
         __builtin_amdgcn_sched_barrier(0);
         if (last) {
-          wait_vmcnt<0>();
+          wait_vmcnt<(ST - 2) * LOADS>();
           bare_barrier();
-          read_a(st ^ 1, 0);
+          read_a(next, 0);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) sn[g] = fb_uniform_load(ws[g] + min(kb + 1, a.nb - 1));
         } else {
           read_a(st, s + 1);
         }
-        if (last) sw_next = sw_after;
 #pragma unroll
         for (int n = 0; n < PER; ++n)
-          load(n + (last ? 0 : PER * (s + 1)), last ? st : st ^ 1, kb + (last ? 2 : 1));
-        const float ss = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw), s));
+          load(n + (last ? 0 : PER * (s + 1)), last ? st : before, kb + (last ? ST : ST - 1));
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           add((s + SW - 1) % SW, t);
           p[t] = fb_block_product(av[s & 1], bv[t]);
-          if (!SAME || s % (GATED ? SW / 2 : SW) == 0) m[t] = sx[t] * ss;
+          if (s % PER_GROUP == 0) m[t] = sx[t] * ss[s / PER_GROUP];
           if (last) {
             __builtin_amdgcn_sched_barrier(0);
-            read_b(st ^ 1, t);
-            read_sx(st ^ 1, t);
+            read_b(next, t);
+            read_sx(next, t);
           }
         }
       }
-      sw = sw_next;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) ss[g] = sn[g];
+      st = next;
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) add(SW - 1, t);
@@ -369,8 +537,7 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
     more = fb_tile_of(tt, tc, j, &tile_t, &tile_c);
     if (more) {
       set_tile(tile_t, tile_c);
-#pragma unroll
-      for (int n = 0; n < LOADS; ++n) load(n, 0, 0);
+      load_blocks(0, ST - 1);
     }
     store_results(first_token, tokens, channel0);
     bare_barrier();
@@ -378,37 +545,69 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT>& sh, int tt, i
   wait_vmcnt<0>();  // no load may still be writing this workgroup's LDS when it ends
 }
 
-template <int EPI, int SW, int WT, bool SAME>
+template <int EPI, int SW, int WT, int ST, bool SAME>
 __global__ __launch_bounds__(128 * WT) void fp8b128_tile_kernel(Fp8b128GemmArgs a, int tt, int tc) {
-  __shared__ FbTile<SW, WT> sh;
-  fb_tiles<EPI, SW, WT, SAME>(a, sh, tt, tc);
+  __shared__ FbTile<SW, WT, ST> sh;
+  fb_tiles<EPI, SW, WT, ST, SAME>(a, sh, tt, tc);
 }
 
-template <int EPI, int SW, int WT>
+template <int EPI, int SW, int WT, int ST>
+struct FbTiles {
+  using S = FbTile<SW, WT, ST>;
+  int tt, tc;  // tiles of tokens and of channels
+  explicit FbTiles(const Fp8b128GemmArgs& a)
+      : tt((int)ceil_div(a.T, S::BT)), tc((int)ceil_div(a.out, S::BC)) {}
+  int64_t rounds() const { return ceil_div((int64_t)tt * tc, FB_CUS); }  // over the compute units
+};
+
+template <int EPI, int SW, int WT, int ST>
 hipError_t launch_tiles(const Fp8b128GemmArgs& a, hipStream_t s) {
-  using S = FbTile<SW, WT>;
-  const int width = fb_gated(EPI) ? a.out / 2 : a.out, bc = fb_gated(EPI) ? S::BC / 2 : S::BC;
-  const int tt = (int)((a.T + S::BT - 1) / S::BT), tc = (width + bc - 1) / bc;
-  // two workgroups of the smaller tile share a compute unit
-  const dim3 grid((unsigned)std::min((tt * tc + 7) & ~7, S::WAVES == 4 ? 2 * FB_CUS : FB_CUS));
-  const dim3 block(S::THREADS);
-  // tiles start at multiples of 64 channels, the up half at channel I = width
-  if (!fb_gated(EPI) || width % 64 == 0)
-    return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, true>, grid, block, s, a, tt, tc);
-  return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, !fb_gated(EPI)>, grid, block, s, a, tt, tc);
+  using S = FbTile<SW, WT, ST>;
+  const FbTiles<EPI, SW, WT, ST> n(a);
+  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)n.tt * n.tc + 7) & ~7, FB_CUS));
+  // tiles start at multiples of 64 channels, the up half at channel I = out / 2
+  if (!fb_gated(EPI) || a.out % 128 == 0)
+    return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, ST, true>, grid, dim3(S::THREADS), s, a, n.tt, n.tc);
+  return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, ST, !fb_gated(EPI)>, grid, dim3(S::THREADS), s, a,
+                      n.tt, n.tc);
 }
 
+// The kernel with the least time expected, by the rounds of workgroups over the compute units and
+// what a round took at 5,120 inputs (0.1 us, bf16 results / fp32 results; a round's time is close
+// to proportional to the inputs):
+//   strips of (NS, TT)   18 / 22 times NS + TT: 5.5 us with (1, 1), 7.2 with (2, 2), 11.2 with
+//                        (4, 2), 14.3 / 18 with (4, 4)
+//   128 x 128 tiles      380 / 540 (for one round: two were never the least)
+//   128 x 256 tiles      470 / 770
+//   256 x 256 tiles      750 (bf16 results only)
+// Measured where two meet: 512 tokens x 1,536 channels 15.9 us by (4, 4) strips, 37.8 by 128 x 128
+// tiles; 512 x 5,120 41.8 and 38.8; 2,048 x 5,120 84.7 by 128 x 128, 69.2 by 256 x 256 tiles;
+// 4,096 x 5,120 125 by 128 x 256, 131 by 256 x 256 tiles; 8,192 x 5,120 230 and 212.
 template <int EPI>
 hipError_t launch_forward(const Fp8b128GemmArgs& a, hipStream_t s) {
-  // By the number of 256 x 256 tiles: from half the compute units on they are the fastest
-  // (8,192 x 5,120 x 7,168: 359 us, against 439 us with 128 x 128); below it smaller tiles
-  // spread the work wider (1,024 x 5,120 x 5,120, 80 tiles: 61 against 80 us; 512 x 5,120 x
-  // 1,536: 46 against 79 us), and up to 256 tokens strips wider still (128 x 5,120 x 1,536: 23
-  // against 46 us).
-  const int64_t big = (a.T + 255) / 256 * ((a.out + 255) / 256);
-  if (big >= 128) return launch_tiles<EPI, EPI == FB_F32 ? 4 : 8, 4>(a, s);
-  if (a.T > 256) return launch_tiles<EPI, 4, 2>(a, s);
-  return launch_strips<EPI>(a, s);
+  constexpr bool EXACT = EPI == FB_F32;
+  if (a.T <= 2) return launch_rows<EPI>(a, s);
+  typedef hipError_t (*Launch)(const Fp8b128GemmArgs&, hipStream_t);
+  int64_t least = INT64_MAX;
+  Launch best = nullptr;
+  auto offer = [&](int64_t cost, Launch f) {
+    if (cost < least) {
+      least = cost;
+      best = f;
+    }
+  };
+  constexpr int U = EXACT ? 22 : 18;
+  if constexpr (!fb_gated(EPI))
+    offer(2 * U * ceil_div(strip_groups<EPI, 1, 1>(a), FB_CUS), launch_strip<EPI, 1, 1>);
+  offer(3 * U * ceil_div(strip_groups<EPI, 2, 1>(a), FB_CUS), launch_strip<EPI, 2, 1>);
+  offer(4 * U * ceil_div(strip_groups<EPI, 2, 2>(a), FB_CUS), launch_strip<EPI, 2, 2>);
+  offer(6 * U * ceil_div(strip_groups<EPI, 4, 2>(a), FB_CUS), launch_strip<EPI, 4, 2>);
+  offer(8 * U * ceil_div(strip_groups<EPI, 4, 4>(a), FB_CUS), launch_strip<EPI, 4, 4>);
+  if (FbTiles<EPI, 4, 2, 2>(a).rounds() == 1) offer(EXACT ? 540 : 380, launch_tiles<EPI, 4, 2, 2>);
+  offer(FbTiles<EPI, 4, 4, 3>(a).rounds() * (EXACT ? 770 : 470), launch_tiles<EPI, 4, 4, 3>);
+  if constexpr (!EXACT)
+    offer(FbTiles<EPI, 8, 4, 2>(a).rounds() * 750, launch_tiles<EPI, 8, 4, 2>);
+  return best(a, s);
 }
 
 }  // namespace

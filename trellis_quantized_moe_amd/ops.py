@@ -350,8 +350,8 @@ def _check_rows(name, t, dtypes, device=None, shape=None):
         raise ValueError("%s must be a contiguous 2-D tensor" % name)
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, not %s" % (name, t.device, device))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), shape))
 
 
 def _call_on(device, fn, *args):
