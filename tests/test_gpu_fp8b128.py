@@ -264,6 +264,30 @@ def test_gated_backward(T, out, inp):
     check_guards(ww, 3.0)
 
 
+@pytest.mark.parametrize("T", [3, 90])
+def test_gradients_of_special_scales(T):
+    # a block the quantizer could not represent (scale NaN, zero codes) makes its inputs' columns
+    # of dw NaN; zero, tiny, huge and negative scales are values like others
+    c = Inputs(989, T, 96, 400)
+    xs, codes = c.scales.copy(), c.codes.copy()
+    xs[1, 2], codes[1, 256:384] = np.nan, 0
+    xs[0, 0], xs[2, 0], xs[2, 1] = 0.0, -xs[2, 0], -2.0 ** -3
+    xs[0, 1], xs[0, 3] = 2.0 ** -120, 2.0 ** 30
+    codes[0, 384:] = 0x38
+    X = oracle.fp8b128_activations(codes, xs)
+    db = grads_of(T, 96, 96)
+    D = oracle.bf16_bits_to_f64(db)
+    dx, dw = ops().fp8b128_gemm_backward(c.layer, to_dev(codes), to_dev(xs), bf16_dev(db))
+    assert torch.isfinite(dx.float()).all()
+    got = f64_of(dw)
+    assert np.isnan(got[:, 256:384]).all()
+    keep = np.r_[0:256, 384:400]
+    mag = np.abs(D).T @ np.abs(X[:, keep])
+    ref = D.T @ X[:, keep]
+    # one scale is no power of two (the negative ones among them): X rounded to bf16
+    assert_within(got[:, keep], ref, BF16 * (np.abs(ref) + mag) + (BF16 + 100 * F32) * mag)
+
+
 def test_backward_needs():
     c = Inputs(979, 50, 96, 272)
     dh = bf16_dev(grads_of(50, 96, 48))

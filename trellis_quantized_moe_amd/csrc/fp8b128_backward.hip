@@ -34,127 +34,157 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
   *reinterpret_cast<u32x2*>(p) = (u32x2){fb_pack_bf16(v[0], v[1]), fb_pack_bf16(v[2], v[3])};
 }
 
-// ---- dx, few tokens: 32 inputs of up to 16 * TT tokens per workgroup ------------------------
+// ---- dx, few tokens: strips of inputs, the outputs split over a workgroup's waves ------------
 //
-// The eight waves take the blocks of 128 outputs in turn, each with LDS of its own (no barrier
-// until the end), one block ahead: the block's 128 x 32 codes straight to LDS, the tokens' dy
-// to registers in operand order. A block's sums are scaled by its weight scale; the waves'
-// sums are added in wave order.
-constexpr int DS_WAVES = 8;
-constexpr int DS_THREADS = 64 * DS_WAVES;
-
-template <int TT>
-struct DxStripShared {
-  alignas(16) uint8_t w[DS_WAVES][2][128 * 32];
-  f32x4 red[DS_WAVES][TT * 2][64];
+// A workgroup owns NS strips of 16 inputs (64 bytes of a row of codes) of up to 16 * TT tokens. Its W waves take the blocks of 128 outputs in turn, in two steps of 64, each
+// with D stages of LDS of its own that its loads fill D - 1 steps ahead (no barrier until the
+// end). A block's products are added from zero and then scaled into the sums; the waves' sums
+// are added in wave order.
+template <int NS, int TT>
+struct DxStrip {
+  static constexpr int IW = 16 * NS, W = TT <= 2 ? 8 : 4, D = TT <= 2 ? 2 : 3;
+  static constexpr int LOADS = NS + 2 * TT;  // per step, of 1024 bytes
+  union {
+    struct {
+      alignas(16) uint8_t w[64 * IW];
+      alignas(16) uint8_t d[16 * TT * 128];
+    } stage[W][D];
+    f32x4 red[W][TT * NS][64];
+  };
 };
 
-template <int TT>
-__device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStripShared<TT>& sh) {
+template <int NS, int TT>
+__device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStrip<NS, TT>& sh) {
+  using S = DxStrip<NS, TT>;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int cols = (a.in + 31) / 32;
-  const int i0 = (int)(blockIdx.x % cols) * 32;
+  const int cols = (a.in + S::IW - 1) / S::IW;
+  const int i0 = (int)(blockIdx.x % cols) * S::IW;
   const int64_t t0 = (int64_t)(blockIdx.x / cols) * (16 * TT);
   const int rows = (int)min((int64_t)(16 * TT), a.T - t0);
   const int nob = (a.out + 127) / 128;
-
   const GemmRsrc rd = gemm_rsrc(a.dy + t0 * a.out, (uint32_t)rows * (uint32_t)a.out * 2u);
-  const GemmRsrc rs = gemm_rsrc(a.ws, (uint32_t)(nob * a.nb) * 4u);
-  // codes: instruction j fills rows 32 j .. + 31; lane l half l % 2 of row l / 2, which holds
-  // the row's half (l % 2) ^ (row / 4 % 2), so that a transpose read's eight rows meet
-  // different banks
-  const int wrow = lane >> 1, wcol = 16 * ((lane & 1) ^ ((wrow >> 2) & 1));
-  const uint32_t wo = i0 + wcol < a.in ? (uint32_t)wrow * (uint32_t)a.in + i0 + wcol : FB_OOB;
-  uint32_t dof[TT];
+  const float* ws = a.ws + i0 / 128;
+  // codes: an instruction fills 64 / NS rows; lane l position l % NS of row l / NS, which holds the
+  // row's 16-byte chunk (l % NS) ^ swizzle(row): the LDS serves 32 lanes at a time, which read one
+  // chunk of 16 rows, and those get 16 different sixteenths of the 256 bytes that it serves
+  auto swizzle = [&](int row) { return row / (16 / NS) & (NS - 1); };
+  uint32_t wo[NS], dof[2 * TT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
-    dof[t] = 16 * t + r < rows ? (uint32_t)(16 * t + r) * (uint32_t)a.out * 2u + 16u * q : FB_OOB;
-
-  // Loads of one block that the waits count: the compiler could move the scale's across a wait,
-  // so it is not one of them.
-  constexpr int LOADS = 4 + 4 * TT;
-  u32x4 d[2][TT][4];
-  float sc[2];
-  auto load = [&](int k, int ob) {  // blocks past the last are read as zeros
-    const int left = min(128, a.out - 128 * ob);
-    const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 128 * ob : 0) * a.in,
+  for (int j = 0; j < NS; ++j) {
+    const int row = j * (64 / NS) + lane / NS, col = i0 + 16 * ((lane & (NS - 1)) ^ swizzle(row));
+    wo[j] = col < a.in ? (uint32_t)row * (uint32_t)a.in + col : FB_OOB;
+  }
+  // dy: 8 rows; position l % 8 of row l / 8 holds chunk (l % 8) ^ (row % 8)
+  const int dcol = 8 * ((lane & 7) ^ (lane >> 3));  // this lane's first output of a step
+#pragma unroll
+  for (int j = 0; j < 2 * TT; ++j) {
+    const int tok = 8 * j + (lane >> 3);
+    dof[j] = tok < rows ? ((uint32_t)tok * (uint32_t)a.out + dcol) * 2u : FB_OOB;
+  }
+  auto load = [&](int d, int k) {  // the outputs 64 k ..; steps past the last are read as zeros
+    auto& st = sh.stage[w][d];
+    const int left = min(64, a.out - 64 * k);
+    const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 64 * k : 0) * a.in,
                                   left > 0 ? (uint32_t)left * (uint32_t)a.in : 0u);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[w][k][1024 * j]), 16,
-                                               wo == FB_OOB ? FB_OOB : wo + 32u * j * (uint32_t)a.in,
-                                               0, 0, 0);
+    for (int j = 0; j < NS; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&st.w[1024 * j]), 16, wo[j], 0, 0, 0);
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = 128 * ob + 32 * j + 8 * q < a.out && dof[t] != FB_OOB;
-        d[k][t][j] = __builtin_amdgcn_raw_buffer_load_b128(rd, in ? dof[t] + 256u * ob + 64u * j : FB_OOB, 0, 0);
-      }
-    sc[k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-        rs, ob < nob ? (uint32_t)(ob * a.nb + i0 / 128) * 4u : FB_OOB, 0, 0));
+    for (int j = 0; j < 2 * TT; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&st.d[1024 * j]), 16,
+                                               dcol < left ? dof[j] : FB_OOB, 128u * k, 0, 0);
   };
-  f32x4 acc[TT][2];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) acc[t][0] = acc[t][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  // lane (j = l % 16, q) of a transpose read: row 8 q + j / 2, half j % 2 of 16-byte column c
-  auto compute = [&](int k) {
-    f32x4 p[TT][2];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) p[t][0] = p[t][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int row = 32 * j + 8 * q + (r >> 1);
-        const u32x2 v = read_tr8(&sh.w[w][k][32 * row + 16 * (c ^ ((row >> 2) & 1)) + 8 * (r & 1)]);
-        const u32x4 av = fb_bf16_of8(v.x, v.y);
-#pragma unroll
-        for (int t = 0; t < TT; ++t) p[t][c] = mfma_bf16(av, d[k][t][j], p[t][c]);
-      }
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][c][i] = __builtin_fmaf(p[t][c][i], sc[k], acc[t][c][i]);
-  };
-  // one step: the next block's loads, then this block's data (all but those loads have landed)
-  auto step = [&](int k, int ob) {
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the stage is outstanding
-    __builtin_amdgcn_sched_barrier(0);
-    load(k ^ 1, ob + DS_WAVES);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<LOADS>();
-    __builtin_amdgcn_sched_barrier(0);
-    compute(k);
-  };
-  load(0, w);
-  for (int ob = w; ob < nob; ob += 2 * DS_WAVES) {
-    step(0, ob);
-    if (ob + DS_WAVES < nob) step(1, ob + DS_WAVES);
-  }
-  wait_vmcnt<0>();  // no load may still be writing this workgroup's LDS when it ends
+  // step n of this wave: half n % 2 of its block n / 2
+  auto outputs = [&](int n) { return 2 * (w + S::W * (n >> 1)) + (n & 1); };
+
+  f32x4 acc[TT][NS], p[TT][NS];
 #pragma unroll
   for (int t = 0; t < TT; ++t)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) sh.red[w][2 * t + c][lane] = acc[t][c];
+    for (int c = 0; c < NS; ++c) acc[t][c] = p[t][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < S::D - 1; ++n) load(n, outputs(n));
+  auto step = [&](int d, int n, bool second) {
+    float s = 0.0f;
+    if (second) s = fb_uniform_load(ws + (int64_t)(w + S::W * (n >> 1)) * a.nb);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the refilled stage is outstanding
+    __builtin_amdgcn_sched_barrier(0);
+    load((d + S::D - 1) % S::D, outputs(n + S::D - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<S::LOADS * (S::D - 1)>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const auto& st = sh.stage[w][d];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x4 b[TT];
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        b[t] = *reinterpret_cast<const u32x4*>(&st.d[128 * (16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
+#pragma unroll
+      for (int c = 0; c < NS; ++c) {
+        const int row = 32 * j + 8 * q + (r >> 1);
+        const u32x2 v = read_tr8(&st.w[S::IW * row + 16 * (c ^ swizzle(row)) + 8 * (r & 1)]);
+        const u32x4 av = fb_bf16_of8(v.x, v.y);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) p[t][c] = mfma_bf16(av, b[t], p[t][c]);
+      }
+    }
+    if (second) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int c = 0; c < NS; ++c) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][c][i] = __builtin_fmaf(p[t][c][i], s, acc[t][c][i]);
+          p[t][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        }
+    }
+  };
+  const int steps = w < nob ? 2 * ((nob - w + S::W - 1) / S::W) : 0;
+  constexpr int U = S::D == 2 ? 2 : 6;  // steps after which stage and half repeat
+  for (int n = 0; n < steps; n += U) {
+#pragma unroll
+    for (int u = 0; u < U; u += 2)
+      if (n + u < steps) {
+        step(u % S::D, n + u, false);
+        step((u + 1) % S::D, n + u + 1, true);
+      }
+  }
+  wait_vmcnt<0>();
+  __syncthreads();  // no load of this workgroup is writing its LDS, and no wave reads a stage
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int c = 0; c < NS; ++c) sh.red[w][NS * t + c][lane] = acc[t][c];
   __syncthreads();
-  const int v = threadIdx.x >> 6;  // wave v finishes tile v
-  if (v < 2 * TT) {
+  for (int v = w; v < NS * TT; v += S::W) {  // the tiles of results, one after the other
     f32x4 sum = sh.red[0][v][lane];
 #pragma unroll
-    for (int u = 1; u < DS_WAVES; ++u) sum += sh.red[u][v][lane];
-    const int row = 16 * (v >> 1) + r, i = i0 + 16 * (v & 1) + 4 * q;
+    for (int u = 1; u < S::W; ++u) sum += sh.red[u][v][lane];
+    const int row = 16 * (v / NS) + r, i = i0 + 16 * (v % NS) + 4 * q;
     if (row < rows && i < a.in) store4(a.dx + (t0 + row) * a.in + i, sum);
   }
 }
 
-template <int TT>
-__global__ __launch_bounds__(DS_THREADS) void fp8b128_dx_strip_kernel(Fp8b128BackwardArgs a) {
-  __shared__ DxStripShared<TT> sh;
-  dx_strip<TT>(a, sh);
+template <int NS, int TT>
+__global__ __launch_bounds__((64 * DxStrip<NS, TT>::W)) void fp8b128_dx_strip_kernel(Fp8b128BackwardArgs a) {
+  __shared__ DxStrip<NS, TT> sh;
+  dx_strip<NS, TT>(a, sh);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int NS, int TT>
+int64_t dx_strip_groups(const Fp8b128BackwardArgs& a) {  // workgroups
+  return ceil_div(a.in, 16 * NS) * ceil_div(a.T, 16 * TT);
+}
+template <int NS, int TT>
+hipError_t launch_dx_strip(const Fp8b128BackwardArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((fp8b128_dx_strip_kernel<NS, TT>), dim3((unsigned)dx_strip_groups<NS, TT>(a)),
+                     dim3(64 * DxStrip<NS, TT>::W), 0, s, a);
+  return hipGetLastError();
 }
 
 // The 64 x 64 results of each wave of a tile (row 16 t + lane % 16, inputs 16 c + 4 (lane / 16) ..
@@ -487,21 +517,23 @@ __global__ __launch_bounds__(512) void fp8b128_dw_kernel(Fp8b128BackwardArgs a, 
 
 }  // namespace
 
+// The kernel with the least time expected, by the rounds of workgroups over the compute units and
+// what a round took at 1,536 outputs (0.1 us): strips of (4, 1) 31, (4, 2) 41, (4, 4) 70, tiles 230.
+// Measured where two meet, for 5,120 inputs: 32 tokens 5.8 us by (4, 1), 6.3 by (4, 2); 128 tokens
+// 10.7 by (4, 2), 9.8 by (4, 4); 512 tokens 23.9 by (4, 4), 26.8 by tiles; 768 tokens 31.0 and
+// 28.2. (768 inputs x 5,120 outputs, 333 tokens: 13.2 by (4, 1), 67 by tiles.)
 hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s) {
-  // strips spread few tokens wider; tiles move less data once they fill half the GPU
-  const int64_t tiles = (a.T + 127) / 128 * ((a.in + 255) / 256);
-  if (tiles >= 128) {
-    const int tt = (int)((a.T + 127) / 128), ti = (a.in + 255) / 256;
-    hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)std::min((tt * ti + 7) & ~7, FB_CUS)), dim3(512), 0,
-                       s, a, tt, ti);
-    return hipGetLastError();
-  }
-  const int tt = a.T <= 16 ? 1 : 2;
-  const unsigned grid = (unsigned)((a.in + 31) / 32 * ((a.T + 16 * tt - 1) / (16 * tt)));
-  if (tt == 1)
-    hipLaunchKernelGGL(fp8b128_dx_strip_kernel<1>, dim3(grid), dim3(DS_THREADS), 0, s, a);
-  else
-    hipLaunchKernelGGL(fp8b128_dx_strip_kernel<2>, dim3(grid), dim3(DS_THREADS), 0, s, a);
+  const int64_t tt = ceil_div(a.T, 128), ti = ceil_div(a.in, 256);
+  const int64_t s1 = 31 * ceil_div(dx_strip_groups<4, 1>(a), FB_CUS);
+  const int64_t s2 = 41 * ceil_div(dx_strip_groups<4, 2>(a), FB_CUS);
+  const int64_t s4 = 70 * ceil_div(dx_strip_groups<4, 4>(a), FB_CUS);
+  const int64_t tiles = 230 * ceil_div(tt * ti, FB_CUS);
+  const int64_t least = std::min(std::min(s1, s2), std::min(s4, tiles));
+  if (least == s1) return launch_dx_strip<4, 1>(a, s);
+  if (least == s2) return launch_dx_strip<4, 2>(a, s);
+  if (least == s4) return launch_dx_strip<4, 4>(a, s);
+  hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)std::min<int64_t>((tt * ti + 7) & ~7, FB_CUS)),
+                     dim3(512), 0, s, a, (int)tt, (int)ti);
   return hipGetLastError();
 }
 
