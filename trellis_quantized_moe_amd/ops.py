@@ -311,7 +311,7 @@ def mxfp4_to_nvfp4(layer, codes=None, scales=None, scale2=None, status=None):
     return codes, scales, scale2, status
 
 
-@dataclass
+@dataclass(frozen=True)
 class Fp8b128Layer:
     """A dense projection in the fp8b128 store (see tq_fp8b128_layer in include/tq.h)."""
     codes: torch.Tensor      # uint8 or float8_e4m3fn [out, in]
@@ -319,11 +319,12 @@ class Fp8b128Layer:
 
     def __post_init__(self):
         _check_rows("codes", self.codes, _E4M3)
-        self.out, self.in_ = self.codes.shape
-        _check_rows("scales", self.scales, _F32, self.codes.device,
-                    (-(-self.out // 128), -(-self.in_ // 128)))
-        self._c = _lib.Fp8b128LayerC(self.out, self.in_, self.codes.data_ptr(),
-                                     self.scales.data_ptr())
+        out, in_ = self.codes.shape
+        dev = self.codes.device
+        _check_rows("scales", self.scales, _F32, dev, (-(-out // 128), -(-in_ // 128)))
+        # made once: the fields cannot be assigned again
+        c = _lib.Fp8b128LayerC(out, in_, self.codes.data_ptr(), self.scales.data_ptr())
+        self.__dict__.update(out=out, in_=in_, device=dev, _c=c, _ref=ctypes.byref(c))
 
     @classmethod
     def from_host(cls, layer, device="cuda"):
@@ -342,6 +343,10 @@ _F32 = (torch.float32,)
 def _check_rows(name, t, dtypes, device=None, shape=None):
     """The kernels read raw pointers: a tensor has to be on the GPU, contiguous, of one of
     `dtypes` and, where they are given, on `device` and of `shape`."""
+    if (t.dtype in dtypes and t.is_cuda and t.is_contiguous()
+            and (device is None or t.device == device)
+            and (t.dim() == 2 if shape is None else t.shape == shape)):
+        return
     if not t.is_cuda:
         raise ValueError("tensors must be on the GPU")
     if t.dtype not in dtypes:
@@ -350,20 +355,22 @@ def _check_rows(name, t, dtypes, device=None, shape=None):
         raise ValueError("%s must be a contiguous 2-D tensor" % name)
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, not %s" % (name, t.device, device))
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), shape))
+    raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), shape))
 
 
 def _call_on(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with that device current (a kernel
     launched while another device is current would not run on it). The stream's handle is read
     without making a Stream object: 0.1 us instead of 1.8, in calls of a few microseconds."""
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
-        check(fn(*args, stream))
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            check(fn(*args, stream))
+            rc = fn(*args, stream)
+    if rc:
+        check(rc)
 
 
 def _check_ws(ws, device, nbytes):
@@ -377,11 +384,9 @@ def _check_ws(ws, device, nbytes):
 
 def _check_fp8b128(layer, codes, scales):
     """(T, device) of activations that fit the layer."""
-    dev = layer.codes.device
-    _check_rows("codes", codes, _E4M3, dev)
-    T = codes.shape[0]
-    if codes.shape[1] != layer.in_:
-        raise ValueError("codes have %d inputs, the layer %d" % (codes.shape[1], layer.in_))
+    dev = layer.device
+    T = len(codes)
+    _check_rows("codes", codes, _E4M3, dev, (T, layer.in_))
     _check_rows("scales", scales, _F32, dev, (T, -(-layer.in_ // 128)))
     return T, dev
 
@@ -391,16 +396,17 @@ def fp8b128_quantize(x, codes=None, scales=None):
     with one power-of-two scale per 128 inputs (see fp8b128_quantize in include/tq.h)."""
     _check_rows("x", x, _BF16)
     rows, n = x.shape
+    dev = x.device
     nb = -(-n // 128)
     if codes is None:
-        codes = torch.empty((rows, n), dtype=torch.uint8, device=x.device)
+        codes = torch.empty((rows, n), dtype=torch.uint8, device=dev)
     else:
-        _check_rows("codes", codes, _E4M3, x.device, (rows, n))
+        _check_rows("codes", codes, _E4M3, dev, (rows, n))
     if scales is None:
-        scales = torch.empty((rows, nb), dtype=torch.float32, device=x.device)
+        scales = torch.empty((rows, nb), dtype=torch.float32, device=dev)
     else:
-        _check_rows("scales", scales, _F32, x.device, (rows, nb))
-    _call_on(x.device, _lib.load().fp8b128_quantize, x.data_ptr(), rows, n, codes.data_ptr(),
+        _check_rows("scales", scales, _F32, dev, (rows, nb))
+    _call_on(dev, _lib.load().fp8b128_quantize, x.data_ptr(), rows, n, codes.data_ptr(),
              scales.data_ptr())
     return codes, scales
 
@@ -414,7 +420,7 @@ def fp8b128_gemm(layer, codes, scales, flags=0, out=None):
         out = torch.empty((T, layer.out), dtype=dtype, device=dev)
     else:
         _check_rows("out", out, (dtype,), dev, (T, layer.out))
-    _call_on(dev, _lib.load().fp8b128_gemm, ctypes.byref(layer.c_struct()), codes.data_ptr(),
+    _call_on(dev, _lib.load().fp8b128_gemm, layer._ref, codes.data_ptr(),
              scales.data_ptr(), T, out.data_ptr(), flags)
     return out
 
@@ -427,7 +433,7 @@ def fp8b128_gated(layer, codes, scales, out=None):
         out = torch.empty((T, layer.out // 2), dtype=torch.bfloat16, device=dev)
     else:
         _check_rows("out", out, _BF16, dev, (T, layer.out // 2))
-    _call_on(dev, _lib.load().fp8b128_gated, ctypes.byref(layer.c_struct()), codes.data_ptr(),
+    _call_on(dev, _lib.load().fp8b128_gated, layer._ref, codes.data_ptr(),
              scales.data_ptr(), T, out.data_ptr())
     return out
 
@@ -451,7 +457,7 @@ def _fp8b128_backward(fn, layer, codes, scales, dy, width, need_dx, need_dw, dx,
         dw = torch.empty((layer.out, layer.in_), dtype=torch.bfloat16, device=dev)
     lib = _lib.load()
     ws = _check_ws(ws, dev, lib.tq_fp8b128_workspace_bytes(T, layer.out, layer.in_))
-    _call_on(dev, getattr(lib, fn), ctypes.byref(layer.c_struct()), codes.data_ptr(),
+    _call_on(dev, getattr(lib, fn), layer._ref, codes.data_ptr(),
              scales.data_ptr(), T, dy.data_ptr(), None if dx is None else dx.data_ptr(),
              None if dw is None else dw.data_ptr(), ws.data_ptr(), ws.numel())
     return dx, dw
@@ -477,9 +483,9 @@ def fp8b128_gated_backward(layer, codes, scales, dh, need_dx=True, need_dw=True,
 def fp8b128_ffn(gate_up, down, x, flags=0, out=None, ws=None):
     """[T, H]: a dense gated FFN over two fp8b128 projections, fp32 or (TQ_OUT_BF16) bf16 (see
     fp8b128_ffn in include/tq.h)."""
-    dev = gate_up.codes.device
+    dev = gate_up.device
     _check_rows("x", x, _BF16, dev)
-    if down.codes.device != dev:
+    if down.device != dev:
         raise ValueError("the two layers are on different devices")
     T, H = x.shape
     if H != gate_up.in_:
@@ -491,7 +497,7 @@ def fp8b128_ffn(gate_up, down, x, flags=0, out=None, ws=None):
         _check_rows("out", out, (dtype,), dev, (T, H))
     lib = _lib.load()
     ws = _check_ws(ws, dev, lib.tq_fp8b128_ffn_workspace_bytes(T, H, gate_up.out // 2))
-    _call_on(dev, lib.fp8b128_ffn, ctypes.byref(gate_up.c_struct()), ctypes.byref(down.c_struct()),
+    _call_on(dev, lib.fp8b128_ffn, gate_up._ref, down._ref,
              x.data_ptr(), T, out.data_ptr(), flags, ws.data_ptr(), ws.numel())
     return out
 
