@@ -29,13 +29,15 @@ FORWARD = [(1, 16, 16), (1, 1536, 5120), (2, 48, 112), (5, 160, 128), (16, 32, 1
            (200, 400, 272), (257, 528, 640), (300, 1040, 96), (513, 288, 1296), (1030, 784, 528), (3000, 2832, 144),
            # strips of each shape, tiles of each shape, more tiles than compute units
            (12, 5120, 272), (60, 5120, 400), (300, 2064, 656), (1000, 3088, 528), (2100, 2064, 400),
-           (2100, 4112, 272), (4200, 4112, 144)]
+           (2100, 4112, 272), (4200, 4112, 144), (265, 10048, 144), (1714, 11680, 144)]
 GATED = [(1, 32, 16), (1, 1536, 5120), (3, 96, 144), (16, 288, 272), (31, 64, 400), (64, 1440, 528),
          (130, 160, 1040), (257, 544, 256), (300, 800, 400), (700, 1056, 272), (2900, 2848, 272),
-         (60, 5120, 400), (700, 4128, 272), (2100, 2080, 400), (4100, 4096, 144), (4200, 4128, 144)]
+         (60, 5120, 400), (700, 4128, 272), (2100, 2080, 400), (4100, 4096, 144), (4200, 4128, 144),
+         (265, 8672, 144), (1971, 10304, 144)]
 BACKWARD = [(1, 32, 16), (1, 288, 400), (2, 64, 128), (17, 32, 272), (40, 288, 144), (64, 96, 1040),
             (129, 256, 256), (200, 544, 400), (257, 160, 656), (333, 1056, 272), (600, 288, 784), (2100, 352, 2064), (4200, 64, 2320),
-            (1000, 3104, 144), (3000, 2848, 144), (2100, 2048, 272)]
+            (1000, 3104, 144), (3000, 2848, 144), (2100, 2048, 272),
+            (40, 3104, 2064), (33, 5152, 2064), (265, 8672, 144)]
 
 
 def bits_of(t):

@@ -79,22 +79,34 @@ __device__ __forceinline__ f32x4 fb_block_product(const FbOperand<false>& a, con
                                                           0, 0, 0, 0, 0);
 }
 
-constexpr int FB_CUS = 256;  // compute units: workgroups of a grid that walks its tiles
+constexpr int FB_CUS = 256;  // compute units
 
-// Tile j of this workgroup's stream (a workgroup starts with j = blockIdx.x / 8 and, in a grid
-// smaller than the tiles, goes on by gridDim.x / 8): the grid is read as 8 interleaved streams,
-// one per XCD, each a contiguous range of tiles in an order that walks 4 channel tiles per token
-// tile, so that the tiles an XCD works on at one time share rows of both operands in its L2.
-__device__ inline bool fb_tile_of(int tt, int tc, int j, int* t, int* c) {
-  const int n = tt * tc, per = (n + 7) >> 3;
-  const int u = (blockIdx.x & 7) * per + j;
-  if (j >= per || u >= n) return false;
-  const int band = u / (4 * tt), first = 4 * band, width = min(4, tc - first);
-  const int v = u - first * tt;
-  *c = first + v % width;
-  *t = v / width;
-  return true;
-}
+// The work items of a grid over tt x tc tiles. It is read as 8 interleaved streams, one per XCD
+// (workgroup b belongs to stream b % 8 and starts with the stream's item b / 8), each a contiguous
+// range of tiles in an order that walks 4 channel tiles per token tile, so that the tiles an XCD
+// works on at one time share rows of both operands in its L2. Where the last round of a stream
+// has tiles for half of its 32 compute units at most, each of them is two items, halves along
+// the first side, so that the round lasts little over half as long.
+struct FbItems {
+  int tt, tc, per, full, items;  // tiles of a stream, items that are whole tiles, all items
+  __host__ __device__ FbItems(int tt_, int tc_) : tt(tt_), tc(tc_), per((tt_ * tc_ + 7) >> 3) {
+    const int rest = per % (FB_CUS / 8);
+    full = rest <= FB_CUS / 16 ? per - rest : per;
+    items = full + 2 * (per - full);
+  }
+  // Item j of stream x: its tile and which half of it (-1: all); false past the last.
+  __device__ bool at(int x, int j, int* t, int* c, int* half) const {
+    if (j >= items) return false;
+    const int u = x * per + (j < full ? j : full + (j - full) / 2);
+    if (u >= tt * tc) return false;
+    *half = j < full ? -1 : (j - full) & 1;
+    const int band = u / (4 * tt), first = 4 * band, width = min(4, tc - first);
+    const int v = u - first * tt;
+    *c = first + v % width;
+    *t = v / width;
+    return true;
+  }
+};
 
 // ---- epilogues ------------------------------------------------------------------------------
 // What a forward kernel does with the sums of four consecutive channels o .. o + 3 of one

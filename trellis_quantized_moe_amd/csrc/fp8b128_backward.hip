@@ -10,6 +10,7 @@
 #include "fp8b128.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace tq {
 
@@ -187,15 +188,16 @@ hipError_t launch_dx_strip(const Fp8b128BackwardArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The 64 x 64 results of each wave of a tile (row 16 t + lane % 16, inputs 16 c + 4 (lane / 16) ..
-// + 3 in acc[c][t]) to its rows at dst, of which `rows` exist and `bytes` of each, by whole rows
+// The 16 NT x 64 results of each wave of a tile (row 16 t + lane % 16, inputs 16 c + 4 (lane / 16)
+// .. + 3 in acc[c][t]) to its rows at dst, of which `rows` exist and `bytes` of each, by whole rows
 // through 4096 bytes of LDS of the wave's own.
-__device__ __forceinline__ void store_tile(uint8_t* lds, const f32x4 (&acc)[4][4], uint8_t* dst,
+template <int NT>
+__device__ __forceinline__ void store_tile(uint8_t* lds, const f32x4 (&acc)[4][NT], uint8_t* dst,
                                            int64_t stride, int rows, int bytes) {
   const int lane = fb_fresh_lane(), r = lane & 15, q = lane >> 4;
   FbRows<128, 32> out{lds};
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
+  for (int hf = 0; hf < NT / 2; ++hf) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -209,8 +211,8 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, const f32x4 (&acc)[4][4
 
 // ---- dx, many tokens ------------------------------------------------------------------------
 //
-// A workgroup of eight waves owns 256 inputs of 128 tokens, wave (wi, wt) 64 inputs of 64
-// tokens. Steps of 64 outputs: 64 rows of 256 code bytes and 128 rows of 128 bytes of dy go
+// A workgroup of eight waves owns 256 inputs of 128 tokens (half an item: of 64), wave (wi, wt) 64
+// inputs of 64 (32) tokens. Steps of 64 outputs: 64 rows of 256 code bytes and 128 rows of 128 bytes of dy go
 // straight to a ring of four LDS stages, three steps ahead. The products of two steps (one block
 // of 128 outputs) are added from zero and then scaled into the sums.
 struct DxShared {
@@ -226,11 +228,13 @@ struct DxTile {
   uint32_t wo[2], dof[2];
 };
 
-__device__ __forceinline__ DxTile dx_tile_at(const Fp8b128BackwardArgs& a, int tile_t, int tile_i, int w) {
+// The tile, or one half of its tokens.
+__device__ __forceinline__ DxTile dx_tile_at(const Fp8b128BackwardArgs& a, int tile_t, int tile_i,
+                                             int half, int w) {
   const int lane = fb_fresh_lane();
   DxTile d;
-  d.t0 = (int64_t)tile_t * 128;
-  d.rows = (int)min((int64_t)128, a.T - d.t0);
+  d.t0 = (int64_t)tile_t * 128 + (half > 0 ? 64 : 0);
+  d.rows = (int)max(min((int64_t)(half < 0 ? 128 : 64), a.T - d.t0), (int64_t)0);
   d.i0 = tile_i * 256;
   d.ib = min((d.i0 + 64 * (w & 3)) / 128, a.nb - 1);
   // codes: an instruction fills 4 rows; lane l position l % 16 of row l / 16, which holds the
@@ -246,7 +250,7 @@ __device__ __forceinline__ DxTile dx_tile_at(const Fp8b128BackwardArgs& a, int t
   return d;
 }
 
-__device__ void dx_tiles(const Fp8b128BackwardArgs& a, DxShared& sh, int tt, int ti) {
+__device__ void dx_tiles(const Fp8b128BackwardArgs& a, DxShared& sh, const FbItems& items) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = w & 3, wt = w >> 2;
@@ -270,56 +274,6 @@ __device__ void dx_tiles(const Fp8b128BackwardArgs& a, DxShared& sh, int tt, int
     }
   };
 
-  f32x4 acc[4][4], p[4][4];
-  // operands of 32 outputs (half j of a step)
-  u32x2 av[2][4];
-  u32x4 bv[2][4];
-  auto read = [&](int st, int j) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      bv[j][t] = *reinterpret_cast<const u32x4*>(
-          &sh.d[st][128 * (64 * wt + 16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int row = 32 * j + 8 * q + (r >> 1);
-      av[j][c] = read_tr8(&sh.w[st][256 * row + 16 * ((4 * wi + c) ^ (row & 15)) + 8 * (r & 1)]);
-    }
-  };
-  auto multiply = [&](int j, bool first, int st, int k) {  // with the loads of step k, if k >= 0
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (k >= 0) {
-        __builtin_amdgcn_sched_barrier(0);
-        load(c, st, k);
-      }
-      const u32x4 a8 = fb_bf16_of8(av[j][c].x, av[j][c].y);
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        p[c][t] = mfma_bf16(a8, bv[j][t], first ? (f32x4){0.f, 0.f, 0.f, 0.f} : p[c][t]);
-    }
-  };
-  // A step's second half is read while its first half is multiplied, and the next step's first
-  // half while its second is: between the two, the next step's data have landed everywhere,
-  // and this step's stage is no longer read.
-  auto step = [&](int st, int k) {
-    float s = 0.0f;
-    if (st & 1) s = fb_uniform_load(a.ws + (int64_t)(k / 2) * a.nb + d.ib);
-    read(st, 1);
-    multiply(0, (st & 1) == 0, 0, -1);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<2 * LOADS>();
-    bare_barrier();
-    read((st + 1) & 3, 0);
-    multiply(1, false, st, k + 4);
-    if (st & 1) {  // the block of 128 outputs is complete
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[c][t][i] = __builtin_fmaf(p[c][t][i], s, acc[c][t][i]);
-    }
-  };
   auto load_steps = [&](int first, int last) {
 #pragma unroll
     for (int k = first; k < last; ++k)
@@ -327,16 +281,69 @@ __device__ void dx_tiles(const Fp8b128BackwardArgs& a, DxShared& sh, int tt, int
       for (int n = 0; n < 4; ++n) load(n, k, k);
   };
 
-  int tile_t, tile_i;
-  int j = blockIdx.x >> 3;
-  if (!fb_tile_of(tt, ti, j, &tile_t, &tile_i)) return;
-  d = dx_tile_at(a, tile_t, tile_i, w);
+  int tile_t, tile_i, half, j = blockIdx.x >> 3;
+  const int stream = blockIdx.x & 7;
+  if (!items.at(stream, j, &tile_t, &tile_i, &half)) return;
+  d = dx_tile_at(a, tile_t, tile_i, half, w);
   load_steps(0, 3);
-  for (bool more = true; more;) {
+  // One item, whole (NT = 4 token tiles of 16 per wave) or half (NT = 2): its first steps are
+  // loading; afterwards those of the next item are. Returns whether there is one.
+  auto item = [&](auto tiles) {
+    constexpr int NT = decltype(tiles)::value;
+    f32x4 acc[4][NT], p[4][NT];
+    // operands of 32 outputs (half j of a step)
+    u32x2 av[2][4];
+    u32x4 bv[2][NT];
+    auto read = [&](int st, int j) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        bv[j][t] = *reinterpret_cast<const u32x4*>(
+            &sh.d[st][128 * (16 * NT * wt + 16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int row = 32 * j + 8 * q + (r >> 1);
+        av[j][c] = read_tr8(&sh.w[st][256 * row + 16 * ((4 * wi + c) ^ (row & 15)) + 8 * (r & 1)]);
+      }
+    };
+    auto multiply = [&](int j, bool first, int st, int k) {  // with the loads of step k, if k >= 0
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (k >= 0) {
+          __builtin_amdgcn_sched_barrier(0);
+          load(c, st, k);
+        }
+        const u32x4 a8 = fb_bf16_of8(av[j][c].x, av[j][c].y);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          p[c][t] = mfma_bf16(a8, bv[j][t], first ? (f32x4){0.f, 0.f, 0.f, 0.f} : p[c][t]);
+      }
+    };
+    // A step's second half is read while its first half is multiplied, and the next step's first
+    // half while its second is: between the two, the next step's data have landed everywhere,
+    // and this step's stage is no longer read.
+    auto step = [&](int st, int k) {
+      float s = 0.0f;
+      if (st & 1) s = fb_uniform_load(a.ws + (int64_t)(k / 2) * a.nb + d.ib);
+      read(st, 1);
+      multiply(0, (st & 1) == 0, 0, -1);
+      __builtin_amdgcn_sched_barrier(0);
+      wait_vmcnt<2 * LOADS>();
+      bare_barrier();
+      read((st + 1) & 3, 0);
+      multiply(1, false, st, k + 4);
+      if (st & 1) {  // the block of 128 outputs is complete
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[c][t][i] = __builtin_fmaf(p[c][t][i], s, acc[c][t][i]);
+      }
+    };
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < NT; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
     load_steps(3, 4);
     wait_vmcnt<3 * LOADS>();
     bare_barrier();
@@ -353,24 +360,31 @@ __device__ void dx_tiles(const Fp8b128BackwardArgs& a, DxShared& sh, int tt, int
     // the loads past the last step have landed, and no wave reads a stage any more
     wait_vmcnt<0>();
     bare_barrier();
-    uint8_t* dst = reinterpret_cast<uint8_t*>(a.dx + (d.t0 + 64 * wt) * a.in + d.i0 + 64 * wi);
-    const int rows = d.rows - 64 * wt, bytes = (a.in - d.i0 - 64 * wi) * 2;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(a.dx + (d.t0 + 16 * NT * wt) * a.in + d.i0 + 64 * wi);
+    const int rows = d.rows - 16 * NT * wt, bytes = (a.in - d.i0 - 64 * wi) * 2;
     j += gridDim.x >> 3;
-    more = fb_tile_of(tt, ti, j, &tile_t, &tile_i);
+    const bool more = items.at(stream, j, &tile_t, &tile_i, &half);
     if (more) {
-      d = dx_tile_at(a, tile_t, tile_i, w);
+      d = dx_tile_at(a, tile_t, tile_i, half, w);
       load_steps(0, 3);
     }
-    // through the last stage, which the next tile fills after the barrier
+    // through the last stage, which the next item fills after the barrier
     store_tile(w < 4 ? sh.w[3] + 4096 * w : sh.d[3] + 4096 * (w - 4), acc, dst, (int64_t)a.in * 2, rows, bytes);
     bare_barrier();
-  }
+    return more;
+  };
+  while (half < 0)  // halves come last, one to a workgroup
+    if (!item(std::integral_constant<int, 4>())) {
+      wait_vmcnt<0>();
+      return;
+    }
+  item(std::integral_constant<int, 2>());
   wait_vmcnt<0>();
 }
 
-__global__ __launch_bounds__(512) void fp8b128_dx_kernel(Fp8b128BackwardArgs a, int tt, int ti) {
+__global__ __launch_bounds__(512) void fp8b128_dx_kernel(Fp8b128BackwardArgs a, FbItems items) {
   __shared__ DxShared sh;
-  dx_tiles(a, sh, tt, ti);
+  dx_tiles(a, sh, items);
 }
 
 // ---- dw -------------------------------------------------------------------------------------
@@ -397,8 +411,8 @@ __global__ __launch_bounds__(256) void fp8b128_widen_kernel(const uint8_t* __res
   y[2 * k + 1] = out[1];
 }
 
-// A workgroup of eight waves owns 256 inputs of 128 channels, wave (wi, wo) 64 inputs of 64
-// channels; steps of 64 tokens through a ring of three LDS stages, two steps ahead. A row's
+// A workgroup of eight waves owns 256 inputs of 128 channels (half an item: of 64), wave (wi, wo)
+// 64 inputs of 64 (32) channels; steps of 64 tokens through a ring of three LDS stages, two steps ahead. A row's
 // 32-byte chunk c lies at position c ^ swizzle(row): the LDS serves 32 lanes at a time, which
 // read one chunk of rows 8 q + 0..3 and 8 (q + 1) + 0..3 (or + 4..7), and those eight rows get
 // eight different positions.
@@ -409,11 +423,12 @@ struct DwShared {
   alignas(16) uint8_t d[3][64 * 256];
 };
 
-__device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, int tile_i) {
+// NT tiles of 16 channels per wave: 4, or 2 in half an item, the channels o0 .. o0 + 32 NT - 1.
+template <int NT>
+__device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int o0, int i0) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = w & 3, wo = w >> 2;
-  const int i0 = tile_i * 256, o0 = tile_o * 128;
   const int nsteps = (int)((a.T + 63) / 64);
   uint32_t xo[4], dof[2];
 #pragma unroll
@@ -426,7 +441,7 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
   for (int j = 0; j < 2; ++j) {  // four rows of 256 bytes
     const int row = 8 * w + 4 * j + (lane >> 4), pos = lane & 15;
     const int o = o0 + 16 * ((pos >> 1) ^ dw_swizzle(row)) + 8 * (pos & 1);
-    dof[j] = o < a.out ? ((uint32_t)row * (uint32_t)a.out + o) * 2u : FB_OOB;
+    dof[j] = o < min(a.out, o0 + 32 * NT) ? ((uint32_t)row * (uint32_t)a.out + o) * 2u : FB_OOB;
   }
   constexpr int LOADS = 6;
   // A step's loads, in three parts, as in dx_tile; rows past the last token are read as zeros.
@@ -448,19 +463,19 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
                                                  dof[j], 0, 0, 0);
     }
   };
-  f32x4 acc[4][4];
+  f32x4 acc[4][NT];
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
   // operands of 32 tokens (half j of a step). Lane (r, q) of half h: row 32 j + 8 q + 4 h + r / 4,
   // quarter r % 4 of a 32-byte chunk
-  u32x4 av[2][4], bv[2][4];
+  u32x4 av[2][4], bv[2][NT];
   auto read = [&](int st, int j) {
     const int row = 32 * j + 8 * q + (r >> 2), sw = dw_swizzle(row);  // the same for row + 4
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint8_t* p = &sh.d[st][256 * row + 32 * ((4 * wo + c) ^ sw) + 8 * (r & 3)];
+    for (int c = 0; c < NT; ++c) {
+      const uint8_t* p = &sh.d[st][256 * row + 32 * ((NT * wo + c) ^ sw) + 8 * (r & 3)];
       const u32x2 lo = read_tr16(p), hi = read_tr16(p + 4 * 256);
       bv[j][c] = (u32x4){lo.x, lo.y, hi.x, hi.y};
     }
@@ -479,7 +494,7 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
         if (c < 3) load(c, st, k);
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[c][t] = mfma_bf16(av[j][c], bv[j][t], acc[c][t]);
+      for (int t = 0; t < NT; ++t) acc[c][t] = mfma_bf16(av[j][c], bv[j][t], acc[c][t]);
     }
   };
 #pragma unroll
@@ -505,35 +520,41 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int tile_o, 
   }
   wait_vmcnt<0>();
   __syncthreads();
-  store_tile(sh.x[0] + 4096 * w, acc, reinterpret_cast<uint8_t*>(a.dw + (int64_t)(o0 + 64 * wo) * a.in + i0 + 64 * wi),
-             (int64_t)a.in * 2, a.out - o0 - 64 * wo, (a.in - i0 - 64 * wi) * 2);
+  store_tile(sh.x[0] + 4096 * w, acc, reinterpret_cast<uint8_t*>(a.dw + (int64_t)(o0 + 16 * NT * wo) * a.in + i0 + 64 * wi),
+             (int64_t)a.in * 2, a.out - o0 - 16 * NT * wo, (a.in - i0 - 64 * wi) * 2);
 }
 
-__global__ __launch_bounds__(512) void fp8b128_dw_kernel(Fp8b128BackwardArgs a, int to, int ti) {
+__global__ __launch_bounds__(512) void fp8b128_dw_kernel(Fp8b128BackwardArgs a, FbItems items) {
   __shared__ DwShared sh;
-  int o, i;
-  if (fb_tile_of(to, ti, blockIdx.x >> 3, &o, &i)) dw_tile(a, sh, o, i);
+  int o, i, half;
+  if (!items.at(blockIdx.x & 7, blockIdx.x >> 3, &o, &i, &half)) return;
+  if (half < 0)
+    dw_tile<4>(a, sh, 128 * o, 256 * i);
+  else
+    dw_tile<2>(a, sh, 128 * o + 64 * half, 256 * i);
 }
 
 }  // namespace
 
 // The kernel with the least time expected, by the rounds of workgroups over the compute units and
-// what a round took at 1,536 outputs (0.1 us): strips of (4, 1) 31, (4, 2) 41, (4, 4) 70, tiles 230.
-// Measured where two meet, for 5,120 inputs: 32 tokens 5.8 us by (4, 1), 6.3 by (4, 2); 128 tokens
-// 10.7 by (4, 2), 9.8 by (4, 4); 512 tokens 23.9 by (4, 4), 26.8 by tiles; 768 tokens 31.0 and
-// 28.2. (768 inputs x 5,120 outputs, 333 tokens: 13.2 by (4, 1), 67 by tiles.)
+// what a round took at 1,536 outputs (0.1 us): strips of (4, 1) 31, (4, 2) 41, (4, 4) 70, tiles
+// 230, a round of halves of tiles 135. Measured where two meet, for 5,120 inputs: 32 tokens 5.8 us
+// by (4, 1), 6.3 by (4, 2); 128 tokens 10.7 by (4, 2), 9.8 by (4, 4); 512 tokens 23.9 by (4, 4),
+// 26.8 by whole tiles, 19.0 by halves; 768 tokens 31.0, 28.2 and 20.9. (768 inputs x 5,120
+// outputs, 333 tokens: 13.2 by (4, 1), 67 by whole tiles.)
 hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s) {
   const int64_t tt = ceil_div(a.T, 128), ti = ceil_div(a.in, 256);
   const int64_t s1 = 31 * ceil_div(dx_strip_groups<4, 1>(a), FB_CUS);
   const int64_t s2 = 41 * ceil_div(dx_strip_groups<4, 2>(a), FB_CUS);
   const int64_t s4 = 70 * ceil_div(dx_strip_groups<4, 4>(a), FB_CUS);
-  const int64_t tiles = 230 * ceil_div(tt * ti, FB_CUS);
+  const FbItems items((int)tt, (int)ti);
+  const int64_t tiles = 230 * ceil_div(items.full, FB_CUS / 8) + (items.items > items.full ? 135 : 0);
   const int64_t least = std::min(std::min(s1, s2), std::min(s4, tiles));
   if (least == s1) return launch_dx_strip<4, 1>(a, s);
   if (least == s2) return launch_dx_strip<4, 2>(a, s);
   if (least == s4) return launch_dx_strip<4, 4>(a, s);
-  hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)std::min<int64_t>((tt * ti + 7) & ~7, FB_CUS)),
-                     dim3(512), 0, s, a, (int)tt, (int)ti);
+  hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)(8 * std::min(items.items, FB_CUS / 8))), dim3(512),
+                     0, s, a, items);
   return hipGetLastError();
 }
 
@@ -543,8 +564,8 @@ hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& a, hipStream_t s) {
                      a.xs, n16, a.in, a.nb, reinterpret_cast<u32x4*>(a.xw));
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int to = (a.out + 127) / 128, ti = (a.in + 255) / 256;
-  hipLaunchKernelGGL(fp8b128_dw_kernel, dim3((unsigned)((to * ti + 7) & ~7)), dim3(512), 0, s, a, to, ti);
+  const FbItems items((a.out + 127) / 128, (a.in + 255) / 256);
+  hipLaunchKernelGGL(fp8b128_dw_kernel, dim3((unsigned)(8 * items.items)), dim3(512), 0, s, a, items);
   return hipGetLastError();
 }
 

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 namespace tq {
 
@@ -311,7 +312,8 @@ struct FbTile {
 // SAME: the wave's strips (gated: its gate strips, and its up strips) lie in one block of 128
 // channels, so that a block of inputs has one scale for them.
 template <int EPI, int SW, int WT, int ST, bool SAME>
-__device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT, ST>& sh, int tt, int tc) {
+__device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT, ST>& sh,
+                         const FbItems& items) {
   using S = FbTile<SW, WT, ST>;
   constexpr bool GATED = fb_gated(EPI), EXACT = EPI == FB_F32;
   constexpr int NX = S::BT / S::WAVES / 8, NW = S::BC / S::WAVES / 8;
@@ -335,10 +337,10 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT, ST>& sh, int t
   // the scales of the wave's strips: one for each, or (SAME) for each half, block by block
   constexpr int NG = !SAME ? SW : GATED ? 2 : 1, PER_GROUP = SW / NG;
   const float* ws[NG];
-  auto set_tile = [&](int tile_t, int tile_c) {
+  auto set_tile = [&](int tile_t, int tile_c, int half_item) {  // the tile, or a half of its tokens
     const int lane = fb_fresh_lane(), chunk = 16 * ((lane & 7) ^ (lane >> 3));
-    t0 = (int64_t)tile_t * S::BT;
-    rows = (int)min((int64_t)S::BT, a.T - t0);
+    t0 = (int64_t)tile_t * S::BT + (half_item > 0 ? S::BT / 2 : 0);
+    rows = (int)max(min((int64_t)(half_item < 0 ? S::BT : S::BT / 2), a.T - t0), (int64_t)0);
     c0 = tile_c * (GATED ? S::BC / 2 : S::BC);
     // weight row k of the tile: channel and validity
     auto channel = [&](int k) {
@@ -390,83 +392,87 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT, ST>& sh, int t
       for (int n = 0; n < LOADS; ++n) load(n, kb, kb);
   };
 
-  f32x4 acc[SW][4], p[4];
-  float m[4];
-  const int at0 = 128 * r + 16 * (q ^ (r & 7)), at1 = 128 * r + 16 * ((4 + q) ^ (r & 7));
-  FbOperand<EXACT> av[2], bv[4];
-  float sx[4];
-  auto read_a = [&](int st, int s) {
-    const uint8_t* l = sh.w[st] + 128 * strip_row(s);
-    av[s & 1].set(*reinterpret_cast<const u32x4*>(l + at0), *reinterpret_cast<const u32x4*>(l + at1));
-  };
-  auto read_b = [&](int st, int t) {
-    const uint8_t* l = sh.x[st] + 128 * (64 * wt + 16 * t);
-    bv[t].set(*reinterpret_cast<const u32x4*>(l + at0), *reinterpret_cast<const u32x4*>(l + at1));
-  };
-  auto read_sx = [&](int st, int t) { sx[t] = sh.sx[st][64 * wt + 16 * t + r]; };
-  // Adds the last product of token tile t to the sum of strip s (the strip before the one
-  // whose product comes next, so that it has had three products' time to finish).
-  auto add = [&](int s, int t) {
+  int tile_t, tile_c, half_item, j = blockIdx.x >> 3;
+  const int stream = blockIdx.x & 7;
+  if (!items.at(stream, j, &tile_t, &tile_c, &half_item)) return;
+  set_tile(tile_t, tile_c, half_item);
+  load_blocks(0, ST - 1);
+  // One item, whole (NT = 4 token tiles of 16 per wave) or half (NT = 2): its first blocks are
+  // loading; afterwards those of the next item are. Returns whether there is one.
+  auto item = [&](auto tiles) {
+    constexpr int NT = decltype(tiles)::value;
+    f32x4 acc[SW][NT], p[NT];
+    float m[NT];
+    const int at0 = 128 * r + 16 * (q ^ (r & 7)), at1 = 128 * r + 16 * ((4 + q) ^ (r & 7));
+    FbOperand<EXACT> av[2], bv[NT];
+    float sx[NT];
+    auto read_a = [&](int st, int s) {
+      const uint8_t* l = sh.w[st] + 128 * strip_row(s);
+      av[s & 1].set(*reinterpret_cast<const u32x4*>(l + at0), *reinterpret_cast<const u32x4*>(l + at1));
+    };
+    auto read_b = [&](int st, int t) {
+      const uint8_t* l = sh.x[st] + 128 * (16 * NT * wt + 16 * t);
+      bv[t].set(*reinterpret_cast<const u32x4*>(l + at0), *reinterpret_cast<const u32x4*>(l + at1));
+    };
+    auto read_sx = [&](int st, int t) { sx[t] = sh.sx[st][16 * NT * wt + 16 * t + r]; };
+    // Adds the last product of token tile t to the sum of strip s (the strip before the one
+    // whose product comes next, so that it has had three products' time to finish).
+    auto add = [&](int s, int t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[s][t][i] = __builtin_fmaf(p[t][i], m[t], acc[s][t][i]);
-    asm volatile("" : "+v"(acc[s][t]));  // done here, not where the compiler would gather them
-  };
+      for (int i = 0; i < 4; ++i) acc[s][t][i] = __builtin_fmaf(p[t][i], m[t], acc[s][t][i]);
+      asm volatile("" : "+v"(acc[s][t]));  // done here, not where the compiler would gather them
+    };
 
-  // The results leave through LDS (the last stage: its refill waits for the barrier after), 32
-  // (fp32: 16) tokens of the wave at a time: stored straight from registers, by 32 bytes of 16 rows an
-  // instruction, the bf16 tile took 30,000 cycles beside the 114,000 of its products at 5,120
-  // inputs.
-  constexpr int NO = GATED ? SW / 2 : SW, ESIZE = EPI == FB_F32 ? 4 : 2, ROW = 16 * NO * ESIZE;
-  constexpr int N = EPI == FB_F32 ? 16 : 32;
-  static_assert(N * ROW * S::WAVES <= sizeof(sh.w[0]) + sizeof(sh.x[0]), "results' way out");
-  auto store_results = [&](int64_t token, int tokens, int channel0) {
-    const int lane = fb_fresh_lane(), r = lane & 15, q = lane >> 4;
-    constexpr int IN_W = sizeof(sh.w[0]) / (N * ROW);  // waves whose rows fit the weights' part
-    FbRows<ROW, N> out{w < IN_W ? sh.w[ST - 1] + w * (N * ROW) : sh.x[ST - 1] + (w - IN_W) * (N * ROW)};
-    const int bytes = min(16 * NO, width - channel0) * ESIZE;
-    const int64_t stride = (int64_t)(EPI == FB_GATED ? half : a.out) * ESIZE;
+    // The results leave through LDS (the last stage: its refill waits for the barrier after), 32
+    // (fp32: 16) tokens of the wave at a time: stored straight from registers, by 32 bytes of 16 rows an
+    // instruction, the bf16 tile took 30,000 cycles beside the 114,000 of its products at 5,120
+    // inputs.
+    constexpr int NO = GATED ? SW / 2 : SW, ESIZE = EPI == FB_F32 ? 4 : 2, ROW = 16 * NO * ESIZE;
+    constexpr int N = EPI == FB_F32 ? 16 : 32;
+    static_assert(N * ROW * S::WAVES <= sizeof(sh.w[0]) + sizeof(sh.x[0]), "results' way out");
+    auto store_results = [&](int64_t token, int tokens, int channel0) {
+      const int lane = fb_fresh_lane(), r = lane & 15, q = lane >> 4;
+      constexpr int IN_W = sizeof(sh.w[0]) / (N * ROW);  // waves whose rows fit the weights' part
+      FbRows<ROW, N> out{w < IN_W ? sh.w[ST - 1] + w * (N * ROW) : sh.x[ST - 1] + (w - IN_W) * (N * ROW)};
+      const int bytes = min(16 * NO, width - channel0) * ESIZE;
+      const int64_t stride = (int64_t)(EPI == FB_GATED ? half : a.out) * ESIZE;
 #pragma unroll
-    for (int f = 0; f < 64; f += N) {
-      uint8_t* dst = static_cast<uint8_t*>(a.y) + (token + f) * stride + (int64_t)channel0 * ESIZE;
-      u32x2 du[NO][N / 16];
-#pragma unroll
-      for (int s = 0; s < NO; ++s)
-#pragma unroll
-        for (int v = 0; v < N / 16; ++v) {
-          const int t = f / 16 + v, k = 16 * v + r, o = 16 * s + 4 * q;
-          const f32x4 g = acc[s][t], u = acc[s + SW - NO][t];
-          if constexpr (EPI == FB_F32) {
-            out.put(k, 4 * o, g);
-          } else if constexpr (EPI == FB_BF16) {
-            out.put(k, 2 * o, (u32x2){fb_pack_bf16(g[0], g[1]), fb_pack_bf16(g[2], g[3])});
-          } else if constexpr (EPI == FB_GATED) {
-            out.put(k, 2 * o, fb_gate4(g, u));
-          } else {
-            u32x2 dh = (u32x2){0, 0}, dg;
-            if (f + k < tokens && channel0 + o < width)
-              dh = *reinterpret_cast<const u32x2*>(a.dh + (token + f + k) * half + channel0 + o);
-            fb_gate_grad4(g, u, dh, &dg, &du[s][v]);
-            out.put(k, 2 * o, dg);
-          }
-        }
-      out.store(dst, stride, tokens - f, bytes, lane);
-      if constexpr (EPI == FB_GATED_GRAD) {
+      for (int f = 0; f < 16 * NT; f += N) {
+        uint8_t* dst = static_cast<uint8_t*>(a.y) + (token + f) * stride + (int64_t)channel0 * ESIZE;
+        u32x2 du[NO][N / 16];
 #pragma unroll
         for (int s = 0; s < NO; ++s)
 #pragma unroll
-          for (int v = 0; v < N / 16; ++v) out.put(16 * v + r, 2 * (16 * s + 4 * q), du[s][v]);
-        out.store(dst + half * 2, stride, tokens - f, bytes, lane);
-      }
-    }
-  };
-
-  int tile_t, tile_c, j = blockIdx.x >> 3;
-  if (!fb_tile_of(tt, tc, j, &tile_t, &tile_c)) return;
-  set_tile(tile_t, tile_c);
-  load_blocks(0, ST - 1);
-  for (bool more = true; more;) {
+          for (int v = 0; v < N / 16; ++v) {
+            const int t = f / 16 + v, k = 16 * v + r, o = 16 * s + 4 * q;
+            const f32x4 g = acc[s][t], u = acc[s + SW - NO][t];
+            if constexpr (EPI == FB_F32) {
+              out.put(k, 4 * o, g);
+            } else if constexpr (EPI == FB_BF16) {
+              out.put(k, 2 * o, (u32x2){fb_pack_bf16(g[0], g[1]), fb_pack_bf16(g[2], g[3])});
+            } else if constexpr (EPI == FB_GATED) {
+              out.put(k, 2 * o, fb_gate4(g, u));
+            } else {
+              u32x2 dh = (u32x2){0, 0}, dg;
+              if (f + k < tokens && channel0 + o < width)
+                dh = *reinterpret_cast<const u32x2*>(a.dh + (token + f + k) * half + channel0 + o);
+              fb_gate_grad4(g, u, dh, &dg, &du[s][v]);
+              out.put(k, 2 * o, dg);
+            }
+          }
+        out.store(dst, stride, tokens - f, bytes, lane);
+        if constexpr (EPI == FB_GATED_GRAD) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+          for (int s = 0; s < NO; ++s)
+#pragma unroll
+            for (int v = 0; v < N / 16; ++v) out.put(16 * v + r, 2 * (16 * s + 4 * q), du[s][v]);
+          out.store(dst + half * 2, stride, tokens - f, bytes, lane);
+        }
+      }
+    };
+
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int s = 0; s < SW; ++s) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
       p[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -480,7 +486,7 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT, ST>& sh, int t
     bare_barrier();
     read_a(0, 0);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < NT; ++t) {
       read_b(0, t);
       read_sx(0, t);
     }
@@ -511,7 +517,7 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT, ST>& sh, int t
         for (int n = 0; n < PER; ++n)
           load(n + (last ? 0 : PER * (s + 1)), last ? st : before, kb + (last ? ST : ST - 1));
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < NT; ++t) {
           add((s + SW - 1) % SW, t);
           p[t] = fb_block_product(av[s & 1], bv[t]);
           if (s % PER_GROUP == 0) m[t] = sx[t] * ss[s / PER_GROUP];
@@ -527,49 +533,51 @@ __device__ void fb_tiles(const Fp8b128GemmArgs& a, FbTile<SW, WT, ST>& sh, int t
       st = next;
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) add(SW - 1, t);
+    for (int t = 0; t < NT; ++t) add(SW - 1, t);
     // the loads past the last block have landed, and no wave reads a stage any more
     wait_vmcnt<0>();
     bare_barrier();
-    const int64_t first_token = t0 + 64 * wt;
-    const int tokens = rows - 64 * wt, channel0 = c0 + strip_row(0);
+    const int64_t first_token = t0 + 16 * NT * wt;
+    const int tokens = rows - 16 * NT * wt, channel0 = c0 + strip_row(0);
     j += gridDim.x >> 3;
-    more = fb_tile_of(tt, tc, j, &tile_t, &tile_c);
+    const bool more = items.at(stream, j, &tile_t, &tile_c, &half_item);
     if (more) {
-      set_tile(tile_t, tile_c);
+      set_tile(tile_t, tile_c, half_item);
       load_blocks(0, ST - 1);
     }
     store_results(first_token, tokens, channel0);
     bare_barrier();
-  }
-  wait_vmcnt<0>();  // no load may still be writing this workgroup's LDS when it ends
+    return more;
+  };
+  while (half_item < 0)  // halves come last, one to a workgroup
+    if (!item(std::integral_constant<int, 4>())) {
+      wait_vmcnt<0>();  // no load may still be writing this workgroup's LDS when it ends
+      return;
+    }
+  item(std::integral_constant<int, 2>());
+  wait_vmcnt<0>();
 }
 
 template <int EPI, int SW, int WT, int ST, bool SAME>
-__global__ __launch_bounds__(128 * WT) void fp8b128_tile_kernel(Fp8b128GemmArgs a, int tt, int tc) {
+__global__ __launch_bounds__(128 * WT) void fp8b128_tile_kernel(Fp8b128GemmArgs a, FbItems items) {
   __shared__ FbTile<SW, WT, ST> sh;
-  fb_tiles<EPI, SW, WT, ST, SAME>(a, sh, tt, tc);
+  fb_tiles<EPI, SW, WT, ST, SAME>(a, sh, items);
 }
 
 template <int EPI, int SW, int WT, int ST>
-struct FbTiles {
+FbItems tile_items(const Fp8b128GemmArgs& a) {
   using S = FbTile<SW, WT, ST>;
-  int tt, tc;  // tiles of tokens and of channels
-  explicit FbTiles(const Fp8b128GemmArgs& a)
-      : tt((int)ceil_div(a.T, S::BT)), tc((int)ceil_div(a.out, S::BC)) {}
-  int64_t rounds() const { return ceil_div((int64_t)tt * tc, FB_CUS); }  // over the compute units
-};
+  return FbItems((int)ceil_div(a.T, S::BT), (int)ceil_div(a.out, S::BC));
+}
 
 template <int EPI, int SW, int WT, int ST>
 hipError_t launch_tiles(const Fp8b128GemmArgs& a, hipStream_t s) {
-  using S = FbTile<SW, WT, ST>;
-  const FbTiles<EPI, SW, WT, ST> n(a);
-  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)n.tt * n.tc + 7) & ~7, FB_CUS));
+  const FbItems n = tile_items<EPI, SW, WT, ST>(a);
+  const dim3 grid((unsigned)(8 * std::min(n.items, FB_CUS / 8))), block(FbTile<SW, WT, ST>::THREADS);
   // tiles start at multiples of 64 channels, the up half at channel I = out / 2
   if (!fb_gated(EPI) || a.out % 128 == 0)
-    return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, ST, true>, grid, dim3(S::THREADS), s, a, n.tt, n.tc);
-  return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, ST, !fb_gated(EPI)>, grid, dim3(S::THREADS), s, a,
-                      n.tt, n.tc);
+    return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, ST, true>, grid, block, s, a, n);
+  return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, ST, !fb_gated(EPI)>, grid, block, s, a, n);
 }
 
 // The kernel with the least time expected, by the rounds of workgroups over the compute units and
@@ -578,11 +586,12 @@ hipError_t launch_tiles(const Fp8b128GemmArgs& a, hipStream_t s) {
 //   strips of (NS, TT)   18 / 22 times NS + TT: 5.5 us with (1, 1), 7.2 with (2, 2), 11.2 with
 //                        (4, 2), 14.3 / 18 with (4, 4)
 //   128 x 128 tiles      380 / 540 (for one round: two were never the least)
-//   128 x 256 tiles      470 / 770
-//   256 x 256 tiles      750 (bf16 results only)
+//   128 x 256 tiles      470 / 770, a round of halves 300 / 480
+//   256 x 256 tiles      750, a round of halves 520 (bf16 results only)
 // Measured where two meet: 512 tokens x 1,536 channels 15.9 us by (4, 4) strips, 37.8 by 128 x 128
-// tiles; 512 x 5,120 41.8 and 38.8; 2,048 x 5,120 84.7 by 128 x 128, 69.2 by 256 x 256 tiles;
-// 4,096 x 5,120 125 by 128 x 256, 131 by 256 x 256 tiles; 8,192 x 5,120 230 and 212.
+// tiles; 512 x 5,120 41.8, 38.8 and 31.4 by halves of 128 x 256 tiles; 1,024 x 5,120 43.9 by
+// 128 x 256 tiles, 49.9 by halves of 256 x 256 ones; 2,048 x 5,120 81.5 and (whole) 69.2; 8,192 x
+// 7,168 281 us in four rounds of 256 x 256 tiles, 268 with the last one's in halves.
 template <int EPI>
 hipError_t launch_forward(const Fp8b128GemmArgs& a, hipStream_t s) {
   constexpr bool EXACT = EPI == FB_F32;
@@ -603,10 +612,15 @@ hipError_t launch_forward(const Fp8b128GemmArgs& a, hipStream_t s) {
   offer(4 * U * ceil_div(strip_groups<EPI, 2, 2>(a), FB_CUS), launch_strip<EPI, 2, 2>);
   offer(6 * U * ceil_div(strip_groups<EPI, 4, 2>(a), FB_CUS), launch_strip<EPI, 4, 2>);
   offer(8 * U * ceil_div(strip_groups<EPI, 4, 4>(a), FB_CUS), launch_strip<EPI, 4, 4>);
-  if (FbTiles<EPI, 4, 2, 2>(a).rounds() == 1) offer(EXACT ? 540 : 380, launch_tiles<EPI, 4, 2, 2>);
-  offer(FbTiles<EPI, 4, 4, 3>(a).rounds() * (EXACT ? 770 : 470), launch_tiles<EPI, 4, 4, 3>);
+  // whole rounds and, where the last one is of halves, that
+  auto rounds = [](const FbItems& n, int64_t whole, int64_t halves) {
+    return ceil_div(n.full, FB_CUS / 8) * whole + (n.items > n.full ? halves : 0);
+  };
+  if (tile_items<EPI, 4, 2, 2>(a).per <= FB_CUS / 8)
+    offer(EXACT ? 540 : 380, launch_tiles<EPI, 4, 2, 2>);
+  offer(rounds(tile_items<EPI, 4, 4, 3>(a), EXACT ? 770 : 470, EXACT ? 480 : 300), launch_tiles<EPI, 4, 4, 3>);
   if constexpr (!EXACT)
-    offer(FbTiles<EPI, 8, 4, 2>(a).rounds() * 750, launch_tiles<EPI, 8, 4, 2>);
+    offer(rounds(tile_items<EPI, 8, 4, 2>(a), 750, 520), launch_tiles<EPI, 8, 4, 2>);
   return best(a, s);
 }
 
