@@ -458,7 +458,8 @@ typedef struct tq_fp8b128_layer {
  *   x       device bf16 [rows][n], 16-byte aligned; n a multiple of 16 up to 2^20.
  *   codes   device uint8 [rows][n], 16-byte aligned.
  *   scales  device fp32 [rows][ceil(n / 128)].
- * Here and below a call's rows times their longest width must not exceed 2^33 elements.
+ * Here and below a call's rows times their longest width, in whole blocks of 128, must not
+ * exceed 2^33 elements, and no output may overlap an input or another output.
  */
 int fp8b128_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, float* scales,
                      void* stream);
@@ -505,7 +506,6 @@ int fp8b128_gated(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const floa
  *        writes them, else rounded.
  *   ws   device workspace of tq_fp8b128_workspace_bytes(T, L->out, L->in) bytes, 256-byte
  *        aligned; need not be cleared. Calls that share one must be ordered on one stream.
- * No output may overlap an input.
  */
 int fp8b128_gemm_backward(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs,
                           int64_t T, const void* dy, void* dx, void* dw, void* ws,

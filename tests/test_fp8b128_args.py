@@ -91,7 +91,9 @@ def test_no_tokens_is_a_no_op(lib):
 
 def test_quantize_arguments(lib):
     q = lib.fp8b128_quantize
-    for rows, n in ((-1, 128), (4, 0), (4, -16), (4, 24), (4, (1 << 20) + 16), (1 << 24, 1 << 10)):
+    for rows, n in ((-1, 128), (4, 0), (4, -16), (4, 24), (4, (1 << 20) + 16), (1 << 24, 1 << 10),
+                    # a block of 128 has its threads however few inputs it holds
+                    ((1 << 26) + 1, 16), ((1 << 25) + 1, 144)):
         assert q(P, rows, n, P, P, None) == _lib.TQ_EINVAL, (rows, n)
     assert q(0, 4, 128, P, P, None) == _lib.TQ_EINVAL
     assert q(P, 4, 128, 0, P, None) == _lib.TQ_EINVAL
@@ -116,6 +118,10 @@ def test_ffn_arguments(lib):
     need = lib.tq_fp8b128_ffn_workspace_bytes(2, 512, 128)
     assert ffn(g, d, nbytes=need - 1) == _lib.TQ_EWORKSPACE
     assert lib.tq_fp8b128_ffn_workspace_bytes(-1, 512, 128) == 0
+    for T in ((1 << 24) + 1, 1 << 62):  # more than a call takes
+        assert lib.tq_fp8b128_ffn_workspace_bytes(T, 512, 128) == 0
+        assert lib.tq_fp8b128_workspace_bytes(T, 512, 128) == 0
+    assert lib.tq_fp8b128_workspace_bytes(4, 512, 1 << 21) == 0
 
 
 def test_wrappers_refuse_host_tensors():

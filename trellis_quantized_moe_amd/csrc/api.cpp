@@ -1260,7 +1260,8 @@ int trellis_expert_ffn(const tq_trellis_layer* gate_up, const tq_trellis_layer* 
 // ---- the fp8b128 store ---------------------------------------------------------------------
 namespace {
 
-// Elements of one operand or result of a call: keeps every grid below 2^32 threads.
+// Elements of one operand or result of a call, a row counted in whole blocks of 128 (which have
+// threads of their own): keeps every grid below 2^32 threads.
 constexpr int64_t FB_MAX_ELEMENTS = (int64_t)1 << 33;
 constexpr int FB_MAX_DIM = 1 << 20;
 
@@ -1287,11 +1288,15 @@ int check_gated(const tq_fp8b128_layer* L) {
   return TQ_OK;
 }
 
+bool tokens_fit(int64_t T, int64_t width) {
+  return T >= 0 && T <= FB_MAX_ELEMENTS / ((width + 127) / 128 * 128);
+}
+
 int check_tokens(int64_t T, int64_t width) {
   if (T < 0) return fail(TQ_EINVAL, "T = %lld is negative", (long long)T);
-  if (T > FB_MAX_ELEMENTS / width)
-    return fail(TQ_EINVAL, "T = %lld rows of %lld exceed 2^33 elements", (long long)T,
-                (long long)width);
+  if (!tokens_fit(T, width))
+    return fail(TQ_EINVAL, "T = %lld rows of %lld (in whole blocks of 128) exceed 2^33 elements",
+                (long long)T, (long long)width);
   return TQ_OK;
 }
 
@@ -1446,7 +1451,8 @@ int fp8b128_gated(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const floa
 }
 
 size_t tq_fp8b128_workspace_bytes(int64_t T, int32_t out, int32_t in) {
-  if (T < 0 || out < 16 || in < 16) return 0;
+  if (out < 16 || out > FB_MAX_DIM || in < 16 || in > FB_MAX_DIM) return 0;
+  if (!tokens_fit(T, std::max(out, in))) return 0;
   return fp8b128_ws(T, out, in).total;
 }
 
@@ -1523,7 +1529,8 @@ Fp8b128FfnWs fp8b128_ffn_ws(int64_t T, int H, int I) {
 }  // namespace
 
 size_t tq_fp8b128_ffn_workspace_bytes(int64_t T, int32_t H, int32_t I) {
-  if (T < 0 || H < 16 || I < 16) return 0;
+  if (H < 16 || H > FB_MAX_DIM || I < 16 || I > FB_MAX_DIM / 2) return 0;
+  if (!tokens_fit(T, std::max(H, 2 * I))) return 0;
   return fp8b128_ffn_ws(T, H, I).total;
 }
 
