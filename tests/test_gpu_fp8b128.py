@@ -415,6 +415,75 @@ def test_two_streams_and_repeats_give_the_same_bits():
             assert torch.equal(a, b)
 
 
+def test_a_layer_follows_its_tensors():
+    # tensors given other memory are found and checked again; one that does not fit is refused
+    o = ops()
+    c, other = Inputs(990, 6, 96, 272), Inputs(991, 6, 64, 400)
+    L = o.Fp8b128Layer(c.layer.codes.clone(), c.layer.scales.clone())
+    ref = o.fp8b128_gemm(c.layer, c.xq, c.xs)
+    assert torch.equal(ref, o.fp8b128_gemm(L, c.xq, c.xs))
+    L.codes.data, L.scales.data = other.layer.codes, other.layer.scales
+    assert torch.equal(o.fp8b128_gemm(L, other.xq, other.xs),
+                       o.fp8b128_gemm(other.layer, other.xq, other.xs))
+    dy = bf16_dev(grads_of(6, 64, 64))
+    assert torch.equal(o.fp8b128_gemm_backward(L, other.xq, other.xs, dy)[1],
+                       o.fp8b128_gemm_backward(other.layer, other.xq, other.xs, dy)[1])
+    L.codes.data = c.layer.codes.clone()
+    with pytest.raises(ValueError):
+        o.fp8b128_gemm(L, c.xq, c.xs)
+    L.scales.data = c.layer.scales.clone()
+    assert torch.equal(ref, o.fp8b128_gemm(L, c.xq, c.xs))
+
+
+@pytest.mark.parametrize("out,inp", [(32, 2064), (2080, 16)])
+def test_offsets_past_32_bits(out, inp):
+    # 2^21 + 37 tokens: the bytes of codes (or of the results), and with 2,064 inputs (2,080
+    # outputs) the elements too, pass 2^32. The tokens are zero (padding) up to the last 70.
+    o = ops()
+    T, n = (1 << 21) + 37, 70
+    c, I = Inputs(992, n, out, inp), out // 2
+    x = torch.zeros((T, inp), dtype=torch.bfloat16, device=dev())
+    x[-n:] = (torch.from_numpy(c.X).to(torch.bfloat16)).to(dev())
+    xq, xs = o.fp8b128_quantize(x)
+    del x
+    xqt, xst = o.fp8b128_quantize(torch.from_numpy(c.X).to(torch.bfloat16).to(dev()))
+    assert torch.equal(xq[-n:], xqt) and torch.equal(xs[-n:], xst)
+    assert not bool(xq[:-n].any()) and bool((xs[:-n] == 1).all())
+    A = np.abs(c.X) @ np.abs(c.W).T
+    ref = c.X @ c.W.T
+    for flags in (0, o.TQ_OUT_BF16):
+        y = o.fp8b128_gemm(c.layer, xq, xs, flags=flags)
+        assert_within(f64_of(y[-n:]), ref, BF16 * np.abs(ref) + FP8_SUM * A if flags
+                      else (inp + inp / 128 + 10) * F32 * A)
+        assert not bool(y[:-n].any())
+        del y
+    h = o.fp8b128_gated(c.layer, xq, xs)
+    assert not bool(h[:-n].any())
+    g, u, eg, eu = sums_and_error(c)
+    href = oracle.fp8b128_gated(c.X, c.W)
+    assert_within(f64_of(h[-n:]), href, BF16 * np.abs(href) + 1.1 * eg * (np.abs(u) + eu)
+                  + np.abs(oracle.silu(g)) * eu + 8 * F32 * np.abs(href) + 2.0 ** -133)
+    del h
+    # padding has no gradient: the sums over the tokens are those of the last ones
+    db = grads_of(n, out, out)
+    dy = torch.zeros((T, out), dtype=torch.bfloat16, device=dev())
+    dy[-n:] = bf16_dev(db)
+    D = oracle.bf16_bits_to_f64(db)
+    dx, dw = o.fp8b128_gemm_backward(c.layer, xq, xs, dy)
+    check_product_grads(f64_of(dx[-n:]), f64_of(dw), D, 0 * D, c.X, c.W)
+    assert not bool(dx[:-n].any())
+    del dx, dw
+    hb = grads_of(n, out, I)
+    dh = torch.zeros((T, I), dtype=torch.bfloat16, device=dev())
+    dh[-n:] = bf16_dev(hb)
+    dx, dw = o.fp8b128_gated_backward(c.layer, xq, xs, dh)
+    a = np.abs(oracle.bf16_bits_to_f64(hb))
+    D = oracle.fp8b128_gated_grads(c.X, c.W, oracle.bf16_bits_to_f64(hb))
+    eD = np.concatenate([a * (1.1 * eu + 0.5 * eg * (np.abs(u) + eu)), a * 1.1 * eg], axis=1)
+    check_product_grads(f64_of(dx[-n:]), f64_of(dw), D, eD + (BF16 + 10 * F32) * (np.abs(D) + eD), c.X, c.W)
+    assert not bool(dx[:-n].any())
+
+
 def test_timing_hook_covers_one_product():
     o = ops()
     c = Inputs(987, 40, 288, 400)

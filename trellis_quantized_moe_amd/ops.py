@@ -322,17 +322,24 @@ class Fp8b128Layer:
         out, in_ = self.codes.shape
         dev = self.codes.device
         _check_rows("scales", self.scales, _F32, dev, (-(-out // 128), -(-in_ // 128)))
-        # made once: the fields cannot be assigned again
         c = _lib.Fp8b128LayerC(out, in_, self.codes.data_ptr(), self.scales.data_ptr())
         self.__dict__.update(out=out, in_=in_, device=dev, _c=c, _ref=ctypes.byref(c))
+
+    def renew(self):
+        """Checks the layer again if a tensor has been given other memory (set_, resize_, an
+        assignment to .data); the fields themselves cannot be assigned again. Every call does
+        this before it uses the C struct."""
+        if self.codes.data_ptr() != self._c.codes or self.scales.data_ptr() != self._c.scales:
+            self.__post_init__()
+
+    def c_struct(self):
+        self.renew()
+        return self._c
 
     @classmethod
     def from_host(cls, layer, device="cuda"):
         return cls(torch.from_numpy(np.ascontiguousarray(layer["codes"], dtype=np.uint8)).to(device),
                    torch.from_numpy(np.ascontiguousarray(layer["scales"], dtype=np.float32)).to(device))
-
-    def c_struct(self):
-        return self._c
 
 
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
@@ -384,6 +391,7 @@ def _check_ws(ws, device, nbytes):
 
 def _check_fp8b128(layer, codes, scales):
     """(T, device) of activations that fit the layer."""
+    layer.renew()
     dev = layer.device
     T = len(codes)
     _check_rows("codes", codes, _E4M3, dev, (T, layer.in_))
@@ -444,9 +452,9 @@ def fp8b128_workspace(T, out, in_, device="cuda"):
     return torch.empty(max(256, n), dtype=torch.uint8, device=device)
 
 
-def _fp8b128_backward(fn, layer, codes, scales, dy, width, need_dx, need_dw, dx, dw, ws):
+def _fp8b128_backward(fn, layer, codes, scales, dy, parts, need_dx, need_dw, dx, dw, ws):
     T, dev = _check_fp8b128(layer, codes, scales)
-    _check_rows("the output's gradient", dy, _BF16, dev, (T, width))
+    _check_rows("the output's gradient", dy, _BF16, dev, (T, layer.out // parts))
     if dx is not None:
         _check_rows("dx", dx, _BF16, dev, (T, layer.in_))
     elif need_dx:
@@ -467,7 +475,7 @@ def fp8b128_gemm_backward(layer, codes, scales, dy, need_dx=True, need_dw=True, 
                           ws=None):
     """(dx bf16 [T, in], dw bf16 [out, in]): the gradients of fp8b128_gemm from dy [T, out];
     None for one that is not needed (see fp8b128_gemm_backward in include/tq.h)."""
-    return _fp8b128_backward("fp8b128_gemm_backward", layer, codes, scales, dy, layer.out,
+    return _fp8b128_backward("fp8b128_gemm_backward", layer, codes, scales, dy, 1,
                              need_dx, need_dw, dx, dw, ws)
 
 
@@ -476,13 +484,15 @@ def fp8b128_gated_backward(layer, codes, scales, dh, need_dx=True, need_dw=True,
     """(dx bf16 [T, in], dw bf16 [2I, in]): the gradients of fp8b128_gated from dh [T, I] and
     the 8-bit activations; None for one that is not needed (see fp8b128_gated_backward in
     include/tq.h)."""
-    return _fp8b128_backward("fp8b128_gated_backward", layer, codes, scales, dh, layer.out // 2,
+    return _fp8b128_backward("fp8b128_gated_backward", layer, codes, scales, dh, 2,
                              need_dx, need_dw, dx, dw, ws)
 
 
 def fp8b128_ffn(gate_up, down, x, flags=0, out=None, ws=None):
     """[T, H]: a dense gated FFN over two fp8b128 projections, fp32 or (TQ_OUT_BF16) bf16 (see
     fp8b128_ffn in include/tq.h)."""
+    gate_up.renew()
+    down.renew()
     dev = gate_up.device
     _check_rows("x", x, _BF16, dev)
     if down.device != dev:
