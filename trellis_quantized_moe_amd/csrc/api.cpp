@@ -1342,7 +1342,8 @@ int timed_forward(const tq::Fp8b128GemmArgs& a, int epi, hipStream_t s, const ch
 }
 
 // The workspace of the backward calls: the gradients of gate and up (bf16 [T][out], the gated
-// call only) and X as bf16 [T][in] (dw).
+// call only), and X as bf16 [T][in] or the sums of ranges of tokens (dw, one or the other). What
+// T tokens need is enough for fewer.
 struct Fp8b128Ws {
   size_t dgu, xw, total;
 };
@@ -1351,7 +1352,7 @@ Fp8b128Ws fp8b128_ws(int64_t T, int out, int in) {
   Fp8b128Ws w{};
   w.dgu = 0;
   w.xw = round_up((size_t)T * out * 2, 256);
-  w.total = w.xw + round_up((size_t)T * in * 2, 256);
+  w.total = w.xw + round_up(std::max((size_t)T * in * 2, tq::fp8b128_dw_part_bytes(T, out, in)), 256);
   return w;
 }
 
@@ -1365,6 +1366,7 @@ int backward_products(const tq_fp8b128_layer* L, const uint8_t* xq, const float*
   a.xs = xs;
   a.dy = dy;
   a.xw = at<uint16_t>(ws, fp8b128_ws(T, L->out, L->in).xw);
+  a.part = reinterpret_cast<float*>(a.xw);
   a.dx = static_cast<uint16_t*>(dx);
   a.dw = static_cast<uint16_t*>(dw);
   a.T = T;

@@ -37,6 +37,16 @@ __device__ __forceinline__ uint32_t fb_pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
+// Sixteen codes times their scale as bf16 (exact for a scale that is a power of two).
+__device__ __forceinline__ void fb_widen(u32x4 c, float s, u32x4 (&out)[2]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const u32x2 v = fb_bf16_of4(c[j]);
+    out[j / 2][j % 2 * 2] = fb_pack_bf16(bf16_lo_to_f32(v.x) * s, bf16_hi_to_f32(v.x) * s);
+    out[j / 2][j % 2 * 2 + 1] = fb_pack_bf16(bf16_lo_to_f32(v.y) * s, bf16_hi_to_f32(v.y) * s);
+  }
+}
+
 // The sum over one block of 128 inputs of the products of two rows' codes, for a 16 x 16 tile:
 // lane (r = l % 16, q = l / 16) holds bytes 16 q .. 16 q + 15 and 64 + 16 q .. 64 + 16 q + 15
 // of row r of A and of row r of B; result element i is D[4 q + i][r].

@@ -387,7 +387,7 @@ __global__ __launch_bounds__(512) void fp8b128_dx_kernel(Fp8b128BackwardArgs a, 
   dx_tiles(a, sh, items);
 }
 
-// ---- dw -------------------------------------------------------------------------------------
+// ---- dw, many tokens ------------------------------------------------------------------------
 //
 // X as bf16 [T][in] (exact for scales that are powers of two), once per call: every channel
 // tile of the product reads it.
@@ -401,12 +401,7 @@ __global__ __launch_bounds__(256) void fp8b128_widen_kernel(const uint8_t* __res
   const float s = xs[t * nb + (int)(k % per) / 8];
   const u32x4 c = *reinterpret_cast<const u32x4*>(x + 16 * k);
   u32x4 out[2];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const u32x2 v = fb_bf16_of4(c[j]);
-    out[j / 2][j % 2 * 2] = fb_pack_bf16(bf16_lo_to_f32(v.x) * s, bf16_hi_to_f32(v.x) * s);
-    out[j / 2][j % 2 * 2 + 1] = fb_pack_bf16(bf16_lo_to_f32(v.y) * s, bf16_hi_to_f32(v.y) * s);
-  }
+  fb_widen(c, s, out);
   y[2 * k] = out[0];
   y[2 * k + 1] = out[1];
 }
@@ -534,6 +529,175 @@ __global__ __launch_bounds__(512) void fp8b128_dw_kernel(Fp8b128BackwardArgs a, 
     dw_tile<2>(a, sh, 128 * o + 64 * half, 256 * i);
 }
 
+// ---- dw, few tokens or few tiles ------------------------------------------------------------
+//
+// A workgroup of four waves owns 128 inputs of 128 channels and one of `splits` ranges of the
+// tokens, wave (wi, wo) 64 inputs of 64 channels. X is widened on its way from registers to LDS, so
+// that there is no launch before this one; the next step's loads are in flight while a step's
+// products are made, and a second workgroup on the compute unit fills the waits. With several
+// ranges the sums go to the workspace in fp32, and a second launch adds them in order.
+struct DwRange {
+  alignas(16) uint8_t x[2][64 * 256];
+  alignas(16) uint8_t d[2][64 * 256];
+};
+
+__device__ void dw_range(const Fp8b128BackwardArgs& a, DwRange& sh) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = w & 1, wo = w >> 1;
+  const int ti = (a.in + 127) / 128, to = (a.out + 127) / 128;
+  const int tile = blockIdx.x % (ti * to), split = blockIdx.x / (ti * to);
+  const int i0 = tile % ti * 128, o0 = tile / ti * 128;
+  const int nsteps = (int)((a.T + 63) / 64);
+  const int per = (nsteps + a.splits - 1) / a.splits, first = split * per, last = min(first + per, nsteps);
+  // this thread's 16-byte pieces of a step: two of the codes (32 bytes of bf16, a chunk of the
+  // LDS row), four of dy
+  const int xrow = threadIdx.x >> 3, xcol = i0 + 16 * (threadIdx.x & 7);
+  const int drow = threadIdx.x >> 4, dcol = o0 + 8 * (threadIdx.x & 15);
+  u32x4 cx[2], cd[4];
+  float cs[2];
+  auto load = [&](int k) {
+    const int64_t t = (int64_t)64 * k;
+    const int left = k < last ? (int)min((int64_t)64, a.T - t) : 0;
+    const int64_t at = left > 0 ? t : 0;
+    const GemmRsrc rx = gemm_rsrc(a.x + at * a.in, (uint32_t)left * (uint32_t)a.in);
+    const GemmRsrc rs = gemm_rsrc(a.xs + at * a.nb, (uint32_t)(left * a.nb) * 4u);
+    const GemmRsrc rd = gemm_rsrc(a.dy + at * a.out, (uint32_t)left * (uint32_t)a.out * 2u);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // outside the resource: zeros
+      const int row = xrow + 32 * j;
+      cx[j] = __builtin_amdgcn_raw_buffer_load_b128(
+          rx, xcol < a.in ? (uint32_t)row * (uint32_t)a.in + xcol : FB_OOB, 0, 0);
+      cs[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          rs, xcol < a.in ? (uint32_t)(row * a.nb + i0 / 128) * 4u : FB_OOB, 0, 0));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      cd[j] = __builtin_amdgcn_raw_buffer_load_b128(
+          rd, dcol < a.out ? ((uint32_t)(drow + 16 * j) * (uint32_t)a.out + dcol) * 2u : FB_OOB, 0, 0);
+  };
+  auto store = [&](int st) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = xrow + 32 * j;
+      u32x4 v[2];
+      fb_widen(cx[j], cs[j], v);
+      u32x4* p = reinterpret_cast<u32x4*>(&sh.x[st][256 * row + 32 * ((threadIdx.x & 7) ^ dw_swizzle(row))]);
+      p[0] = v[0];
+      p[1] = v[1];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = drow + 16 * j, c = threadIdx.x & 15;
+      *reinterpret_cast<u32x4*>(&sh.d[st][256 * row + 32 * ((c >> 1) ^ dw_swizzle(row)) + 16 * (c & 1)]) = cd[j];
+    }
+  };
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](int st) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // 32 tokens, operands as in dw_tile
+      const int row = 32 * j + 8 * q + (r >> 2), sw = dw_swizzle(row);
+      auto read = [&](const uint8_t* l, int chunk) {
+        const uint8_t* p = l + 256 * row + 32 * (chunk ^ sw) + 8 * (r & 3);
+        const u32x2 lo = read_tr16(p), hi = read_tr16(p + 4 * 256);
+        return (u32x4){lo.x, lo.y, hi.x, hi.y};
+      };
+      u32x4 bv[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) bv[t] = read(sh.d[st], 4 * wo + t);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const u32x4 av = read(sh.x[st], 4 * wi + c);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[c][t] = mfma_bf16(av, bv[t], acc[c][t]);
+      }
+    }
+  };
+  load(first);
+  for (int k = first; k < last; k += 2) {
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+      if (k + st < last) {
+        store(st);  // the readers of two steps ago have passed the last step's barrier
+        load(k + st + 1);
+        __syncthreads();
+        multiply(st);
+      }
+  }
+  __syncthreads();
+  const int o = o0 + 64 * wo, i = i0 + 64 * wi;
+  if (a.splits == 1) {
+    store_tile((w < 2 ? sh.x[0] : sh.d[0]) + 4096 * (w & 1), acc,
+               reinterpret_cast<uint8_t*>(a.dw + (int64_t)o * a.in + i), (int64_t)a.in * 2, a.out - o, (a.in - i) * 2);
+    return;
+  }
+  float* part = a.part + (int64_t)split * a.out * a.in;
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int row = o + 16 * t + r, col = i + 16 * c + 4 * q;
+      if (row < a.out && col < a.in) *reinterpret_cast<f32x4*>(part + (int64_t)row * a.in + col) = acc[c][t];
+    }
+}
+
+__global__ __launch_bounds__(256, 2) void fp8b128_dw_range_kernel(Fp8b128BackwardArgs a) {
+  __shared__ DwRange sh;
+  dw_range(a, sh);
+}
+
+__global__ __launch_bounds__(256) void fp8b128_dw_join_kernel(const f32x4* __restrict__ part, int64_t n4,
+                                                              int splits, uint16_t* __restrict__ dw) {
+  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;  // four results
+  if (k >= n4) return;
+  f32x4 sum = part[k];
+  for (int s = 1; s < splits; ++s) sum += part[s * n4 + k];
+  store4(dw + 4 * k, sum);
+}
+
+// Ranges of tokens of the dw of few tiles: as many workgroups as two on every compute unit, of one
+// step of 64 tokens at least.
+int dw_most_splits(int64_t T, int out, int in) {
+  const int64_t tiles = ceil_div(out, 128) * ceil_div(in, 128);
+  return (int)std::max((int64_t)1, std::min(ceil_div(T, 64), 2 * FB_CUS / tiles));
+}
+
+// How dw is computed: X widened first (0), or the number of ranges; whichever has the least time
+// expected (0.01 us):
+//   widened  500, the widening of 3 bytes an input at 5 TB/s, and for each round of tiles over the
+//            compute units 450 + 87 a step of 64 tokens, for a round of halves 200 + 51 a step
+//   ranges   400, for each round of two workgroups on every compute unit 230 + 133 a step, of one
+//            80 + 90; with several ranges 300 and 8 bytes a result and range at 5 TB/s
+// Measured, widened / one range / the best number of ranges: 64 tokens x 5,120 x 1,536 10.9 / 8.4
+// us, x 5,120 x 4,096 20.2 / 15.0; 512 x 5,120 x 4,096 39.1 / 39.2; 2,048 x 5,120 x 1,536 45.8 /
+// 50.5; 2,048 x 768 x 768 26.2 / 33.6 / 19.9 (4); 8,192 x 256 x 64 71 / 117 / 18.3 (16), x 768 x
+// 768 74.7 / 119 / 31.0 (14), x 768 x 5,120 92.1 / 129 / 109 (2).
+int dw_splits(const Fp8b128BackwardArgs& a) {
+  const FbItems items((a.out + 127) / 128, (a.in + 255) / 256);
+  const int64_t steps = ceil_div(a.T, 64), results = (int64_t)a.out * a.in;
+  const int64_t tiles = ceil_div(a.out, 128) * ceil_div(a.in, 128);
+  const int most = dw_most_splits(a.T, a.out, a.in);
+  int64_t least = 500 + a.T * a.in * 3 / 50000 + ceil_div(items.full, FB_CUS / 8) * (450 + 87 * steps) +
+                  (items.items > items.full ? 200 + 51 * steps : 0);
+  int best = 0;
+  for (int s = 1; s <= most; s += std::max(1, s / 2)) {
+    const int64_t n = ceil_div(steps, s), k = ceil_div(steps, n);  // steps of a range, ranges with any
+    const int64_t two = 230 + 133 * n, rest = tiles * k % (2 * FB_CUS);
+    const int64_t cost = 400 + tiles * k / (2 * FB_CUS) * two +
+                         (rest > FB_CUS ? two : rest > 0 ? 80 + 90 * n : 0) +
+                         (k > 1 ? 300 + k * results * 8 / 50000 : 0);
+    if (cost < least) {
+      least = cost;
+      best = (int)k;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 // The kernel with the least time expected, by the rounds of workgroups over the compute units and
@@ -558,7 +722,24 @@ hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& a, hipStream_t s) {
+size_t fp8b128_dw_part_bytes(int64_t T, int out, int in) {
+  const int s = dw_most_splits(T, out, in);
+  return s > 1 ? (size_t)s * out * in * 4 : 0;
+}
+
+hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& args, hipStream_t s) {
+  Fp8b128BackwardArgs a = args;
+  a.splits = dw_splits(a);
+  if (a.splits > 0) {
+    const int64_t tiles = ceil_div(a.out, 128) * ceil_div(a.in, 128);
+    hipLaunchKernelGGL(fp8b128_dw_range_kernel, dim3((unsigned)(tiles * a.splits)), dim3(256), 0, s, a);
+    if (a.splits > 1) {
+      const int64_t n4 = (int64_t)a.out * a.in / 4;
+      hipLaunchKernelGGL(fp8b128_dw_join_kernel, dim3((unsigned)ceil_div(n4, 256)), dim3(256), 0, s,
+                         reinterpret_cast<const f32x4*>(a.part), n4, a.splits, a.dw);
+    }
+    return hipGetLastError();
+  }
   const int64_t n16 = a.T * (a.in / 16);
   hipLaunchKernelGGL(fp8b128_widen_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, s, a.x,
                      a.xs, n16, a.in, a.nb, reinterpret_cast<u32x4*>(a.xw));

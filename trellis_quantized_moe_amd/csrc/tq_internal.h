@@ -327,7 +327,9 @@ struct Fp8b128BackwardArgs {
   const uint8_t* x;
   const float* xs;
   const uint16_t* dy;  // bf16 [T][out]
-  uint16_t* xw;        // workspace of dw: X as bf16 [T][in]
+  uint16_t* xw;        // workspace of dw: X as bf16 [T][in], or
+  float* part;         // the sums of ranges of tokens, fp32 [splits][out][in]
+  int splits;
   uint16_t* dx;        // bf16 [T][in]
   uint16_t* dw;        // bf16 [out][in]
   int64_t T;
@@ -335,6 +337,8 @@ struct Fp8b128BackwardArgs {
 };
 hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s);
 hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& a, hipStream_t s);
+// Bytes of `part` that T or fewer tokens take at most.
+size_t fp8b128_dw_part_bytes(int64_t T, int out, int in);
 hipError_t launch_fp8b128_quantize(const uint16_t* x, int64_t rows, int n, uint8_t* codes,
                                    float* scales, hipStream_t s);
 hipError_t launch_nvfp4_transcode(const uint8_t* units, int E, int out, int in,
