@@ -37,10 +37,11 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
 
 // ---- dx, few tokens: strips of inputs, the outputs split over a workgroup's waves ------------
 //
-// A workgroup owns NS strips of 16 inputs (64 bytes of a row of codes) of up to 16 * TT tokens. Its W waves take the blocks of 128 outputs in turn, in two steps of 64, each
-// with D stages of LDS of its own that its loads fill D - 1 steps ahead (no barrier until the
-// end). A block's products are added from zero and then scaled into the sums; the waves' sums
-// are added in wave order.
+// A workgroup owns NS strips of 16 inputs (64 bytes of a row of codes) of up to 16 * TT tokens. Its
+// W waves take the blocks of 128 outputs in turn, in two steps of 64, each with D stages of LDS of
+// its own that its loads fill D - 1 steps ahead (no barrier until the end). A block's products are added from zero and then scaled into the sums; the waves' sums
+// are added in wave order. 32 tokens x 5,120 inputs x 4,096 outputs take 10.5 us, 2 TB/s of codes;
+// with neighbouring strips on different XCDs, each reading the lines they share, it was 17.3.
 template <int NS, int TT>
 struct DxStrip {
   static constexpr int IW = 16 * NS, W = TT <= 2 ? 8 : 4, D = TT <= 2 ? 2 : 3;
@@ -59,9 +60,12 @@ __device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStrip<NS, TT>& sh) {
   using S = DxStrip<NS, TT>;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int cols = (a.in + S::IW - 1) / S::IW;
-  const int i0 = (int)(blockIdx.x % cols) * S::IW;
-  const int64_t t0 = (int64_t)(blockIdx.x / cols) * (16 * TT);
+  // an XCD (workgroup b belongs to b % 8) has all tokens of consecutive strips: they read the same
+  // codes, and neighbouring strips the same lines of them
+  const int tiles = (int)((a.T + 16 * TT - 1) / (16 * TT)), groups = gridDim.x, x = blockIdx.x & 7;
+  const int g = x * (groups >> 3) + min(x, groups & 7) + (blockIdx.x >> 3);
+  const int i0 = g / tiles * S::IW;
+  const int64_t t0 = (int64_t)(g % tiles) * (16 * TT);
   const int rows = (int)min((int64_t)(16 * TT), a.T - t0);
   const int nob = (a.out + 127) / 128;
   const GemmRsrc rd = gemm_rsrc(a.dy + t0 * a.out, (uint32_t)rows * (uint32_t)a.out * 2u);
@@ -181,6 +185,7 @@ template <int NS, int TT>
 int64_t dx_strip_groups(const Fp8b128BackwardArgs& a) {  // workgroups
   return ceil_div(a.in, 16 * NS) * ceil_div(a.T, 16 * TT);
 }
+
 template <int NS, int TT>
 hipError_t launch_dx_strip(const Fp8b128BackwardArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((fp8b128_dx_strip_kernel<NS, TT>), dim3((unsigned)dx_strip_groups<NS, TT>(a)),
@@ -650,11 +655,13 @@ __global__ __launch_bounds__(256, 2) void fp8b128_dw_range_kernel(Fp8b128Backwar
   dw_range(a, sh);
 }
 
+// The sums of the ranges, one after the other, as bf16: four results a thread.
 __global__ __launch_bounds__(256) void fp8b128_dw_join_kernel(const f32x4* __restrict__ part, int64_t n4,
                                                               int splits, uint16_t* __restrict__ dw) {
-  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;  // four results
+  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (k >= n4) return;
   f32x4 sum = part[k];
+#pragma unroll 4
   for (int s = 1; s < splits; ++s) sum += part[s * n4 + k];
   store4(dw + 4 * k, sum);
 }
@@ -671,7 +678,7 @@ int dw_most_splits(int64_t T, int out, int in) {
 //   widened  500, the widening of 3 bytes an input at 5 TB/s, and for each round of tiles over the
 //            compute units 450 + 87 a step of 64 tokens, for a round of halves 200 + 51 a step
 //   ranges   400, for each round of two workgroups on every compute unit 230 + 133 a step, of one
-//            80 + 90; with several ranges 300 and 8 bytes a result and range at 5 TB/s
+//            80 + 90; with several ranges 300 and for each 15 and 8 bytes a result at 5 TB/s
 // Measured, widened / one range / the best number of ranges: 64 tokens x 5,120 x 1,536 10.9 / 8.4
 // us, x 5,120 x 4,096 20.2 / 15.0; 512 x 5,120 x 4,096 39.1 / 39.2; 2,048 x 5,120 x 1,536 45.8 /
 // 50.5; 2,048 x 768 x 768 26.2 / 33.6 / 19.9 (4); 8,192 x 256 x 64 71 / 117 / 18.3 (16), x 768 x
@@ -689,7 +696,7 @@ int dw_splits(const Fp8b128BackwardArgs& a) {
     const int64_t two = 230 + 133 * n, rest = tiles * k % (2 * FB_CUS);
     const int64_t cost = 400 + tiles * k / (2 * FB_CUS) * two +
                          (rest > FB_CUS ? two : rest > 0 ? 80 + 90 * n : 0) +
-                         (k > 1 ? 300 + k * results * 8 / 50000 : 0);
+                         (k > 1 ? 300 + k * (15 + results * 8 / 50000) : 0);
     if (cost < least) {
       least = cost;
       best = (int)k;
@@ -705,7 +712,8 @@ int dw_splits(const Fp8b128BackwardArgs& a) {
 // 230, a round of halves of tiles 135. Measured where two meet, for 5,120 inputs: 32 tokens 5.8 us
 // by (4, 1), 6.3 by (4, 2); 128 tokens 10.7 by (4, 2), 9.8 by (4, 4); 512 tokens 23.9 by (4, 4),
 // 26.8 by whole tiles, 19.0 by halves; 768 tokens 31.0, 28.2 and 20.9. (768 inputs x 5,120
-// outputs, 333 tokens: 13.2 by (4, 1), 67 by whole tiles.)
+// outputs, 256 tokens: 11.6 by (4, 1), 44 by halves. 5,120 x 4,096, 32 tokens: 10.6 by (4, 1),
+// 12.1 by (4, 2).)
 hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s) {
   const int64_t tt = ceil_div(a.T, 128), ti = ceil_div(a.in, 256);
   const int64_t s1 = 31 * ceil_div(dx_strip_groups<4, 1>(a), FB_CUS);

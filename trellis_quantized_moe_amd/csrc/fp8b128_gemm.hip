@@ -166,9 +166,12 @@ __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int width = GATED ? a.out / 2 : a.out;
-  const int groups = (width + 16 * NO - 1) / (16 * NO);
-  const int c0 = (int)(blockIdx.x % groups) * (16 * NO);
-  const int64_t t0 = (int64_t)(blockIdx.x / groups) * (16 * TT);
+  // an XCD (workgroup b belongs to b % 8) has all tokens of consecutive strips, which read the same
+  // codes
+  const int tiles = (int)((a.T + 16 * TT - 1) / (16 * TT)), all = gridDim.x, x = blockIdx.x & 7;
+  const int g = x * (all >> 3) + min(x, all & 7) + (blockIdx.x >> 3);
+  const int c0 = g / tiles * (16 * NO);
+  const int64_t t0 = (int64_t)(g % tiles) * (16 * TT);
   const int rows = (int)min((int64_t)(16 * TT), a.T - t0);
 
   const GemmRsrc rw = gemm_rsrc(a.w, (uint32_t)a.out * (uint32_t)a.in);
