@@ -393,7 +393,7 @@ def _check_fp8b128(layer, codes, scales):
     """(T, device) of activations that fit the layer."""
     layer.renew()
     dev = layer.device
-    T = len(codes)
+    T = codes.shape[0]
     _check_rows("codes", codes, _E4M3, dev, (T, layer.in_))
     _check_rows("scales", scales, _F32, dev, (T, -(-layer.in_ // 128)))
     return T, dev
