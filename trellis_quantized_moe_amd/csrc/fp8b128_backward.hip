@@ -217,20 +217,21 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, const f32x4 (&acc)[4][N
 // ---- dx, many tokens ------------------------------------------------------------------------
 //
 // A workgroup of eight waves owns 256 inputs of 128 tokens (half an item: of 64), wave (wi, wt) 64
-// inputs of 64 (32) tokens. Steps of 64 outputs: 64 rows of 256 code bytes and 128 rows of 128 bytes of dy go
-// straight to a ring of four LDS stages, three steps ahead. The products of two steps (one block
-// of 128 outputs) are added from zero and then scaled into the sums.
+// inputs of 64 (32) tokens. Per block of 128 outputs, 128 rows of 256 code bytes and 128 rows of
+// 256 bytes of dy go straight to one of two LDS stages. A wave takes the block strip by strip of 16
+// inputs: the strip's codes become bf16 once, its products with the block's dy (in registers for
+// all strips) are added from zero, and the strip before it is scaled into its sums meanwhile.
 struct DxShared {
-  alignas(16) uint8_t w[4][64 * 256];
-  alignas(16) uint8_t d[4][128 * 128];
+  alignas(16) uint8_t w[2][128 * 256];
+  alignas(16) uint8_t d[2][128 * 256];
 };
 
-// One workgroup per compute unit takes tile after tile: the first steps of the next tile are
+// One workgroup per compute unit takes tile after tile: the first block of the next tile is
 // loading while a tile's results are stored.
 struct DxTile {
   int64_t t0;
   int rows, i0, ib;
-  uint32_t wo[2], dof[2];
+  uint32_t wo[4], dof[4];
 };
 
 // The tile, or one half of its tokens.
@@ -242,15 +243,13 @@ __device__ __forceinline__ DxTile dx_tile_at(const Fp8b128BackwardArgs& a, int t
   d.rows = (int)max(min((int64_t)(half < 0 ? 128 : 64), a.T - d.t0), (int64_t)0);
   d.i0 = tile_i * 256;
   d.ib = min((d.i0 + 64 * (w & 3)) / 128, a.nb - 1);
-  // codes: an instruction fills 4 rows; lane l position l % 16 of row l / 16, which holds the
-  // row's 16-byte chunk (l % 16) ^ (row % 16). dy: 8 rows; position l % 8 of row l / 8 holds
-  // chunk (l % 8) ^ (row % 8).
+  // an instruction fills 4 rows; lane l position l % 16 of row l / 16, which holds the row's
+  // 16-byte chunk (l % 16) ^ (row % 16)
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int row = 8 * w + 4 * j + (lane >> 4), col = d.i0 + 16 * ((lane & 15) ^ (row & 15));
-    d.wo[j] = col < a.in ? (uint32_t)row * (uint32_t)a.in + col : FB_OOB;
-    const int tok = 16 * w + 8 * j + (lane >> 3);
-    d.dof[j] = tok < d.rows ? (uint32_t)tok * (uint32_t)a.out * 2u + 16u * ((lane & 7) ^ (lane >> 3)) : FB_OOB;
+  for (int j = 0; j < 4; ++j) {
+    const int row = 16 * w + 4 * j + (lane >> 4), chunk = (lane & 15) ^ (row & 15);
+    d.wo[j] = d.i0 + 16 * chunk < a.in ? (uint32_t)row * (uint32_t)a.in + d.i0 + 16 * chunk : FB_OOB;
+    d.dof[j] = row < d.rows ? (uint32_t)row * (uint32_t)a.out * 2u + 16u * chunk : FB_OOB;
   }
   return d;
 }
@@ -259,110 +258,117 @@ __device__ void dx_tiles(const Fp8b128BackwardArgs& a, DxShared& sh, const FbIte
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = w & 3, wt = w >> 2;
-  const int nsteps = (a.out + 63) / 64;
-  const int dcol = 8 * ((lane & 7) ^ (lane >> 3));  // this lane's first output of a step
-  constexpr int LOADS = 4;  // of one step; the scales come through the scalar cache
+  const int nob = (a.out + 127) / 128;
+  const int dcol = 8 * ((lane & 15) ^ (lane >> 4));  // of part 0; of part n it is dcol ^ 32 n
+  constexpr int LOADS = 8, PER = 4;  // of one block; issued at a time
   DxTile d;
-  // A step's loads, in four parts (a wave cannot go on while the memory unit's queue is full, so
-  // they are issued between the products); steps past the last are read as zeros.
+  // A block's loads, in parts (a wave cannot go on while the memory unit's queue is full, so
+  // they are issued between the products); blocks past the last are read as zeros.
   auto load = [&](int n, int st, int k) {
-    const int left = min(64, a.out - 64 * k);
-    if (n < 2) {
-      const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 64 * k : 0) * a.in,
+    const int left = min(128, a.out - 128 * k);
+    if (n < 4) {
+      const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 128 * k : 0) * a.in,
                                     left > 0 ? (uint32_t)left * (uint32_t)a.in : 0u);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][256 * (8 * w + 4 * n)]), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&sh.w[st][256 * (16 * w + 4 * n)]), 16,
                                                d.wo[n], 0, 0, 0);
     } else {
       const GemmRsrc rd = gemm_rsrc(a.dy + d.t0 * a.out, (uint32_t)d.rows * (uint32_t)a.out * 2u);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][128 * (16 * w + 8 * (n - 2))]), 16,
-                                               dcol < left ? d.dof[n - 2] : FB_OOB, 128u * k, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&sh.d[st][256 * (16 * w + 4 * (n - 4))]), 16,
+                                               (dcol ^ (32 * (n - 4))) < left ? d.dof[n - 4] : FB_OOB,
+                                               256u * k, 0, 0);
     }
-  };
-
-  auto load_steps = [&](int first, int last) {
-#pragma unroll
-    for (int k = first; k < last; ++k)
-#pragma unroll
-      for (int n = 0; n < 4; ++n) load(n, k, k);
   };
 
   int tile_t, tile_i, half, j = blockIdx.x >> 3;
   const int stream = blockIdx.x & 7;
   if (!items.at(stream, j, &tile_t, &tile_i, &half)) return;
   d = dx_tile_at(a, tile_t, tile_i, half, w);
-  load_steps(0, 3);
-  // One item, whole (NT = 4 token tiles of 16 per wave) or half (NT = 2): its first steps are
-  // loading; afterwards those of the next item are. Returns whether there is one.
+#pragma unroll
+  for (int n = 0; n < LOADS; ++n) load(n, 0, 0);
+  // One item, whole (NT = 4 token tiles of 16 per wave) or half (NT = 2): its first block is
+  // loading; afterwards that of the next item is. Returns whether there is one.
   auto item = [&](auto tiles) {
     constexpr int NT = decltype(tiles)::value;
-    f32x4 acc[4][NT], p[4][NT];
-    // operands of 32 outputs (half j of a step)
-    u32x2 av[2][4];
-    u32x4 bv[2][NT];
-    auto read = [&](int st, int j) {
+    f32x4 acc[4][NT], p[NT];
+    u32x2 av[2][4];   // of a strip: the codes of 32 outputs each
+    u32x4 bv[NT][4];  // dy of the block
+    auto read_a = [&](int st, int c) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        bv[j][t] = *reinterpret_cast<const u32x4*>(
-            &sh.d[st][128 * (16 * NT * wt + 16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int j = 0; j < 4; ++j) {
         const int row = 32 * j + 8 * q + (r >> 1);
-        av[j][c] = read_tr8(&sh.w[st][256 * row + 16 * ((4 * wi + c) ^ (row & 15)) + 8 * (r & 1)]);
+        av[c & 1][j] = read_tr8(&sh.w[st][256 * row + 16 * ((4 * wi + c) ^ (row & 15)) + 8 * (r & 1)]);
       }
     };
-    auto multiply = [&](int j, bool first, int st, int k) {  // with the loads of step k, if k >= 0
+    auto read_b = [&](int st, int t) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        bv[t][j] = *reinterpret_cast<const u32x4*>(
+            &sh.d[st][256 * (16 * NT * wt + 16 * t + r) + 16 * ((4 * j + q) ^ r)]);
+    };
+    auto add = [&](int c, int t, float s) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[c][t][i] = __builtin_fmaf(p[t][i], s, acc[c][t][i]);
+      asm volatile("" : "+v"(acc[c][t]));  // done here, not where the compiler would gather them
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      p[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int n = 0; n < PER; ++n) load(n, 1, 1);
+    wait_vmcnt<PER>();
+    bare_barrier();
+    read_a(0, 0);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) read_b(0, t);
+    float s = fb_uniform_load(a.ws + d.ib), before = 0.0f;
+    // One block. Before its last strip, whose operands are in registers, the next block has
+    // landed everywhere and this stage is no longer read: its refill starts, and the next block's
+    // operands are read as the last strip's products release the registers.
+    int st = 0;
+    for (int kb = 0; kb < nob; ++kb) {
+      float next_s = 0.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (k >= 0) {
-          __builtin_amdgcn_sched_barrier(0);
-          load(c, st, k);
+        const bool last = c == 3;
+        __builtin_amdgcn_sched_barrier(0);
+        if (last) {
+          wait_vmcnt<0>();
+          bare_barrier();
+          read_a(st ^ 1, 0);
+          next_s = fb_uniform_load(a.ws + (int64_t)min(kb + 1, nob - 1) * a.nb + d.ib);
+        } else {
+          read_a(st, c + 1);
         }
-        const u32x4 a8 = fb_bf16_of8(av[j][c].x, av[j][c].y);
+        if (c == 0)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          p[c][t] = mfma_bf16(a8, bv[j][t], first ? (f32x4){0.f, 0.f, 0.f, 0.f} : p[c][t]);
+          for (int n = PER; n < LOADS; ++n) load(n, st ^ 1, kb + 1);
+        if (last)
+#pragma unroll
+          for (int n = 0; n < PER; ++n) load(n, st, kb + 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const u32x4 a8 = fb_bf16_of8(av[c & 1][j].x, av[c & 1][j].y);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (j == 0) add((c + 3) % 4, t, c == 0 ? before : s);
+            p[t] = mfma_bf16(a8, bv[t][j], j == 0 ? (f32x4){0.f, 0.f, 0.f, 0.f} : p[t]);
+            if (last && j == 3) {
+              __builtin_amdgcn_sched_barrier(0);
+              read_b(st ^ 1, t);
+            }
+          }
+        }
       }
-    };
-    // A step's second half is read while its first half is multiplied, and the next step's first
-    // half while its second is: between the two, the next step's data have landed everywhere,
-    // and this step's stage is no longer read.
-    auto step = [&](int st, int k) {
-      float s = 0.0f;
-      if (st & 1) s = fb_uniform_load(a.ws + (int64_t)(k / 2) * a.nb + d.ib);
-      read(st, 1);
-      multiply(0, (st & 1) == 0, 0, -1);
-      __builtin_amdgcn_sched_barrier(0);
-      wait_vmcnt<2 * LOADS>();
-      bare_barrier();
-      read((st + 1) & 3, 0);
-      multiply(1, false, st, k + 4);
-      if (st & 1) {  // the block of 128 outputs is complete
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[c][t][i] = __builtin_fmaf(p[c][t][i], s, acc[c][t][i]);
-      }
-    };
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    load_steps(3, 4);
-    wait_vmcnt<3 * LOADS>();
-    bare_barrier();
-    read(0, 0);
-    // whole blocks (a step past the last adds zeros)
-    for (int k = 0; k < nsteps; k += 4) {
-      step(0, k);
-      step(1, k + 1);
-      if (k + 2 < nsteps) {
-        step(2, k + 2);
-        step(3, k + 3);
-      }
+      before = s;
+      s = next_s;
+      st ^= 1;
     }
-    // the loads past the last step have landed, and no wave reads a stage any more
+#pragma unroll
+    for (int t = 0; t < NT; ++t) add(3, t, before);
+    // the loads past the last block have landed, and no wave reads a stage any more
     wait_vmcnt<0>();
     bare_barrier();
     uint8_t* dst = reinterpret_cast<uint8_t*>(a.dx + (d.t0 + 16 * NT * wt) * a.in + d.i0 + 64 * wi);
@@ -371,10 +377,11 @@ __device__ void dx_tiles(const Fp8b128BackwardArgs& a, DxShared& sh, const FbIte
     const bool more = items.at(stream, j, &tile_t, &tile_i, &half);
     if (more) {
       d = dx_tile_at(a, tile_t, tile_i, half, w);
-      load_steps(0, 3);
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n) load(n, 0, 0);
     }
-    // through the last stage, which the next item fills after the barrier
-    store_tile(w < 4 ? sh.w[3] + 4096 * w : sh.d[3] + 4096 * (w - 4), acc, dst, (int64_t)a.in * 2, rows, bytes);
+    // through the second stage, which the next item fills after the barrier
+    store_tile(sh.w[1] + 4096 * w, acc, dst, (int64_t)a.in * 2, rows, bytes);
     bare_barrier();
     return more;
   };
