@@ -37,7 +37,9 @@ GATED = [(1, 32, 16), (1, 1536, 5120), (3, 96, 144), (16, 288, 272), (31, 64, 40
 BACKWARD = [(1, 32, 16), (1, 288, 400), (2, 64, 128), (17, 32, 272), (40, 288, 144), (64, 96, 1040),
             (129, 256, 256), (200, 544, 400), (257, 160, 656), (333, 1056, 272), (600, 288, 784), (2100, 352, 2064), (4200, 64, 2320),
             (1000, 3104, 144), (3000, 2848, 144), (2100, 2048, 272),
-            (40, 3104, 2064), (33, 5152, 2064), (265, 8672, 144)]
+            (40, 3104, 2064), (33, 5152, 2064), (265, 8672, 144),
+            # whole and half tiles of the weight gradient
+            (600, 2080, 2064), (420, 2848, 2832)]
 
 
 def bits_of(t):
@@ -393,6 +395,35 @@ def test_replayed_graph_equals_eager(T):
         torch.cuda.synchronize()
         for a, b in zip(out, eager):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,out,inp", [(70, 96, 272), (1100, 64, 272), (500, 1056, 272)])
+def test_two_graphs_share_a_workspace(T, out, inp):
+    # on one stream, in any order: one range of tokens, several, and X widened first
+    o = ops()
+    c = Inputs(993, T, out, inp)
+    dy, dh = bf16_dev(grads_of(T, out, out)), bf16_dev(grads_of(T, out, out // 2))
+    ws = o.fp8b128_workspace(T, out, inp, dev())
+    calls = [lambda: o.fp8b128_gemm_backward(c.layer, c.xq, c.xs, dy, ws=ws),
+             lambda: o.fp8b128_gated_backward(c.layer, c.xq, c.xs, dh, ws=ws)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for call in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call())
+    for k in range(3):
+        dy.copy_(bf16_dev(grads_of(T, out, out)) * (k + 1))
+        dh.copy_(bf16_dev(grads_of(T, out, out // 2)) * (k - 1))
+        for g in (0, 1, 0, 1, 1):
+            graphs[g].replay()
+        eager = [call() for call in calls]
+        graphs[0].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, eager):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_two_streams_and_repeats_give_the_same_bits():
