@@ -10,6 +10,9 @@ Tolerances, per element, from the number formats (a rounding is off by at most h
 The gradients' bounds follow the formulas: errors of g and u times the slopes, dg and du
 rounded to bf16, fp32 sums, a last rounding to bf16."""
 
+import copy
+import pickle
+
 import numpy as np
 import pytest
 
@@ -464,6 +467,17 @@ def test_a_layer_follows_its_tensors():
         o.fp8b128_gemm(L, c.xq, c.xs)
     L.scales.data = c.layer.scales.clone()
     assert torch.equal(ref, o.fp8b128_gemm(L, c.xq, c.xs))
+
+
+def test_layers_are_copied_with_their_tensors():
+    o = ops()
+    c = Inputs(994, 6, 96, 272)
+    ref = o.fp8b128_gemm(c.layer, c.xq, c.xs)
+    L = copy.deepcopy(c.layer)
+    assert L.codes.data_ptr() != c.layer.codes.data_ptr()
+    c.layer.codes.zero_()
+    assert torch.equal(ref, o.fp8b128_gemm(L, c.xq, c.xs))
+    assert torch.equal(ref, o.fp8b128_gemm(pickle.loads(pickle.dumps(L)), c.xq, c.xs))
 
 
 @pytest.mark.parametrize("out,inp", [(32, 2064), (2080, 16)])

@@ -336,6 +336,9 @@ class Fp8b128Layer:
         self.renew()
         return self._c
 
+    def __reduce__(self):
+        return Fp8b128Layer, (self.codes, self.scales)  # copies and pickles hold the tensors alone
+
     @classmethod
     def from_host(cls, layer, device="cuda"):
         return cls(torch.from_numpy(np.ascontiguousarray(layer["codes"], dtype=np.uint8)).to(device),
