@@ -42,7 +42,10 @@ BACKWARD = [(1, 32, 16), (1, 288, 400), (2, 64, 128), (17, 32, 272), (40, 288, 1
             (1000, 3104, 144), (3000, 2848, 144), (2100, 2048, 272),
             (40, 3104, 2064), (33, 5152, 2064), (265, 8672, 144),
             # whole and half tiles of the weight gradient
-            (600, 2080, 2064), (420, 2848, 2832)]
+            (600, 2080, 2064), (420, 2848, 2832),
+            # the two gradients in one launch or apart, in each of their kernels
+            (580, 1056, 144), (580, 64, 1296), (130, 1600, 2064), (310, 1056, 2832), (400, 160, 1296),
+            (580, 160, 2832), (850, 64, 2064), (940, 352, 4112), (4300, 64, 784), (4000, 64, 4112)]
 
 
 def bits_of(t):
@@ -308,6 +311,20 @@ def test_backward_needs():
     ws.fill_(255)  # the workspace need not be cleared
     dx2, dw2 = o.fp8b128_gated_backward(c.layer, c.xq, c.xs, dh, ws=ws)
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("T,out,inp", [(70, 96, 272), (333, 1056, 272), (580, 1056, 144), (580, 64, 1296),
+                                       (420, 2848, 2832), (850, 64, 2064)])
+def test_one_gradient_alone(T, out, inp):
+    c = Inputs(995, T, out, inp)
+    db = grads_of(T, out, out)
+    D = oracle.bf16_bits_to_f64(db)
+    o, dy = ops(), bf16_dev(db)
+    dx, none = o.fp8b128_gemm_backward(c.layer, c.xq, c.xs, dy, need_dw=False)
+    assert none is None
+    none, dw = o.fp8b128_gemm_backward(c.layer, c.xq, c.xs, dy, need_dx=False)
+    assert none is None
+    check_product_grads(f64_of(dx), f64_of(dw), D, 0 * D, c.X, c.W)
 
 
 def test_no_tokens():

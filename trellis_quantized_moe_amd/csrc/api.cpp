@@ -1373,9 +1373,7 @@ int backward_products(const tq_fp8b128_layer* L, const uint8_t* xq, const float*
   a.out = L->out;
   a.in = L->in;
   a.nb = fb_blocks(L->in);
-  hipError_t err = hipSuccess;
-  if (dx) err = tq::launch_fp8b128_dx(a, s);
-  if (err == hipSuccess && dw) err = tq::launch_fp8b128_dw(a, s);
+  hipError_t err = tq::launch_fp8b128_backward(a, s);
   if (err != hipSuccess) return hip_fail(err, "fp8b128 gradient launch");
   return ok();
 }

@@ -55,15 +55,16 @@ struct DxStrip {
   };
 };
 
+// Workgroup `wg` of `groups`.
 template <int NS, int TT>
-__device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStrip<NS, TT>& sh) {
+__device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStrip<NS, TT>& sh, int wg, int groups) {
   using S = DxStrip<NS, TT>;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // an XCD (workgroup b belongs to b % 8) has all tokens of consecutive strips: they read the same
   // codes, and neighbouring strips the same lines of them
-  const int tiles = (int)((a.T + 16 * TT - 1) / (16 * TT)), groups = gridDim.x, x = blockIdx.x & 7;
-  const int g = x * (groups >> 3) + min(x, groups & 7) + (blockIdx.x >> 3);
+  const int tiles = (int)((a.T + 16 * TT - 1) / (16 * TT)), x = wg & 7;
+  const int g = x * (groups >> 3) + min(x, groups & 7) + (wg >> 3);
   const int i0 = g / tiles * S::IW;
   const int64_t t0 = (int64_t)(g % tiles) * (16 * TT);
   const int rows = (int)min((int64_t)(16 * TT), a.T - t0);
@@ -173,24 +174,11 @@ __device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStrip<NS, TT>& sh) {
   }
 }
 
-template <int NS, int TT>
-__global__ __launch_bounds__((64 * DxStrip<NS, TT>::W)) void fp8b128_dx_strip_kernel(Fp8b128BackwardArgs a) {
-  __shared__ DxStrip<NS, TT> sh;
-  dx_strip<NS, TT>(a, sh);
-}
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int NS, int TT>
 int64_t dx_strip_groups(const Fp8b128BackwardArgs& a) {  // workgroups
   return ceil_div(a.in, 16 * NS) * ceil_div(a.T, 16 * TT);
-}
-
-template <int NS, int TT>
-hipError_t launch_dx_strip(const Fp8b128BackwardArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((fp8b128_dx_strip_kernel<NS, TT>), dim3((unsigned)dx_strip_groups<NS, TT>(a)),
-                     dim3(64 * DxStrip<NS, TT>::W), 0, s, a);
-  return hipGetLastError();
 }
 
 // The 16 NT x 64 results of each wave of a tile (row 16 t + lane % 16, inputs 16 c + 4 (lane / 16)
@@ -553,19 +541,22 @@ struct DwRange {
   alignas(16) uint8_t d[2][64 * 256];
 };
 
-__device__ void dw_range(const Fp8b128BackwardArgs& a, DwRange& sh) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// The four waves' item `n`: a tile and a range. Items past the last, and steps past a range's last,
+// are zeros, so that all waves of a workgroup meet at the same barriers.
+__device__ void dw_range(const Fp8b128BackwardArgs& a, DwRange& sh, int n) {
+  const int tid = threadIdx.x & 255, lane = tid & 63, r = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wi = w & 1, wo = w >> 1;
   const int ti = (a.in + 127) / 128, to = (a.out + 127) / 128;
-  const int tile = blockIdx.x % (ti * to), split = blockIdx.x / (ti * to);
+  const int tile = n % (ti * to), split = n / (ti * to);
   const int i0 = tile % ti * 128, o0 = tile / ti * 128;
   const int nsteps = (int)((a.T + 63) / 64);
-  const int per = (nsteps + a.splits - 1) / a.splits, first = split * per, last = min(first + per, nsteps);
+  const int per = (nsteps + a.splits - 1) / a.splits, first = split * per;
+  const int last = split < a.splits ? min(first + per, nsteps) : 0;
   // this thread's 16-byte pieces of a step: two of the codes (32 bytes of bf16, a chunk of the
   // LDS row), four of dy
-  const int xrow = threadIdx.x >> 3, xcol = i0 + 16 * (threadIdx.x & 7);
-  const int drow = threadIdx.x >> 4, dcol = o0 + 8 * (threadIdx.x & 15);
+  const int xrow = tid >> 3, xcol = i0 + 16 * (tid & 7);
+  const int drow = tid >> 4, dcol = o0 + 8 * (tid & 15);
   u32x4 cx[2], cd[4];
   float cs[2];
   auto load = [&](int k) {
@@ -594,13 +585,13 @@ __device__ void dw_range(const Fp8b128BackwardArgs& a, DwRange& sh) {
       const int row = xrow + 32 * j;
       u32x4 v[2];
       fb_widen(cx[j], cs[j], v);
-      u32x4* p = reinterpret_cast<u32x4*>(&sh.x[st][256 * row + 32 * ((threadIdx.x & 7) ^ dw_swizzle(row))]);
+      u32x4* p = reinterpret_cast<u32x4*>(&sh.x[st][256 * row + 32 * ((tid & 7) ^ dw_swizzle(row))]);
       p[0] = v[0];
       p[1] = v[1];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = drow + 16 * j, c = threadIdx.x & 15;
+      const int row = drow + 16 * j, c = tid & 15;
       *reinterpret_cast<u32x4*>(&sh.d[st][256 * row + 32 * ((c >> 1) ^ dw_swizzle(row)) + 16 * (c & 1)]) = cd[j];
     }
   };
@@ -630,18 +621,19 @@ __device__ void dw_range(const Fp8b128BackwardArgs& a, DwRange& sh) {
     }
   };
   load(first);
-  for (int k = first; k < last; k += 2) {
+  for (int k = 0; k < per; k += 2) {
 #pragma unroll
     for (int st = 0; st < 2; ++st)
-      if (k + st < last) {
+      if (k + st < per) {
         store(st);  // the readers of two steps ago have passed the last step's barrier
-        load(k + st + 1);
+        load(first + k + st + 1);
         __syncthreads();
         multiply(st);
       }
   }
   __syncthreads();
   const int o = o0 + 64 * wo, i = i0 + 64 * wi;
+  if (split >= a.splits) return;
   if (a.splits == 1) {
     store_tile((w < 2 ? sh.x[0] : sh.d[0]) + 4096 * (w & 1), acc,
                reinterpret_cast<uint8_t*>(a.dw + (int64_t)o * a.in + i), (int64_t)a.in * 2, a.out - o, (a.in - i) * 2);
@@ -659,7 +651,37 @@ __device__ void dw_range(const Fp8b128BackwardArgs& a, DwRange& sh) {
 
 __global__ __launch_bounds__(256, 2) void fp8b128_dw_range_kernel(Fp8b128BackwardArgs a) {
   __shared__ DwRange sh;
-  dw_range(a, sh);
+  dw_range(a, sh, blockIdx.x);
+}
+
+// ---- dx of few tokens, with dw -------------------------------------------------------------
+//
+// The first `dx_groups` workgroups are dx strips, the others (where dw is made of ranges and both
+// gradients are wanted) dw ranges, an item for each four waves: neither fills the compute units for
+// long, and neither needs the other.
+template <int NS, int TT>
+union DxDwShared {
+  static constexpr int ITEMS = DxStrip<NS, TT>::W / 4;
+  DxStrip<NS, TT> dx;
+  DwRange dw[ITEMS];
+};
+
+template <int NS, int TT>
+__device__ void dx_dw(const Fp8b128BackwardArgs& a, DxDwShared<NS, TT>& sh, int dx_groups) {
+  const int wg = blockIdx.x;
+  if (wg < dx_groups) {
+    dx_strip<NS, TT>(a, sh.dx, wg, dx_groups);
+  } else {
+    const int part = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+    dw_range(a, sh.dw[part], DxDwShared<NS, TT>::ITEMS * (wg - dx_groups) + part);
+  }
+}
+
+template <int NS, int TT>
+__global__ __launch_bounds__((64 * DxStrip<NS, TT>::W)) void fp8b128_dx_dw_kernel(Fp8b128BackwardArgs a,
+                                                                                 int dx_groups) {
+  __shared__ DxDwShared<NS, TT> sh;
+  dx_dw<NS, TT>(a, sh, dx_groups);
 }
 
 // The sums of the ranges, one after the other, as bf16: four results a thread.
@@ -680,6 +702,9 @@ int dw_most_splits(int64_t T, int out, int in) {
   return (int)std::max((int64_t)1, std::min(ceil_div(T, 64), 2 * FB_CUS / tiles));
 }
 
+// Expected time of a launch that adds k ranges (0.01 us).
+int64_t join_cost(int64_t k, int64_t results) { return 300 + k * (15 + results * 8 / 50000); }
+
 // How dw is computed: X widened first (0), or the number of ranges; whichever has the least time
 // expected (0.01 us):
 //   widened  500, the widening of 3 bytes an input at 5 TB/s, and for each round of tiles over the
@@ -690,7 +715,11 @@ int dw_most_splits(int64_t T, int out, int in) {
 // us, x 5,120 x 4,096 20.2 / 15.0; 512 x 5,120 x 4,096 39.1 / 39.2; 2,048 x 5,120 x 1,536 45.8 /
 // 50.5; 2,048 x 768 x 768 26.2 / 33.6 / 19.9 (4); 8,192 x 256 x 64 71 / 117 / 18.3 (16), x 768 x
 // 768 74.7 / 119 / 31.0 (14), x 768 x 5,120 92.1 / 129 / 109 (2).
-int dw_splits(const Fp8b128BackwardArgs& a) {
+struct Plan {
+  int kind;      // of dx: a DxKind; of dw: the number of ranges, or 0
+  int64_t cost;  // 0.01 us
+};
+Plan dw_plan(const Fp8b128BackwardArgs& a) {
   const FbItems items((a.out + 127) / 128, (a.in + 255) / 256);
   const int64_t steps = ceil_div(a.T, 64), results = (int64_t)a.out * a.in;
   const int64_t tiles = ceil_div(a.out, 128) * ceil_div(a.in, 128);
@@ -703,16 +732,18 @@ int dw_splits(const Fp8b128BackwardArgs& a) {
     const int64_t two = 230 + 133 * n, rest = tiles * k % (2 * FB_CUS);
     const int64_t cost = 400 + tiles * k / (2 * FB_CUS) * two +
                          (rest > FB_CUS ? two : rest > 0 ? 80 + 90 * n : 0) +
-                         (k > 1 ? 300 + k * (15 + results * 8 / 50000) : 0);
+                         (k > 1 ? join_cost(k, results) : 0);
     if (cost < least) {
       least = cost;
       best = (int)k;
     }
   }
-  return best;
+  return {best, least};
 }
 
-}  // namespace
+FbItems dx_items(const Fp8b128BackwardArgs& a) {
+  return FbItems((int)ceil_div(a.T, 128), (int)ceil_div(a.in, 256));
+}
 
 // The kernel with the least time expected, by the rounds of workgroups over the compute units and
 // what a round took at 1,536 outputs (0.1 us): strips of (4, 1) 31, (4, 2) 41, (4, 4) 70, tiles
@@ -721,39 +752,34 @@ int dw_splits(const Fp8b128BackwardArgs& a) {
 // 26.8 by whole tiles, 19.0 by halves; 768 tokens 31.0, 28.2 and 20.9. (768 inputs x 5,120
 // outputs, 256 tokens: 11.6 by (4, 1), 44 by halves. 5,120 x 4,096, 32 tokens: 10.6 by (4, 1),
 // 12.1 by (4, 2).)
-hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s) {
-  const int64_t tt = ceil_div(a.T, 128), ti = ceil_div(a.in, 256);
+enum DxKind { DX_TILES = 0, DX_1 = 1, DX_2 = 2, DX_4 = 4 };
+Plan dx_plan(const Fp8b128BackwardArgs& a) {
   const int64_t s1 = 31 * ceil_div(dx_strip_groups<4, 1>(a), FB_CUS);
   const int64_t s2 = 41 * ceil_div(dx_strip_groups<4, 2>(a), FB_CUS);
   const int64_t s4 = 70 * ceil_div(dx_strip_groups<4, 4>(a), FB_CUS);
-  const FbItems items((int)tt, (int)ti);
+  const FbItems items = dx_items(a);
   const int64_t tiles = 230 * ceil_div(items.full, FB_CUS / 8) + (items.items > items.full ? 135 : 0);
   const int64_t least = std::min(std::min(s1, s2), std::min(s4, tiles));
-  if (least == s1) return launch_dx_strip<4, 1>(a, s);
-  if (least == s2) return launch_dx_strip<4, 2>(a, s);
-  if (least == s4) return launch_dx_strip<4, 4>(a, s);
-  hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)(8 * std::min(items.items, FB_CUS / 8))), dim3(512),
-                     0, s, a, items);
+  return {least == s1 ? DX_1 : least == s2 ? DX_2 : least == s4 ? DX_4 : DX_TILES,
+          least * 10 * a.out / 1536};
+}
+
+int64_t dw_range_items(const Fp8b128BackwardArgs& a) {
+  return ceil_div(a.out, 128) * ceil_div(a.in, 128) * a.splits;
+}
+
+hipError_t launch_dw_join(const Fp8b128BackwardArgs& a, hipStream_t s) {
+  const int64_t n4 = (int64_t)a.out * a.in / 4;
+  hipLaunchKernelGGL(fp8b128_dw_join_kernel, dim3((unsigned)ceil_div(n4, 256)), dim3(256), 0, s,
+                     reinterpret_cast<const f32x4*>(a.part), n4, a.splits, a.dw);
   return hipGetLastError();
 }
 
-size_t fp8b128_dw_part_bytes(int64_t T, int out, int in) {
-  const int s = dw_most_splits(T, out, in);
-  return s > 1 ? (size_t)s * out * in * 4 : 0;
-}
-
-hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& args, hipStream_t s) {
-  Fp8b128BackwardArgs a = args;
-  a.splits = dw_splits(a);
+hipError_t launch_dw(const Fp8b128BackwardArgs& a, hipStream_t s) {
   if (a.splits > 0) {
-    const int64_t tiles = ceil_div(a.out, 128) * ceil_div(a.in, 128);
-    hipLaunchKernelGGL(fp8b128_dw_range_kernel, dim3((unsigned)(tiles * a.splits)), dim3(256), 0, s, a);
-    if (a.splits > 1) {
-      const int64_t n4 = (int64_t)a.out * a.in / 4;
-      hipLaunchKernelGGL(fp8b128_dw_join_kernel, dim3((unsigned)ceil_div(n4, 256)), dim3(256), 0, s,
-                         reinterpret_cast<const f32x4*>(a.part), n4, a.splits, a.dw);
-    }
-    return hipGetLastError();
+    hipLaunchKernelGGL(fp8b128_dw_range_kernel, dim3((unsigned)dw_range_items(a)), dim3(256), 0, s, a);
+    hipError_t err = hipGetLastError();
+    return err == hipSuccess && a.splits > 1 ? launch_dw_join(a, s) : err;
   }
   const int64_t n16 = a.T * (a.in / 16);
   hipLaunchKernelGGL(fp8b128_widen_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, s, a.x,
@@ -763,6 +789,83 @@ hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& args, hipStream_t s) {
   const FbItems items((a.out + 127) / 128, (a.in + 255) / 256);
   hipLaunchKernelGGL(fp8b128_dw_kernel, dim3((unsigned)(8 * items.items)), dim3(512), 0, s, a, items);
   return hipGetLastError();
+}
+
+// Expected time of dx strips and dw ranges in one launch (0.01 us). A strip's workgroup takes 150
+// (TT = 1), 100 or 180 for each block of 128 outputs of a wave, or what it reads at its share of
+// 11 TB/s from L2; a workgroup of ranges 160 + 110 a step of 64 tokens (one item, TT = 4: 180 +
+// 75). Where all workgroups have a compute unit the longer of the two counts, else their sum over
+// the compute units and a last round of the shorter. The constants are a fit to calls of 1 to 512
+// tokens and 64 to 5,120 channels; a choice by them took 0.6 % more than the fastest on average.
+// Measured, apart / (4, 1) / (4, 2) / (4, 4): 8 tokens x 768 inputs x 768 outputs 8.6 / 6.3 / 6.3 /
+// 7.5 us, x 5,120 x 4,096 29.2 / 19.8 / 19.7 / 26.8; 333 x 768 x 5,120 23.3 / 24.0 / 16.3 / 20.5,
+// x 768 x 768 13.5 / 15.0 / 12.7 / 10.8, x 5,120 x 1,536 31.5 / 40.0 / 34.2 / 36.1.
+template <int NS, int TT>
+int64_t together_cost(const Fp8b128BackwardArgs& a) {
+  using S = DxStrip<NS, TT>;
+  constexpr int ITEMS = DxDwShared<NS, TT>::ITEMS;
+  const int64_t blocks = ceil_div(a.out, 128), steps = ceil_div(ceil_div(a.T, 64), a.splits);
+  const int64_t dx = dx_strip_groups<NS, TT>(a), dw = ceil_div(dw_range_items(a), ITEMS);
+  const int64_t read = blocks * (8192 + 4096 * TT) * std::min((int64_t)FB_CUS, dx + dw) / 110000;
+  const int64_t strip = std::max(ceil_div(blocks, S::W) * (TT == 1 ? 150 : TT == 2 ? 100 : 180), read);
+  const int64_t range = ITEMS == 2 ? 160 + 110 * steps : 180 + 75 * steps;
+  const int64_t sum = dx + dw <= FB_CUS ? 0 : (dx * strip + dw * range) / FB_CUS + std::min(strip, range);
+  return 400 + std::max(sum, std::max(strip, range)) +
+         (a.splits > 1 ? join_cost(a.splits, (int64_t)a.out * a.in) : 0);
+}
+
+// dx strips, and the ranges of dw if `with_dw`.
+template <int NS, int TT>
+hipError_t launch_strips(const Fp8b128BackwardArgs& a, bool with_dw, hipStream_t s) {
+  const int64_t dx = dx_strip_groups<NS, TT>(a);
+  const int64_t dw = with_dw ? ceil_div(dw_range_items(a), DxDwShared<NS, TT>::ITEMS) : 0;
+  hipLaunchKernelGGL((fp8b128_dx_dw_kernel<NS, TT>), dim3((unsigned)(dx + dw)),
+                     dim3(64 * DxStrip<NS, TT>::W), 0, s, a, (int)dx);
+  hipError_t err = hipGetLastError();
+  return err == hipSuccess && with_dw && a.splits > 1 ? launch_dw_join(a, s) : err;
+}
+
+}  // namespace
+
+size_t fp8b128_dw_part_bytes(int64_t T, int out, int in) {
+  const int s = dw_most_splits(T, out, in);
+  return s > 1 ? (size_t)s * out * in * 4 : 0;
+}
+
+hipError_t launch_fp8b128_backward(const Fp8b128BackwardArgs& args, hipStream_t s) {
+  Fp8b128BackwardArgs a = args;
+  const Plan dw = dw_plan(a), dx = dx_plan(a);
+  a.splits = dw.kind;
+  if (!a.dx) return launch_dw(a, s);
+  int kind = dx.kind;
+  bool with_dw = false;
+  if (a.dw && a.splits > 0) {
+    int64_t least = dx.cost + dw.cost + 220;
+    auto offer = [&](int k, int64_t cost) {
+      if (cost < least) {
+        least = cost;
+        kind = k;
+        with_dw = true;
+      }
+    };
+    offer(DX_1, together_cost<4, 1>(a));
+    offer(DX_2, together_cost<4, 2>(a));
+    offer(DX_4, together_cost<4, 4>(a));
+  }
+  hipError_t err;
+  if (kind == DX_1) {
+    err = launch_strips<4, 1>(a, with_dw, s);
+  } else if (kind == DX_2) {
+    err = launch_strips<4, 2>(a, with_dw, s);
+  } else if (kind == DX_4) {
+    err = launch_strips<4, 4>(a, with_dw, s);
+  } else {
+    const FbItems items = dx_items(a);
+    hipLaunchKernelGGL(fp8b128_dx_kernel, dim3((unsigned)(8 * std::min(items.items, FB_CUS / 8))), dim3(512),
+                       0, s, a, items);
+    err = hipGetLastError();
+  }
+  return err == hipSuccess && a.dw && !with_dw ? launch_dw(a, s) : err;
 }
 
 }  // namespace tq

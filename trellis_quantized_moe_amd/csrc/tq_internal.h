@@ -330,13 +330,12 @@ struct Fp8b128BackwardArgs {
   uint16_t* xw;        // workspace of dw: X as bf16 [T][in], or
   float* part;         // the sums of ranges of tokens, fp32 [splits][out][in]
   int splits;
-  uint16_t* dx;        // bf16 [T][in]
-  uint16_t* dw;        // bf16 [out][in]
+  uint16_t* dx;        // bf16 [T][in], or null
+  uint16_t* dw;        // bf16 [out][in], or null
   int64_t T;
   int out, in, nb;
 };
-hipError_t launch_fp8b128_dx(const Fp8b128BackwardArgs& a, hipStream_t s);
-hipError_t launch_fp8b128_dw(const Fp8b128BackwardArgs& a, hipStream_t s);
+hipError_t launch_fp8b128_backward(const Fp8b128BackwardArgs& a, hipStream_t s);
 // Bytes of `part` that T or fewer tokens take at most.
 size_t fp8b128_dw_part_bytes(int64_t T, int out, int in);
 hipError_t launch_fp8b128_quantize(const uint16_t* x, int64_t rows, int n, uint8_t* codes,
