@@ -39,9 +39,11 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
 //
 // A workgroup owns NS strips of 16 inputs (64 bytes of a row of codes) of up to 16 * TT tokens. Its
 // W waves take the blocks of 128 outputs in turn, in two steps of 64, each with D stages of LDS of
-// its own that its loads fill D - 1 steps ahead (no barrier until the end). A block's products are added from zero and then scaled into the sums; the waves' sums
-// are added in wave order. 32 tokens x 5,120 inputs x 4,096 outputs take 10.5 us, 2 TB/s of codes;
-// with neighbouring strips on different XCDs, each reading the lines they share, it was 17.3.
+// its own that its loads fill D - 1 steps ahead (no barrier until the end). A block's products are
+// added from zero and then scaled into the sums; the waves' sums are added in wave order. Bound by
+// what all workgroups read from L2, 11 to 13 TB/s: 333 tokens x 768 inputs x 5,120 outputs 13.1 us.
+// 32 x 5,120 x 4,096 take 10.5 us; with neighbouring strips on different XCDs, each reading the
+// lines they share, it was 17.3.
 template <int NS, int TT>
 struct DxStrip {
   static constexpr int IW = 16 * NS, W = TT <= 2 ? 8 : 4, D = TT <= 2 ? 2 : 3;
@@ -209,6 +211,9 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, const f32x4 (&acc)[4][N
 // 256 bytes of dy go straight to one of two LDS stages. A wave takes the block strip by strip of 16
 // inputs: the strip's codes become bf16 once, its products with the block's dy (in registers for
 // all strips) are added from zero, and the strip before it is scaled into its sums meanwhile.
+// 8,192 tokens x 5,120 inputs x 1,536 outputs take 120 to 130 us (1.0 to 1.07 PFLOP/s), the matrix
+// cores busy 56 % of the cycles at 1.88 GHz; in steps of 64 outputs, with the sums of a whole block
+// waiting to be scaled at once, it was 136 us and 48 %.
 struct DxShared {
   alignas(16) uint8_t w[2][128 * 256];
   alignas(16) uint8_t d[2][128 * 256];
@@ -390,7 +395,8 @@ __global__ __launch_bounds__(512) void fp8b128_dx_kernel(Fp8b128BackwardArgs a, 
 // ---- dw, many tokens ------------------------------------------------------------------------
 //
 // X as bf16 [T][in] (exact for scales that are powers of two), once per call: every channel
-// tile of the product reads it.
+// tile of the product reads it. Bound by memory: 8,192 x 5,120 take 25 us. Widening in the product
+// instead, on the way from registers to LDS, took the product from 112 to 162 us at 1,536 outputs.
 __global__ __launch_bounds__(256) void fp8b128_widen_kernel(const uint8_t* __restrict__ x,
                                                             const float* __restrict__ xs, int64_t n16,
                                                             int in, int nb, u32x4* __restrict__ y) {
@@ -407,10 +413,11 @@ __global__ __launch_bounds__(256) void fp8b128_widen_kernel(const uint8_t* __res
 }
 
 // A workgroup of eight waves owns 256 inputs of 128 channels (half an item: of 64), wave (wi, wo)
-// 64 inputs of 64 (32) channels; steps of 64 tokens through a ring of three LDS stages, two steps ahead. A row's
-// 32-byte chunk c lies at position c ^ swizzle(row): the LDS serves 32 lanes at a time, which
-// read one chunk of rows 8 q + 0..3 and 8 (q + 1) + 0..3 (or + 4..7), and those eight rows get
-// eight different positions.
+// 64 inputs of 64 (32) channels; steps of 64 tokens through a ring of three LDS stages, two steps
+// ahead. A row's 32-byte chunk c lies at position c ^ swizzle(row): the LDS serves 32 lanes at a
+// time, which read one chunk of rows 8 q + 0..3 and 8 (q + 1) + 0..3 (or + 4..7), and those eight
+// rows get eight different positions. 8,192 tokens x 5,120 inputs x 1,536 channels take 112 to 118
+// us (1.1 PFLOP/s), the matrix cores busy 61 % of the cycles at 1.75 GHz.
 __device__ __forceinline__ int dw_swizzle(int row) { return (row & 3) | (row >> 1 & 4); }
 
 struct DwShared {
@@ -439,7 +446,8 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int o0, int 
     dof[j] = o < min(a.out, o0 + 32 * NT) ? ((uint32_t)row * (uint32_t)a.out + o) * 2u : FB_OOB;
   }
   constexpr int LOADS = 6;
-  // A step's loads, in three parts, as in dx_tile; rows past the last token are read as zeros.
+  // A step's loads, in three parts, issued between the products; rows past the last token are read
+  // as zeros.
   auto load = [&](int n, int st, int k) {
     const int64_t t = (int64_t)64 * k;
     const int left = (int)min((int64_t)64, a.T - t);
@@ -499,7 +507,10 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int o0, int 
   wait_vmcnt<2 * LOADS>();
   bare_barrier();
   read(0, 0);
-  auto step = [&](int st, int k) {  // as in dx_tile
+  // A step's second half is read while its first half is multiplied, and the next step's first
+  // half while its second is: between the two, the next step's data have landed everywhere, and
+  // this step's stage is no longer read.
+  auto step = [&](int st, int k) {
     read(st, 1);
     multiply(0, 0, -1);
     __builtin_amdgcn_sched_barrier(0);
@@ -534,8 +545,9 @@ __global__ __launch_bounds__(512) void fp8b128_dw_kernel(Fp8b128BackwardArgs a, 
 // A workgroup of four waves owns 128 inputs of 128 channels and one of `splits` ranges of the
 // tokens, wave (wi, wo) 64 inputs of 64 channels. X is widened on its way from registers to LDS, so
 // that there is no launch before this one; the next step's loads are in flight while a step's
-// products are made, and a second workgroup on the compute unit fills the waits. With several
-// ranges the sums go to the workspace in fp32, and a second launch adds them in order.
+// products are made, and other waves on the compute unit fill the waits. With several ranges the
+// sums go to the workspace in fp32, and a second launch adds them in order. 64 tokens x 5,120
+// inputs x 1,536 channels take 8.4 us (X widened first: 10.9), bound by the 15.7 MB of results.
 struct DwRange {
   alignas(16) uint8_t x[2][64 * 256];
   alignas(16) uint8_t d[2][64 * 256];
@@ -592,7 +604,8 @@ __device__ void dw_range(const Fp8b128BackwardArgs& a, DwRange& sh, int n) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = drow + 16 * j, c = tid & 15;
-      *reinterpret_cast<u32x4*>(&sh.d[st][256 * row + 32 * ((c >> 1) ^ dw_swizzle(row)) + 16 * (c & 1)]) = cd[j];
+      *reinterpret_cast<u32x4*>(
+          &sh.d[st][256 * row + 32 * ((c >> 1) ^ dw_swizzle(row)) + 16 * (c & 1)]) = cd[j];
     }
   };
   f32x4 acc[4][4];
@@ -713,7 +726,7 @@ int64_t join_cost(int64_t k, int64_t results) { return 300 + k * (15 + results *
 //            80 + 90; with several ranges 300 and for each 15 and 8 bytes a result at 5 TB/s
 // Measured, widened / one range / the best number of ranges: 64 tokens x 5,120 x 1,536 10.9 / 8.4
 // us, x 5,120 x 4,096 20.2 / 15.0; 512 x 5,120 x 4,096 39.1 / 39.2; 2,048 x 5,120 x 1,536 45.8 /
-// 50.5; 2,048 x 768 x 768 26.2 / 33.6 / 19.9 (4); 8,192 x 256 x 64 71 / 117 / 18.3 (16), x 768 x
+// 50.5; 2,048 x 768 x 768 26.2 / 33.6 / 19.9 (4); 8,192 x 256 x 64 71 / 117 / 13.5 (16), x 768 x
 // 768 74.7 / 119 / 31.0 (14), x 768 x 5,120 92.1 / 129 / 109 (2).
 struct Plan {
   int kind;      // of dx: a DxKind; of dw: the number of ranges, or 0
