@@ -321,9 +321,12 @@ class Fp8b128Layer:
         _check_rows("codes", self.codes, _E4M3)
         out, in_ = self.codes.shape
         dev = self.codes.device
-        _check_rows("scales", self.scales, _F32, dev, (-(-out // 128), -(-in_ // 128)))
+        blocks = -(-in_ // 128)
+        _check_rows("scales", self.scales, _F32, dev, (-(-out // 128), blocks))
         c = _lib.Fp8b128LayerC(out, in_, self.codes.data_ptr(), self.scales.data_ptr())
-        self.__dict__.update(out=out, in_=in_, device=dev, _c=c, _ref=ctypes.byref(c))
+        d = self.__dict__
+        d["out"], d["in_"], d["blocks"], d["device"] = out, in_, blocks, dev
+        d["_c"], d["_ref"] = c, ctypes.byref(c)
 
     def renew(self):
         """Checks the layer again if a tensor has been given other memory (set_, resize_, an
@@ -374,7 +377,7 @@ def _call_on(device, fn, *args):
     without making a Stream object: 0.1 us instead of 1.8, in calls of a few microseconds."""
     index = device.index
     stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -396,9 +399,14 @@ def _check_fp8b128(layer, codes, scales):
     """(T, device) of activations that fit the layer."""
     layer.renew()
     dev = layer.device
-    T = codes.shape[0]
-    _check_rows("codes", codes, _E4M3, dev, (T, layer.in_))
-    _check_rows("scales", scales, _F32, dev, (T, -(-layer.in_ // 128)))
+    shape = codes.shape
+    T = shape[0] if shape else 0
+    if not (codes.dtype in _E4M3 and scales.dtype == torch.float32 and codes.device == dev
+            and scales.device == dev and shape == (T, layer.in_)
+            and scales.shape == (T, layer.blocks) and codes.is_contiguous()
+            and scales.is_contiguous()):  # the same checks, with their messages
+        _check_rows("codes", codes, _E4M3, dev, (T, layer.in_))
+        _check_rows("scales", scales, _F32, dev, (T, layer.blocks))
     return T, dev
 
 
@@ -410,11 +418,11 @@ def fp8b128_quantize(x, codes=None, scales=None):
     dev = x.device
     nb = -(-n // 128)
     if codes is None:
-        codes = torch.empty((rows, n), dtype=torch.uint8, device=dev)
+        codes = x.new_empty((rows, n), dtype=torch.uint8)
     else:
         _check_rows("codes", codes, _E4M3, dev, (rows, n))
     if scales is None:
-        scales = torch.empty((rows, nb), dtype=torch.float32, device=dev)
+        scales = x.new_empty((rows, nb), dtype=torch.float32)
     else:
         _check_rows("scales", scales, _F32, dev, (rows, nb))
     _call_on(dev, _lib.load().fp8b128_quantize, x.data_ptr(), rows, n, codes.data_ptr(),
@@ -428,7 +436,7 @@ def fp8b128_gemm(layer, codes, scales, flags=0, out=None):
     T, dev = _check_fp8b128(layer, codes, scales)
     dtype = torch.bfloat16 if flags & TQ_OUT_BF16 else torch.float32
     if out is None:
-        out = torch.empty((T, layer.out), dtype=dtype, device=dev)
+        out = codes.new_empty((T, layer.out), dtype=dtype)
     else:
         _check_rows("out", out, (dtype,), dev, (T, layer.out))
     _call_on(dev, _lib.load().fp8b128_gemm, layer._ref, codes.data_ptr(),
@@ -441,7 +449,7 @@ def fp8b128_gated(layer, codes, scales, out=None):
     (out = 2I) (see fp8b128_gated in include/tq.h)."""
     T, dev = _check_fp8b128(layer, codes, scales)
     if out is None:
-        out = torch.empty((T, layer.out // 2), dtype=torch.bfloat16, device=dev)
+        out = codes.new_empty((T, layer.out // 2), dtype=torch.bfloat16)
     else:
         _check_rows("out", out, _BF16, dev, (T, layer.out // 2))
     _call_on(dev, _lib.load().fp8b128_gated, layer._ref, codes.data_ptr(),
@@ -461,11 +469,11 @@ def _fp8b128_backward(fn, layer, codes, scales, dy, parts, need_dx, need_dw, dx,
     if dx is not None:
         _check_rows("dx", dx, _BF16, dev, (T, layer.in_))
     elif need_dx:
-        dx = torch.empty((T, layer.in_), dtype=torch.bfloat16, device=dev)
+        dx = dy.new_empty((T, layer.in_), dtype=torch.bfloat16)
     if dw is not None:
         _check_rows("dw", dw, _BF16, dev, (layer.out, layer.in_))
     elif need_dw:
-        dw = torch.empty((layer.out, layer.in_), dtype=torch.bfloat16, device=dev)
+        dw = dy.new_empty((layer.out, layer.in_), dtype=torch.bfloat16)
     lib = _lib.load()
     ws = _check_ws(ws, dev, lib.tq_fp8b128_workspace_bytes(T, layer.out, layer.in_))
     _call_on(dev, getattr(lib, fn), layer._ref, codes.data_ptr(),
