@@ -40,9 +40,10 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
 // A workgroup owns NS strips of 16 inputs (64 bytes of a row of codes) of up to 16 * TT tokens. Its
 // W waves take the blocks of 128 outputs in turn, in two steps of 64, each with D stages of LDS of
 // its own that its loads fill D - 1 steps ahead (no barrier until the end). A block's products are
-// added from zero and then scaled into the sums; the waves' sums are added in wave order. Bound by
-// what all workgroups read from L2, 11 to 13 TB/s: 333 tokens x 768 inputs x 5,120 outputs 13.1 us.
-// 32 x 5,120 x 4,096 take 10.5 us; with neighbouring strips on different XCDs, each reading the
+// added from zero and then scaled into the sums; the waves' sums are added in wave order. All
+// workgroups together read 11 to 13 TB/s from L2, a third of what loads alone reach, as a wave's
+// loads, LDS reads and products follow one another: 333 tokens x 768 inputs x 5,120 outputs 13.1
+// us. 32 x 5,120 x 4,096 take 10.5 us; with neighbouring strips on different XCDs, each reading the
 // lines they share, it was 17.3.
 template <int NS, int TT>
 struct DxStrip {

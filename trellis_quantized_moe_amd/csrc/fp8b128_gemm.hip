@@ -140,8 +140,10 @@ hipError_t launch_rows(const Fp8b128GemmArgs& a, hipStream_t s) {
 //
 // A workgroup owns NS strips of 16 channels (gated: half of them gate strips, half the up strips
 // of the same channels) of up to 16 * TT tokens. Its W waves take the blocks of 128 inputs in
-// turn, each with D stages of LDS of its own that its loads fill D - 1 blocks ahead (no barrier
-// until the end), and their sums are added in wave order, so the result does not depend on
+// turn, each with D stages of LDS of its own (no barrier until the end): a block goes from its
+// stage to registers at once, and the stage is refilled between the block's products, so that D
+// blocks are on their way (issued at once before the products, and a stage later, the loads cost 2
+// to 4 % more). The waves' sums are added in wave order, so the result does not depend on
 // timing. One launch, no workspace. The rows come through LDS because a load in operand order
 // has consecutive lanes in different rows, which the memory unit takes one by one: strips of
 // 16 channels and tokens loaded that way took 9.9 us at 32 x 5,120 x 1,536.
@@ -198,15 +200,17 @@ __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
     ws[s] = a.ws + (int64_t)((min(c0 + 16 * (s % NO), width - 16) + s / NO * width) / 128) * a.nb;
   const uint32_t xso = lane < rows ? (uint32_t)(lane * a.nb) * 4u : FB_OOB;
 
-  auto load = [&](int d, int kb) {  // chunks past the row's end, blocks past the last: zeros
+  // Loads first .. last - 1 of a block's S::LOADS; chunks past the row's end are zeros.
+  auto load = [&](int first, int last, int d, int kb) {
     auto& st = sh.stage[w][d];
     const bool in = 128 * kb + chunk < a.in;
 #pragma unroll
-    for (int j = 0; j < 2 * (NS + TT); ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 2 * NS ? rw : rx, (LdsPtr)(&st.rows[1024 * j]), 16,
-                                               in ? ro[j] : FB_OOB, 128u * kb, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&st.sx[0]), 4, kb < a.nb ? xso : FB_OOB,
-                                             4u * kb, 0, 0);
+    for (int j = first; j < last; ++j)
+      if (j < S::LOADS - 1)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 2 * NS ? rw : rx, (LdsPtr)(&st.rows[1024 * j]), 16,
+                                                 in ? ro[j] : FB_OOB, 128u * kb, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (LdsPtr)(&st.sx[0]), 4, xso, 4u * kb, 0, 0);
   };
 
   f32x4 acc[TT][NS];
@@ -216,34 +220,50 @@ __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
     for (int s = 0; s < NS; ++s) acc[t][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
   const int at0 = 128 * r + 16 * (q ^ (r & 7)), at1 = 128 * r + 16 * ((4 + q) ^ (r & 7));
 #pragma unroll
-  for (int d = 0; d < S::D - 1; ++d) load(d, w + S::W * d);
+  for (int d = 0; d < S::D; ++d)
+    if (w + S::W * d < a.nb) load(0, S::LOADS, d, w + S::W * d);
+  // A block: into registers, then its products, with the loads that refill its stage between them.
   auto step = [&](int d, int kb) {
     float ss[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) ss[s] = fb_uniform_load(ws[s] + kb);
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the refilled stage is outstanding
-    __builtin_amdgcn_sched_barrier(0);
-    load((d + S::D - 1) % S::D, kb + S::W * (S::D - 1));
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<S::LOADS * (S::D - 1)>();
+    if (kb + S::W * (S::D - 1) < a.nb)
+      wait_vmcnt<S::LOADS * (S::D - 1)>();
+    else  // fewer blocks are in flight
+      wait_vmcnt<0>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     const auto& st = sh.stage[w][d];
+    u32x4 rows[NS + TT][2];
+    float sx[TT];
+#pragma unroll
+    for (int s = 0; s < NS + TT; ++s) {
+      rows[s][0] = *reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at0);
+      rows[s][1] = *reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at1);
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) sx[t] = st.sx[16 * t + r];
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the stage is outstanding
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const int refill = kb + S::W * S::D;
     FbOperand<EXACT> wv[NS];
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
-      wv[s].set(*reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at0),
-                *reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at1));
+    for (int s = 0; s < NS; ++s) wv[s].set(rows[s][0], rows[s][1]);
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       FbOperand<EXACT> xv;
-      xv.set(*reinterpret_cast<const u32x4*>(st.rows + 2048 * (NS + t) + at0),
-             *reinterpret_cast<const u32x4*>(st.rows + 2048 * (NS + t) + at1));
-      const float sx = st.sx[16 * t + r];
+      xv.set(rows[NS + t][0], rows[NS + t][1]);
+      if (refill < a.nb) {
+        __builtin_amdgcn_sched_barrier(0);
+        load(t * S::LOADS / TT, (t + 1) * S::LOADS / TT, d, refill);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const f32x4 p = fb_block_product(wv[s], xv);
-        const float m = sx * ss[s];
+        const float m = sx[t] * ss[s];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][s][i] = __builtin_fmaf(p[i], m, acc[t][s][i]);
       }
