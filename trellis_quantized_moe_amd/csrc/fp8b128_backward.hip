@@ -38,22 +38,22 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
 // ---- dx, few tokens: strips of inputs, the outputs split over a workgroup's waves ------------
 //
 // A workgroup owns NS strips of 16 inputs (64 bytes of a row of codes) of up to 16 * TT tokens. Its
-// W waves take the blocks of 128 outputs in turn, in two steps of 64, each with D stages of LDS of
-// its own that its loads fill D - 1 steps ahead (no barrier until the end). A block's products are
-// added from zero and then scaled into the sums; the waves' sums are added in wave order. All
-// workgroups together read 11 to 13 TB/s from L2, a third of what loads alone reach, as a wave's
-// loads, LDS reads and products follow one another: 333 tokens x 768 inputs x 5,120 outputs 13.1
-// us. 32 x 5,120 x 4,096 take 10.5 us; with neighbouring strips on different XCDs, each reading the
-// lines they share, it was 17.3.
+// W waves take the blocks of 128 outputs in turn, in two steps of 64, each through LDS of its own
+// (no barrier until the end): a step goes from there to registers at once, and the next one's loads
+// are issued between its products. A block's products are added from zero and then scaled into the
+// sums; the waves' sums are added in wave order. All workgroups together read 11 to 13 TB/s from
+// L2, a third of what loads alone reach, as a wave's loads, LDS reads and products follow one
+// another: 333 tokens x 768 inputs x 5,120 outputs take 13.1 us. 32 x 5,120 x 4,096 take 10.5 us;
+// with neighbouring strips on different XCDs, each reading the lines they share, it was 17.3.
 template <int NS, int TT>
 struct DxStrip {
-  static constexpr int IW = 16 * NS, W = TT <= 2 ? 8 : 4, D = TT <= 2 ? 2 : 3;
+  static constexpr int IW = 16 * NS, W = 8;
   static constexpr int LOADS = NS + 2 * TT;  // per step, of 1024 bytes
   union {
     struct {
       alignas(16) uint8_t w[64 * IW];
       alignas(16) uint8_t d[16 * TT * 128];
-    } stage[W][D];
+    } stage[W];
     f32x4 red[W][TT * NS][64];
   };
 };
@@ -91,18 +91,19 @@ __device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStrip<NS, TT>& sh, int 
     const int tok = 8 * j + (lane >> 3);
     dof[j] = tok < rows ? ((uint32_t)tok * (uint32_t)a.out + dcol) * 2u : FB_OOB;
   }
-  auto load = [&](int d, int k) {  // the outputs 64 k ..; steps past the last are read as zeros
-    auto& st = sh.stage[w][d];
+  // Loads first .. last - 1 of a step's S::LOADS, the outputs 64 k ..; past the last they are zeros.
+  auto load = [&](int first, int last, int k) {
+    auto& st = sh.stage[w];
     const int left = min(64, a.out - 64 * k);
     const GemmRsrc rw = gemm_rsrc(a.w + (int64_t)(left > 0 ? 64 * k : 0) * a.in,
                                   left > 0 ? (uint32_t)left * (uint32_t)a.in : 0u);
 #pragma unroll
-    for (int j = 0; j < NS; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&st.w[1024 * j]), 16, wo[j], 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < 2 * TT; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&st.d[1024 * j]), 16,
-                                               dcol < left ? dof[j] : FB_OOB, 128u * k, 0, 0);
+    for (int j = first; j < last; ++j)
+      if (j < NS)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(&st.w[1024 * j]), 16, wo[j], 0, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (LdsPtr)(&st.d[1024 * (j - NS)]), 16,
+                                                 dcol < left ? dof[j - NS] : FB_OOB, 128u * k, 0, 0);
   };
   // step n of this wave: half n % 2 of its block n / 2
   auto outputs = [&](int n) { return 2 * (w + S::W * (n >> 1)) + (n & 1); };
@@ -112,32 +113,44 @@ __device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStrip<NS, TT>& sh, int 
   for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int c = 0; c < NS; ++c) acc[t][c] = p[t][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int n = 0; n < S::D - 1; ++n) load(n, outputs(n));
-  auto step = [&](int d, int n, bool second) {
+  const int steps = w < nob ? 2 * ((nob - w + S::W - 1) / S::W) : 0;
+  if (steps > 0) load(0, S::LOADS, outputs(0));
+  // A step: into registers, then its products, with the next step's loads between them.
+  auto step = [&](int n, bool second) {
     float s = 0.0f;
     if (second) s = fb_uniform_load(ws + (int64_t)(w + S::W * (n >> 1)) * a.nb);
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the refilled stage is outstanding
-    __builtin_amdgcn_sched_barrier(0);
-    load((d + S::D - 1) % S::D, outputs(n + S::D - 1));
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<S::LOADS * (S::D - 1)>();
+    wait_vmcnt<0>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    const auto& st = sh.stage[w][d];
+    const auto& st = sh.stage[w];
+    u32x4 b[2][TT];
+    u32x2 v[2][NS];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      u32x4 b[TT];
 #pragma unroll
       for (int t = 0; t < TT; ++t)
-        b[t] = *reinterpret_cast<const u32x4*>(&st.d[128 * (16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
+        b[j][t] = *reinterpret_cast<const u32x4*>(&st.d[128 * (16 * t + r) + 16 * ((4 * j + q) ^ (r & 7))]);
 #pragma unroll
       for (int c = 0; c < NS; ++c) {
         const int row = 32 * j + 8 * q + (r >> 1);
-        const u32x2 v = read_tr8(&st.w[S::IW * row + 16 * (c ^ swizzle(row)) + 8 * (r & 1)]);
-        const u32x4 av = fb_bf16_of8(v.x, v.y);
+        v[j][c] = read_tr8(&st.w[S::IW * row + 16 * (c ^ swizzle(row)) + 8 * (r & 1)]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the stage is outstanding
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) p[t][c] = mfma_bf16(av, b[t], p[t][c]);
+    for (int j = 0; j < 2; ++j) {
+      if (n + 1 < steps) {
+        load(j * S::LOADS / 2, (j + 1) * S::LOADS / 2, outputs(n + 1));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int c = 0; c < NS; ++c) {
+        const u32x4 av = fb_bf16_of8(v[j][c].x, v[j][c].y);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) p[t][c] = mfma_bf16(av, b[j][t], p[t][c]);
       }
     }
     if (second) {
@@ -151,17 +164,10 @@ __device__ void dx_strip(const Fp8b128BackwardArgs& a, DxStrip<NS, TT>& sh, int 
         }
     }
   };
-  const int steps = w < nob ? 2 * ((nob - w + S::W - 1) / S::W) : 0;
-  constexpr int U = S::D == 2 ? 2 : 6;  // steps after which stage and half repeat
-  for (int n = 0; n < steps; n += U) {
-#pragma unroll
-    for (int u = 0; u < U; u += 2)
-      if (n + u < steps) {
-        step(u % S::D, n + u, false);
-        step((u + 1) % S::D, n + u + 1, true);
-      }
+  for (int n = 0; n < steps; n += 2) {
+    step(n, false);
+    step(n + 1, true);
   }
-  wait_vmcnt<0>();
   __syncthreads();  // no load of this workgroup is writing its LDS, and no wave reads a stage
 #pragma unroll
   for (int t = 0; t < TT; ++t)
@@ -671,31 +677,31 @@ __global__ __launch_bounds__(256, 2) void fp8b128_dw_range_kernel(Fp8b128Backwar
 // ---- dx of few tokens, with dw -------------------------------------------------------------
 //
 // The first `dx_groups` workgroups are dx strips, the others (where dw is made of ranges and both
-// gradients are wanted) dw ranges, an item for each four waves: neither fills the compute units for
-// long, and neither needs the other.
+// gradients are wanted) dw ranges: neither fills the compute units for long, and neither needs the
+// other. Four waves take an item of dw; a workgroup has two, or one (and four waves that end at
+// once) where that still leaves every workgroup a compute unit.
 template <int NS, int TT>
 union DxDwShared {
-  static constexpr int ITEMS = DxStrip<NS, TT>::W / 4;
   DxStrip<NS, TT> dx;
-  DwRange dw[ITEMS];
+  DwRange dw[2];
 };
 
 template <int NS, int TT>
-__device__ void dx_dw(const Fp8b128BackwardArgs& a, DxDwShared<NS, TT>& sh, int dx_groups) {
+__device__ void dx_dw(const Fp8b128BackwardArgs& a, DxDwShared<NS, TT>& sh, int dx_groups, int items) {
   const int wg = blockIdx.x;
   if (wg < dx_groups) {
     dx_strip<NS, TT>(a, sh.dx, wg, dx_groups);
   } else {
     const int part = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
-    dw_range(a, sh.dw[part], DxDwShared<NS, TT>::ITEMS * (wg - dx_groups) + part);
+    if (part < items) dw_range(a, sh.dw[part], items * (wg - dx_groups) + part);
   }
 }
 
 template <int NS, int TT>
 __global__ __launch_bounds__((64 * DxStrip<NS, TT>::W)) void fp8b128_dx_dw_kernel(Fp8b128BackwardArgs a,
-                                                                                 int dx_groups) {
+                                                                                 int dx_groups, int items) {
   __shared__ DxDwShared<NS, TT> sh;
-  dx_dw<NS, TT>(a, sh, dx_groups);
+  dx_dw<NS, TT>(a, sh, dx_groups, items);
 }
 
 // The sums of the ranges, one after the other, as bf16: four results a thread.
@@ -782,6 +788,11 @@ int64_t dw_range_items(const Fp8b128BackwardArgs& a) {
   return ceil_div(a.out, 128) * ceil_div(a.in, 128) * a.splits;
 }
 
+// Items of dw of a workgroup in a launch with dx_groups of dx.
+int items_together(const Fp8b128BackwardArgs& a, int64_t dx_groups) {
+  return dx_groups + dw_range_items(a) <= FB_CUS ? 1 : 2;
+}
+
 hipError_t launch_dw_join(const Fp8b128BackwardArgs& a, hipStream_t s) {
   const int64_t n4 = (int64_t)a.out * a.in / 4;
   hipLaunchKernelGGL(fp8b128_dw_join_kernel, dim3((unsigned)ceil_div(n4, 256)), dim3(256), 0, s,
@@ -805,24 +816,26 @@ hipError_t launch_dw(const Fp8b128BackwardArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Expected time of dx strips and dw ranges in one launch (0.01 us). A strip's workgroup takes 150
-// (TT = 1), 100 or 180 for each block of 128 outputs of a wave, or what it reads at its share of
-// 11 TB/s from L2; a workgroup of ranges 160 + 110 a step of 64 tokens (one item, TT = 4: 180 +
-// 75). Where all workgroups have a compute unit the longer of the two counts, else their sum over
-// the compute units and a last round of the shorter. The constants are a fit to calls of 1 to 512
-// tokens and 64 to 5,120 channels; a choice by them took 0.6 % more than the fastest on average.
-// Measured, apart / (4, 1) / (4, 2) / (4, 4): 8 tokens x 768 inputs x 768 outputs 8.6 / 6.3 / 6.3 /
-// 7.5 us, x 5,120 x 4,096 29.2 / 19.8 / 19.7 / 26.8; 333 x 768 x 5,120 23.3 / 24.0 / 16.3 / 20.5,
-// x 768 x 768 13.5 / 15.0 / 12.7 / 10.8, x 5,120 x 1,536 31.5 / 40.0 / 34.2 / 36.1.
+// Expected time of dx strips and dw ranges in one launch (0.01 us). A strip's workgroup takes 170
+// (TT = 1), 130 or 260 for each block of 128 outputs of a wave, or what it reads at its share of
+// 11 TB/s from L2; a workgroup of two ranges 200 + 110 a step of 64 tokens, of one 30 + 70. Where
+// all workgroups have a compute unit the longer of the two counts, else their sum over the compute
+// units and a last round of the shorter. The constants are a fit to calls of 1 to 512 tokens and 64
+// to 5,120 channels; a choice by them took 0.5 % more than the fastest on average. Measured, apart
+// / (4, 1) / (4, 2) / (4, 4): 8 tokens x 768 inputs x 768 outputs 8.4 / 5.7 / 5.4 / 6.5 us, x 5,120
+// x 4,096 29.2 / 20.1 / 19.9 / 22.8; 333 x 768 x 5,120 23.6 / 24.2 / 16.4 / 20.7, x 768 x 768 13.5
+// / 15.6 / 10.1 / 10.1; 130 x 2,576 x 1,440 15.1 / 15.2 / 15.0 / 10.9; 512 x 5,120 x 1,536 35.2 /
+// 59.1 / 45.7 / 39.5.
 template <int NS, int TT>
 int64_t together_cost(const Fp8b128BackwardArgs& a) {
   using S = DxStrip<NS, TT>;
-  constexpr int ITEMS = DxDwShared<NS, TT>::ITEMS;
   const int64_t blocks = ceil_div(a.out, 128), steps = ceil_div(ceil_div(a.T, 64), a.splits);
-  const int64_t dx = dx_strip_groups<NS, TT>(a), dw = ceil_div(dw_range_items(a), ITEMS);
+  const int64_t dx = dx_strip_groups<NS, TT>(a);
+  const int items = items_together(a, dx);
+  const int64_t dw = ceil_div(dw_range_items(a), items);
   const int64_t read = blocks * (8192 + 4096 * TT) * std::min((int64_t)FB_CUS, dx + dw) / 110000;
-  const int64_t strip = std::max(ceil_div(blocks, S::W) * (TT == 1 ? 150 : TT == 2 ? 100 : 180), read);
-  const int64_t range = ITEMS == 2 ? 160 + 110 * steps : 180 + 75 * steps;
+  const int64_t strip = std::max(ceil_div(blocks, S::W) * (TT == 1 ? 170 : TT == 2 ? 130 : 260), read);
+  const int64_t range = items == 2 ? 200 + 110 * steps : 30 + 70 * steps;
   const int64_t sum = dx + dw <= FB_CUS ? 0 : (dx * strip + dw * range) / FB_CUS + std::min(strip, range);
   return 400 + std::max(sum, std::max(strip, range)) +
          (a.splits > 1 ? join_cost(a.splits, (int64_t)a.out * a.in) : 0);
@@ -832,9 +845,10 @@ int64_t together_cost(const Fp8b128BackwardArgs& a) {
 template <int NS, int TT>
 hipError_t launch_strips(const Fp8b128BackwardArgs& a, bool with_dw, hipStream_t s) {
   const int64_t dx = dx_strip_groups<NS, TT>(a);
-  const int64_t dw = with_dw ? ceil_div(dw_range_items(a), DxDwShared<NS, TT>::ITEMS) : 0;
+  const int items = with_dw ? items_together(a, dx) : 0;
+  const int64_t dw = with_dw ? ceil_div(dw_range_items(a), items) : 0;
   hipLaunchKernelGGL((fp8b128_dx_dw_kernel<NS, TT>), dim3((unsigned)(dx + dw)),
-                     dim3(64 * DxStrip<NS, TT>::W), 0, s, a, (int)dx);
+                     dim3(64 * DxStrip<NS, TT>::W), 0, s, a, (int)dx, items);
   hipError_t err = hipGetLastError();
   return err == hipSuccess && with_dw && a.splits > 1 ? launch_dw_join(a, s) : err;
 }

@@ -140,23 +140,23 @@ hipError_t launch_rows(const Fp8b128GemmArgs& a, hipStream_t s) {
 //
 // A workgroup owns NS strips of 16 channels (gated: half of them gate strips, half the up strips
 // of the same channels) of up to 16 * TT tokens. Its W waves take the blocks of 128 inputs in
-// turn, each with D stages of LDS of its own (no barrier until the end): a block goes from its
-// stage to registers at once, and the stage is refilled between the block's products, so that D
-// blocks are on their way (issued at once before the products, and a stage later, the loads cost 2
-// to 4 % more). The waves' sums are added in wave order, so the result does not depend on
-// timing. One launch, no workspace. The rows come through LDS because a load in operand order
+// turn, each through LDS of its own (no barrier until the end): a block goes from there to
+// registers at once, and the next one's loads are issued between its products. The waves' sums are
+// added in wave order, so the result does not depend on timing. One LDS stage and eight waves, two
+// on a SIMD, are better than four waves with two or three stages: 213 tokens x 5,120 x 1,536 10.6
+// and 11.5 us (fp32 results 11.7 and 14.2). One launch, no workspace. The rows come through LDS because a load in operand order
 // has consecutive lanes in different rows, which the memory unit takes one by one: strips of
 // 16 channels and tokens loaded that way took 9.9 us at 32 x 5,120 x 1,536.
 template <int NS, int TT>
 struct FbStrip {
   static constexpr int ROWS = 16 * (NS + TT);
-  static constexpr int W = NS + TT <= 4 ? 8 : 4, D = NS + TT <= 3 ? 3 : NS + TT == 6 ? 3 : 2;
+  static constexpr int W = 8;
   static constexpr int LOADS = ROWS / 8 + 1;  // per block
   union {
     struct {
       alignas(16) uint8_t rows[ROWS * 128];  // strips, then tokens
       alignas(16) float sx[64];
-    } stage[W][D];
+    } stage[W];
     f32x4 red[W][TT * NS][64];
   };
 };
@@ -201,8 +201,8 @@ __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
   const uint32_t xso = lane < rows ? (uint32_t)(lane * a.nb) * 4u : FB_OOB;
 
   // Loads first .. last - 1 of a block's S::LOADS; chunks past the row's end are zeros.
-  auto load = [&](int first, int last, int d, int kb) {
-    auto& st = sh.stage[w][d];
+  auto load = [&](int first, int last, int kb) {
+    auto& st = sh.stage[w];
     const bool in = 128 * kb + chunk < a.in;
 #pragma unroll
     for (int j = first; j < last; ++j)
@@ -219,27 +219,22 @@ __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) acc[t][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
   const int at0 = 128 * r + 16 * (q ^ (r & 7)), at1 = 128 * r + 16 * ((4 + q) ^ (r & 7));
-#pragma unroll
-  for (int d = 0; d < S::D; ++d)
-    if (w + S::W * d < a.nb) load(0, S::LOADS, d, w + S::W * d);
-  // A block: into registers, then its products, with the loads that refill its stage between them.
-  auto step = [&](int d, int kb) {
+  if (w < a.nb) load(0, S::LOADS, w);
+  // A block: into registers, then its products, with the next block's loads between them.
+  for (int kb = w; kb < a.nb; kb += S::W) {
     float ss[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) ss[s] = fb_uniform_load(ws[s] + kb);
-    if (kb + S::W * (S::D - 1) < a.nb)
-      wait_vmcnt<S::LOADS * (S::D - 1)>();
-    else  // fewer blocks are in flight
-      wait_vmcnt<0>();
+    wait_vmcnt<0>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    const auto& st = sh.stage[w][d];
-    u32x4 rows[NS + TT][2];
+    const auto& st = sh.stage[w];
+    u32x4 codes[NS + TT][2];
     float sx[TT];
 #pragma unroll
     for (int s = 0; s < NS + TT; ++s) {
-      rows[s][0] = *reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at0);
-      rows[s][1] = *reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at1);
+      codes[s][0] = *reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at0);
+      codes[s][1] = *reinterpret_cast<const u32x4*>(st.rows + 2048 * s + at1);
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) sx[t] = st.sx[16 * t + r];
@@ -247,17 +242,16 @@ __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): no read of the stage is outstanding
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    const int refill = kb + S::W * S::D;
     FbOperand<EXACT> wv[NS];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) wv[s].set(rows[s][0], rows[s][1]);
+    for (int s = 0; s < NS; ++s) wv[s].set(codes[s][0], codes[s][1]);
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       FbOperand<EXACT> xv;
-      xv.set(rows[NS + t][0], rows[NS + t][1]);
-      if (refill < a.nb) {
+      xv.set(codes[NS + t][0], codes[NS + t][1]);
+      if (kb + S::W < a.nb) {
         __builtin_amdgcn_sched_barrier(0);
-        load(t * S::LOADS / TT, (t + 1) * S::LOADS / TT, d, refill);
+        load(t * S::LOADS / TT, (t + 1) * S::LOADS / TT, kb + S::W);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -268,13 +262,7 @@ __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
         for (int i = 0; i < 4; ++i) acc[t][s][i] = __builtin_fmaf(p[i], m, acc[t][s][i]);
       }
     }
-  };
-  for (int kb = w; kb < a.nb; kb += S::W * S::D) {
-#pragma unroll
-    for (int d = 0; d < S::D; ++d)
-      if (kb + S::W * d < a.nb) step(d, kb + S::W * d);
   }
-  wait_vmcnt<0>();
   __syncthreads();  // no load of this workgroup is writing its LDS, and no wave reads a stage
 #pragma unroll
   for (int t = 0; t < TT; ++t)
