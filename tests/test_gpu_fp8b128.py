@@ -32,11 +32,14 @@ FORWARD = [(1, 16, 16), (1, 1536, 5120), (2, 48, 112), (5, 160, 128), (16, 32, 1
            (200, 400, 272), (257, 528, 640), (300, 1040, 96), (513, 288, 1296), (1030, 784, 528), (3000, 2832, 144),
            # strips of each shape, tiles of each shape, more tiles than compute units
            (12, 5120, 272), (60, 5120, 400), (300, 2064, 656), (1000, 3088, 528), (2100, 2064, 400),
-           (2100, 4112, 272), (4200, 4112, 144), (265, 10048, 144), (1714, 11680, 144)]
+           (2100, 4112, 272), (4200, 4112, 144), (265, 10048, 144), (1714, 11680, 144),
+           (33, 5984, 2064), (333, 3808, 1040), (273, 3808, 1040), (513, 10880, 144), (3513, 9248, 144),
+           (1714, 9248, 400)]
 GATED = [(1, 32, 16), (1, 1536, 5120), (3, 96, 144), (16, 288, 272), (31, 64, 400), (64, 1440, 528),
          (130, 160, 1040), (257, 544, 256), (300, 800, 400), (700, 1056, 272), (2900, 2848, 272),
          (60, 5120, 400), (700, 4128, 272), (2100, 2080, 400), (4100, 4096, 144), (4200, 4128, 144),
-         (265, 8672, 144), (1971, 10304, 144)]
+         (265, 8672, 144), (1971, 10304, 144), (33, 5984, 2064), (33, 8704, 1040), (273, 3808, 1040),
+         (513, 10880, 144), (3513, 9248, 144)]
 BACKWARD = [(1, 32, 16), (1, 288, 400), (2, 64, 128), (17, 32, 272), (40, 288, 144), (64, 96, 1040),
             (129, 256, 256), (200, 544, 400), (257, 160, 656), (333, 1056, 272), (600, 288, 784), (2100, 352, 2064), (4200, 64, 2320),
             (1000, 3104, 144), (3000, 2848, 144), (2100, 2048, 272),
@@ -45,7 +48,8 @@ BACKWARD = [(1, 32, 16), (1, 288, 400), (2, 64, 128), (17, 32, 272), (40, 288, 1
             (600, 2080, 2064), (420, 2848, 2832),
             # the two gradients in one launch or apart, in each of their kernels
             (580, 1056, 144), (580, 64, 1296), (130, 1600, 2064), (310, 1056, 2832), (400, 160, 1296),
-            (580, 160, 2832), (850, 64, 2064), (940, 352, 4112), (4300, 64, 784), (4000, 64, 4112)]
+            (580, 160, 2832), (850, 64, 2064), (940, 352, 4112), (4300, 64, 784), (4000, 64, 4112),
+            (513, 10880, 144), (1714, 9248, 144)]
 
 
 def bits_of(t):

@@ -595,18 +595,19 @@ hipError_t launch_tiles(const Fp8b128GemmArgs& a, hipStream_t s) {
   return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, ST, !fb_gated(EPI)>, grid, block, s, a, n);
 }
 
-// The kernel with the least time expected, by the rounds of workgroups over the compute units and
-// what a round took at 5,120 inputs (0.1 us, bf16 results / fp32 results; a round's time is close
-// to proportional to the inputs):
-//   strips of (NS, TT)   18 / 22 times NS + TT: 5.5 us with (1, 1), 7.2 with (2, 2), 11.2 with
-//                        (4, 2), 14.3 / 18 with (4, 4)
-//   128 x 128 tiles      380 / 540 (for one round: two were never the least)
-//   128 x 256 tiles      470 / 770, a round of halves 300 / 480
-//   256 x 256 tiles      750, a round of halves 520 (bf16 results only)
-// Measured where two meet: 512 tokens x 1,536 channels 15.9 us by (4, 4) strips, 37.8 by 128 x 128
-// tiles; 512 x 5,120 41.8, 38.8 and 31.4 by halves of 128 x 256 tiles; 1,024 x 5,120 43.9 by
-// 128 x 256 tiles, 49.9 by halves of 256 x 256 ones; 2,048 x 5,120 81.5 and (whole) 69.2; 8,192 x
-// 7,168 281 us in four rounds of 256 x 256 tiles, 268 with the last one's in halves.
+// The kernel with the least time expected, beside the 3.7 us that all have in common (0.01 us; bf16
+// results / fp32 results). Of strips, by the rounds of workgroups over the compute units and the
+// blocks of 128 inputs of a wave, an eighth of all:
+//   (1, 1) 29 / 31 a block and round, (2, 1) 48 / 55, (2, 2) 69 / 89, and 38 for each round after
+//   the first; (4, 2) 93 a round and 113 / 147 a block of it, (4, 4) 123 and 161 / 216
+// Of tiles, by the rounds of tiles, the last of halves, and all blocks:
+//   128 x 128 54 and 75 / 120 a block (for one round: two were never the least); 128 x 256 147 a
+//   round and 103 / 145 a block of it, of halves 59 / 104; 256 x 256 83 and 148, 114 (bf16 only)
+// The constants are a fit to calls of 3 to 1,024 tokens, 768 to 5,120 inputs and channels; a choice
+// by them took 0.5 % more than the fastest on average. Measured, (2, 2) / (4, 4) / 128 x 128 / 128 x
+// 256 / 256 x 256: 213 tokens x 768 x 5,120 9.2 / 10.4 / 8.3 / 8.6 / 10.7 us; 768 x 2,576 x 1,440
+// 16.4 / 18.7 / 20.6 / 20.3 / 32.6; 1,024 x 5,120 x 5,120 43.9 by 128 x 256 tiles, 49.9 by halves of
+// 256 x 256; 8,192 x 5,120 x 7,168 281 in four rounds of 256 x 256, 268 with the last in halves.
 template <int EPI>
 hipError_t launch_forward(const Fp8b128GemmArgs& a, hipStream_t s) {
   constexpr bool EXACT = EPI == FB_F32;
@@ -620,22 +621,28 @@ hipError_t launch_forward(const Fp8b128GemmArgs& a, hipStream_t s) {
       best = f;
     }
   };
-  constexpr int U = EXACT ? 22 : 18;
-  if constexpr (!fb_gated(EPI))
-    offer(2 * U * ceil_div(strip_groups<EPI, 1, 1>(a), FB_CUS), launch_strip<EPI, 1, 1>);
-  offer(3 * U * ceil_div(strip_groups<EPI, 2, 1>(a), FB_CUS), launch_strip<EPI, 2, 1>);
-  offer(4 * U * ceil_div(strip_groups<EPI, 2, 2>(a), FB_CUS), launch_strip<EPI, 2, 2>);
-  offer(6 * U * ceil_div(strip_groups<EPI, 4, 2>(a), FB_CUS), launch_strip<EPI, 4, 2>);
-  offer(8 * U * ceil_div(strip_groups<EPI, 4, 4>(a), FB_CUS), launch_strip<EPI, 4, 4>);
+  const int64_t wave_blocks = ceil_div(a.nb, FbStrip<1, 1>::W);
+  auto strips = [&](int64_t groups, int block, Launch f) {
+    const int64_t rounds = ceil_div(groups, FB_CUS);
+    offer(rounds * block * wave_blocks + 38 * (rounds - 1), f);
+  };
+  if constexpr (!fb_gated(EPI)) strips(strip_groups<EPI, 1, 1>(a), EXACT ? 31 : 29, launch_strip<EPI, 1, 1>);
+  strips(strip_groups<EPI, 2, 1>(a), EXACT ? 55 : 48, launch_strip<EPI, 2, 1>);
+  strips(strip_groups<EPI, 2, 2>(a), EXACT ? 89 : 69, launch_strip<EPI, 2, 2>);
+  offer(ceil_div(strip_groups<EPI, 4, 2>(a), FB_CUS) * (93 + (EXACT ? 147 : 113) * wave_blocks),
+        launch_strip<EPI, 4, 2>);
+  offer(ceil_div(strip_groups<EPI, 4, 4>(a), FB_CUS) * (123 + (EXACT ? 216 : 161) * wave_blocks),
+        launch_strip<EPI, 4, 4>);
   // whole rounds and, where the last one is of halves, that
-  auto rounds = [](const FbItems& n, int64_t whole, int64_t halves) {
-    return ceil_div(n.full, FB_CUS / 8) * whole + (n.items > n.full ? halves : 0);
+  auto rounds = [&](const FbItems& n, int64_t round, int64_t whole, int64_t halves) {
+    return ceil_div(n.full, FB_CUS / 8) * (round + whole * a.nb) +
+           (n.items > n.full ? round + halves * a.nb : 0);
   };
   if (tile_items<EPI, 4, 2, 2>(a).per <= FB_CUS / 8)
-    offer(EXACT ? 540 : 380, launch_tiles<EPI, 4, 2, 2>);
-  offer(rounds(tile_items<EPI, 4, 4, 3>(a), EXACT ? 770 : 470, EXACT ? 480 : 300), launch_tiles<EPI, 4, 4, 3>);
+    offer(54 + (EXACT ? 120 : 75) * a.nb, launch_tiles<EPI, 4, 2, 2>);
+  offer(rounds(tile_items<EPI, 4, 4, 3>(a), 147, EXACT ? 145 : 103, EXACT ? 104 : 59), launch_tiles<EPI, 4, 4, 3>);
   if constexpr (!EXACT)
-    offer(rounds(tile_items<EPI, 8, 4, 2>(a), 750, 520), launch_tiles<EPI, 8, 4, 2>);
+    offer(rounds(tile_items<EPI, 8, 4, 2>(a), 83, 148, 114), launch_tiles<EPI, 8, 4, 2>);
   return best(a, s);
 }
 
