@@ -765,23 +765,25 @@ FbItems dx_items(const Fp8b128BackwardArgs& a) {
   return FbItems((int)ceil_div(a.T, 128), (int)ceil_div(a.in, 256));
 }
 
-// The kernel with the least time expected, by the rounds of workgroups over the compute units and
-// what a round took at 1,536 outputs (0.1 us): strips of (4, 1) 31, (4, 2) 41, (4, 4) 70, tiles
-// 230, a round of halves of tiles 135. Measured where two meet, for 5,120 inputs: 32 tokens 5.8 us
-// by (4, 1), 6.3 by (4, 2); 128 tokens 10.7 by (4, 2), 9.8 by (4, 4); 512 tokens 23.9 by (4, 4),
-// 26.8 by whole tiles, 19.0 by halves; 768 tokens 31.0, 28.2 and 20.9. (768 inputs x 5,120
-// outputs, 256 tokens: 11.6 by (4, 1), 44 by halves. 5,120 x 4,096, 32 tokens: 10.6 by (4, 1),
-// 12.1 by (4, 2).)
+// The kernel of dx with the least time expected, beside the 2 us that all have in common (0.01 us),
+// by the rounds of workgroups over the compute units and the blocks of 128 outputs (strips: of a
+// wave, an eighth of all): strips of (4, 1) 96 a round and 159 a block of it, (4, 2) 86 and 205,
+// (4, 4) 103 and 314, tiles 260 and 168, of a round of halves 103. The constants are a fit to calls
+// of 16 to 1,024 tokens; a choice by them took 0.4 % more than the fastest on average. Measured,
+// (4, 1) / (4, 2) / (4, 4) / tiles: 32 tokens x 5,120 inputs x 4,096 outputs 10.5 / 11.7 / 14.3 / 36
+// us; 201 x 1,200 x 2,640 9.7 / 9.2 / 11.1 / 23.7; 333 x 5,120 x 1,536 27.0 / 20.2 / 15.8 / 17.5;
+// 768 x 2,576 x 1,440 35.4 / 24.7 / 18.9 / 17.9.
 enum DxKind { DX_TILES = 0, DX_1 = 1, DX_2 = 2, DX_4 = 4 };
 Plan dx_plan(const Fp8b128BackwardArgs& a) {
-  const int64_t s1 = 31 * ceil_div(dx_strip_groups<4, 1>(a), FB_CUS);
-  const int64_t s2 = 41 * ceil_div(dx_strip_groups<4, 2>(a), FB_CUS);
-  const int64_t s4 = 70 * ceil_div(dx_strip_groups<4, 4>(a), FB_CUS);
+  const int64_t blocks = ceil_div(a.out, 128), wave_blocks = ceil_div(blocks, DxStrip<4, 1>::W);
+  const int64_t s1 = ceil_div(dx_strip_groups<4, 1>(a), FB_CUS) * (96 + 159 * wave_blocks);
+  const int64_t s2 = ceil_div(dx_strip_groups<4, 2>(a), FB_CUS) * (86 + 205 * wave_blocks);
+  const int64_t s4 = ceil_div(dx_strip_groups<4, 4>(a), FB_CUS) * (103 + 314 * wave_blocks);
   const FbItems items = dx_items(a);
-  const int64_t tiles = 230 * ceil_div(items.full, FB_CUS / 8) + (items.items > items.full ? 135 : 0);
+  const int64_t tiles = ceil_div(items.full, FB_CUS / 8) * (260 + 168 * blocks) +
+                        (items.items > items.full ? 260 + 103 * blocks : 0);
   const int64_t least = std::min(std::min(s1, s2), std::min(s4, tiles));
-  return {least == s1 ? DX_1 : least == s2 ? DX_2 : least == s4 ? DX_4 : DX_TILES,
-          least * 10 * a.out / 1536};
+  return {least == s1 ? DX_1 : least == s2 ? DX_2 : least == s4 ? DX_4 : DX_TILES, least};
 }
 
 int64_t dw_range_items(const Fp8b128BackwardArgs& a) {
@@ -868,7 +870,7 @@ hipError_t launch_fp8b128_backward(const Fp8b128BackwardArgs& args, hipStream_t 
   int kind = dx.kind;
   bool with_dw = false;
   if (a.dw && a.splits > 0) {
-    int64_t least = dx.cost + dw.cost + 220;
+    int64_t least = dx.cost + dw.cost + 110;
     auto offer = [&](int k, int64_t cost) {
       if (cost < least) {
         least = cost;
