@@ -533,7 +533,8 @@ __device__ void dw_tile(const Fp8b128BackwardArgs& a, DwShared& sh, int o0, int 
   }
   wait_vmcnt<0>();
   __syncthreads();
-  store_tile(sh.x[0] + 4096 * w, acc, reinterpret_cast<uint8_t*>(a.dw + (int64_t)(o0 + 16 * NT * wo) * a.in + i0 + 64 * wi),
+  store_tile(sh.x[0] + 4096 * w, acc,
+             reinterpret_cast<uint8_t*>(a.dw + (int64_t)(o0 + 16 * NT * wo) * a.in + i0 + 64 * wi),
              (int64_t)a.in * 2, a.out - o0 - 16 * NT * wo, (a.in - i0 - 64 * wi) * 2);
 }
 
