@@ -327,12 +327,20 @@ class Fp8b128Layer:
         d = self.__dict__
         d["out"], d["in_"], d["blocks"], d["device"] = out, in_, blocks, dev
         d["_c"], d["_ref"] = c, ctypes.byref(c)
+        d["_checked"] = self._state()
+
+    def _state(self):
+        """All that the checks and the C struct depend on."""
+        c, s = self.codes, self.scales
+        return (c.data_ptr(), s.data_ptr(), c.shape, s.shape, c.dtype, s.dtype, c.device, s.device,
+                c.is_contiguous(), s.is_contiguous())
 
     def renew(self):
-        """Checks the layer again if a tensor has been given other memory (set_, resize_, an
-        assignment to .data); the fields themselves cannot be assigned again. Every call does
-        this before it uses the C struct."""
-        if self.codes.data_ptr() != self._c.codes or self.scales.data_ptr() != self._c.scales:
+        """Checks the layer again if a tensor has been given other memory, another shape or
+        another type (set_, resize_, t_, an assignment to .data), also at the same address; the
+        fields themselves cannot be assigned again. Every call does this before it uses the C
+        struct."""
+        if self._state() != self._checked:
             self.__post_init__()
 
     def c_struct(self):
