@@ -480,9 +480,12 @@ int fp8b128_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, flo
  * than 2^-10 * sum over i of |X[t][i]| * |W[o][i]|, a code below 2^-6 counting as that. On normal
  * data it is 5e-5 of y in the 2-norm at most, far below bf16's rounding; where large terms cancel
  * it can be all of what is left, and the fp32 result is the one to ask for.
- * NaN codes, infinite or NaN scales give NaN in the outputs they enter. The same call gives the
- * same bits; a token's bits may depend on T, which decides how the inputs are split and, as above,
- * how the products are added.
+ * NaN codes and NaN scales give NaN in the outputs they enter, an infinite scale gives infinities
+ * or NaN. A block's two scales are multiplied first, in fp32: two finite ones whose product is not
+ * count as infinite, and a product below 2^-126 has only the bits that are left there (it is off by
+ * 2^-150 at most).
+ * The same call gives the same bits; a token's bits may depend on T, which decides how the inputs
+ * are split and, as above, how the products are added.
  */
 int fp8b128_gemm(const tq_fp8b128_layer* L, const uint8_t* xq, const float* xs, int64_t T,
                  void* y, uint32_t flags, void* stream);
@@ -509,7 +512,8 @@ int fp8b128_gated(const tq_fp8b128_layer* gate_up, const uint8_t* xq, const floa
  *   dx   device bf16 [T][L->in], 16-byte aligned, or NULL (not wanted).
  *   dw   device bf16 [L->out][L->in], 16-byte aligned, or NULL. With T == 0 it is all zero.
  *        X enters as bf16: exact for scales that are powers of two, as fp8b128_quantize
- *        writes them, else rounded.
+ *        writes them, where that is a normal number of bf16, else rounded (the largest bf16
+ *        numbers have a code of 256 at the scale 2^120, an infinity).
  *   ws   device workspace of tq_fp8b128_workspace_bytes(T, L->out, L->in) bytes, 256-byte
  *        aligned; need not be cleared. Calls that share one must be ordered on one stream.
  */
