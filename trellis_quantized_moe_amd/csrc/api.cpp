@@ -1378,7 +1378,7 @@ int backward_products(const tq_fp8b128_layer* L, const uint8_t* xq, const float*
   return ok();
 }
 
-int check_gradients(const tq_fp8b128_layer* L, void* dx, void* dw, int64_t T) {
+int check_gradients(void* dx, void* dw) {
   if (!dx && !dw) return fail(TQ_EINVAL, "dx and dw are both NULL");
   if (!aligned(dx, 16) || !aligned(dw, 16)) return fail(TQ_EALIGN, "dx and dw must be 16-byte aligned");
   return TQ_OK;
@@ -1465,7 +1465,7 @@ int fp8b128_gemm_backward(const tq_fp8b128_layer* L, const uint8_t* xq, const fl
   if (rc) return rc;
   rc = check_rows(dy, "dy", T);
   if (rc) return rc;
-  rc = check_gradients(L, dx, dw, T);
+  rc = check_gradients(dx, dw);
   if (rc) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (T == 0) return empty_gradients(L, dw, s);
@@ -1487,7 +1487,7 @@ int fp8b128_gated_backward(const tq_fp8b128_layer* gate_up, const uint8_t* xq, c
   if (rc) return rc;
   rc = check_rows(dh, "dh", T);
   if (rc) return rc;
-  rc = check_gradients(gate_up, dx, dw, T);
+  rc = check_gradients(dx, dw);
   if (rc) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (T == 0) return empty_gradients(gate_up, dw, s);

@@ -343,10 +343,6 @@ class Fp8b128Layer:
         if self._state() != self._checked:
             self.__post_init__()
 
-    def c_struct(self):
-        self.renew()
-        return self._c
-
     def __reduce__(self):
         return Fp8b128Layer, (self.codes, self.scales)  # copies and pickles hold the tensors alone
 
