@@ -318,16 +318,19 @@ class Fp8b128Layer:
     scales: torch.Tensor     # fp32 [ceil(out / 128), ceil(in / 128)]
 
     def __post_init__(self):
-        _check_rows("codes", self.codes, _E4M3)
-        out, in_ = self.codes.shape
-        dev = self.codes.device
-        blocks = -(-in_ // 128)
-        _check_rows("scales", self.scales, _F32, dev, (-(-out // 128), blocks))
-        c = _lib.Fp8b128LayerC(out, in_, self.codes.data_ptr(), self.scales.data_ptr())
+        state = self._state()
+        codes_at, scales_at, shape, scales_shape, dtype, scales_dtype, dev, scales_dev, whole, scales_whole = state
+        out, in_ = shape if len(shape) == 2 else (0, 0)
+        fit = (-(-out // 128), -(-in_ // 128))
+        if not (len(shape) == 2 and dtype in _E4M3 and scales_dtype == torch.float32
+                and scales_shape == fit and whole and scales_whole and scales_dev == dev
+                and self.codes.is_cuda):  # the same checks, with their messages
+            _check_rows("codes", self.codes, _E4M3)
+            _check_rows("scales", self.scales, _F32, dev, fit)
+        c = _lib.Fp8b128LayerC(out, in_, codes_at, scales_at)
         d = self.__dict__
-        d["out"], d["in_"], d["blocks"], d["device"] = out, in_, blocks, dev
-        d["_c"], d["_ref"] = c, ctypes.byref(c)
-        d["_checked"] = self._state()
+        d["out"], d["in_"], d["blocks"], d["device"] = out, in_, fit[1], dev
+        d["_c"], d["_ref"], d["_checked"] = c, ctypes.byref(c), state
 
     def _state(self):
         """All that the checks and the C struct depend on."""
