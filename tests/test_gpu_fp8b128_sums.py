@@ -97,7 +97,7 @@ def assert_within(got, ref, tol):
 
 
 @pytest.mark.parametrize("make", [cancelling, outliers])
-@pytest.mark.parametrize("out,n", [(16, 16), (272, 400), (2080, 272)])
+@pytest.mark.parametrize("out,n", [(16, 16), (16, 400), (272, 400), (2080, 272)])
 def test_products(make, out, n):
     c = Rows(*make(max(TOKENS), out, n))
     for T in TOKENS:
@@ -110,8 +110,8 @@ def test_products(make, out, n):
 
 def test_what_the_fp8_matrix_cores_cut():
     # 7.5 is below 2^-13 of 2^(8 + 8) and beside such a pair nothing of it is kept; 8 is
-    for small, kept in ((7.5, 0.0), (8.0, 8.0)):
-        c = Rows(*cancelling(300, 16, 128, small))
+    for out, small, kept in ((16, 7.5, 0.0), (16, 8.0, 8.0), (96, 7.5, 0.0)):
+        c = Rows(*cancelling(300, out, 128, small))
         exact = 96 * small
         assert (c.ref == exact).all()
         for T in (1, 2, 3, 300):
@@ -127,7 +127,7 @@ def gated_bounds(c, T):
 
 
 @pytest.mark.parametrize("make", [cancelling, outliers])
-@pytest.mark.parametrize("out,n", [(32, 16), (288, 400), (2080, 272)])
+@pytest.mark.parametrize("out,n", [(32, 16), (32, 400), (288, 400), (2080, 272)])
 def test_gated_and_gradients(make, out, n):
     x, w = make(max(TOKENS), out, n)
     # sums of the order of one, so that the gate is not saturated everywhere

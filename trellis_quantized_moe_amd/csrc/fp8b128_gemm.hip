@@ -14,13 +14,13 @@ namespace tq {
 
 namespace {
 
-// ---- one or two tokens: a channel per wave ---------------------------------------------------
+// ---- one or two tokens, few channels: a channel per wave --------------------------------------
 //
 // A wave owns one channel (gated: its gate and up rows) and reads the rows 1,024 inputs at a time,
 // 16 bytes a lane, D such steps ahead; the products are fp32 multiply-adds of the decoded codes
 // (exact products), a lane's 16 are scaled once, and the lanes are added at the end. Bound by
 // latency: the waves of all channels read their few kilobytes at once (one token x 5,120 x 1,536
-// in 4.4 us, 1.8 TB/s; by strips it took 7.4).
+// in 4.4 us, 1.8 TB/s).
 constexpr int FR_WAVES = 4;
 
 // Adds v over the 64 lanes (every lane gets the sum; the order is fixed).
@@ -162,10 +162,10 @@ struct FbStrip {
   };
 };
 
-template <int EPI, int NS, int TT>
+template <int EPI, int NS, int TT, bool EXACT>
 __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
   using S = FbStrip<NS, TT>;
-  constexpr bool GATED = fb_gated(EPI), EXACT = EPI == FB_F32;
+  constexpr bool GATED = fb_gated(EPI);
   constexpr int NO = GATED ? NS / 2 : NS;  // strips of results
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -283,10 +283,10 @@ __device__ void fb_strip(const Fp8b128GemmArgs& a, FbStrip<NS, TT>& sh) {
   }
 }
 
-template <int EPI, int NS, int TT>
+template <int EPI, int NS, int TT, bool EXACT>
 __global__ __launch_bounds__((64 * FbStrip<NS, TT>::W)) void fp8b128_strip_kernel(Fp8b128GemmArgs a) {
   __shared__ FbStrip<NS, TT> sh;
-  fb_strip<EPI, NS, TT>(a, sh);
+  fb_strip<EPI, NS, TT, EXACT>(a, sh);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -296,9 +296,9 @@ int64_t strip_groups(const Fp8b128GemmArgs& a) {  // workgroups
   constexpr int NO = fb_gated(EPI) ? NS / 2 : NS;
   return ceil_div(fb_gated(EPI) ? a.out / 2 : a.out, 16 * NO) * ceil_div(a.T, 16 * TT);
 }
-template <int EPI, int NS, int TT>
+template <int EPI, int NS, int TT, bool EXACT = EPI == FB_F32>
 hipError_t launch_strip(const Fp8b128GemmArgs& a, hipStream_t s) {
-  return launch_timed(fp8b128_strip_kernel<EPI, NS, TT>, dim3((unsigned)strip_groups<EPI, NS, TT>(a)),
+  return launch_timed(fp8b128_strip_kernel<EPI, NS, TT, EXACT>, dim3((unsigned)strip_groups<EPI, NS, TT>(a)),
                       dim3(64 * FbStrip<NS, TT>::W), s, a);
 }
 
@@ -596,6 +596,21 @@ hipError_t launch_tiles(const Fp8b128GemmArgs& a, hipStream_t s) {
   return launch_timed(fp8b128_tile_kernel<EPI, SW, WT, ST, !fb_gated(EPI)>, grid, block, s, a, n);
 }
 
+// One or two tokens: exact products in both kernels. A channel per wave has short waves that all
+// read at once, but its time grows with the channels; a strip's waves share a row's inputs and
+// its time grows with them. Measured (us, a channel per wave / strips; gated in brackets), one
+// token: 5,120 x 1,536 4.7 / 4.9 (4.6 / 5.4), 7,168 x 768 3.9 / 5.7 (4.4 / 6.4), 16,384 x 1,536
+// 7.0 / 9.5, 16,384 x 5,120 18.6 / 19.0, 2,048 x 5,120 5.7 / 4.2, 768 x 5,120 5.3 / 3.3, 5,120 x
+// 10,240 17.2 / 13.5, 256 x 20,480 14.0 / 4.3; two: 16,384 x 1,536 8.6 / 9.6, 5,120 x 768 4.0 /
+// 4.5, 5,120 x 1,536 5.5 / 5.0, 7,168 x 5,120 13.4 / 10.8, 256 x 20,480 19.2 / 4.4. Over 70 sizes
+// of 256 to 16,384 inputs and 256 to 20,480 channels the choice took 0.3 % more than the faster on
+// average, at most 10 % (gated: 1.2 % and, at 16,384 x 10,240, 28 %).
+template <int EPI>
+hipError_t launch_few(const Fp8b128GemmArgs& a, hipStream_t s) {
+  if (a.in >= 2 * a.T * a.out) return launch_rows<EPI>(a, s);
+  return launch_strip<EPI, fb_gated(EPI) ? 2 : 1, 1, true>(a, s);
+}
+
 // The kernel with the least time expected, beside the 3.7 us that all have in common (0.01 us; bf16
 // results / fp32 results). Of strips, by the rounds of workgroups over the compute units and the
 // blocks of 128 inputs of a wave, an eighth of all:
@@ -612,7 +627,7 @@ hipError_t launch_tiles(const Fp8b128GemmArgs& a, hipStream_t s) {
 template <int EPI>
 hipError_t launch_forward(const Fp8b128GemmArgs& a, hipStream_t s) {
   constexpr bool EXACT = EPI == FB_F32;
-  if (a.T <= 2) return launch_rows<EPI>(a, s);
+  if (a.T <= 2) return launch_few<EPI>(a, s);
   typedef hipError_t (*Launch)(const Fp8b128GemmArgs&, hipStream_t);
   int64_t least = INT64_MAX;
   Launch best = nullptr;
