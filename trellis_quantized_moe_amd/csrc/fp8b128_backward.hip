@@ -824,7 +824,10 @@ hipError_t launch_dw(const Fp8b128BackwardArgs& a, hipStream_t s) {
 // 11 TB/s from L2; a workgroup of two ranges 200 + 110 a step of 64 tokens, of one 30 + 70. Where
 // all workgroups have a compute unit the longer of the two counts, else their sum over the compute
 // units and a last round of the shorter. The constants are a fit to calls of 1 to 512 tokens and 64
-// to 5,120 channels; a choice by them took 0.5 % more than the fastest on average. Measured, apart
+// to 5,120 channels; a choice by them, with 250 for the second launch of two apart, took 2.2 % more
+// than the fastest on average over 137 such calls, 28 % at most (333 x 4,000 x 800: 22.8 us by (4,
+// 2), 17.9 by (4, 4)); with 110 it took 201 x 2,576 x 1,440 apart, 16.9 us, 15.4 by (4, 2), and 48
+// x 5,120 x 4,096, 26.1 and 20.9. Measured, apart
 // / (4, 1) / (4, 2) / (4, 4): 8 tokens x 768 inputs x 768 outputs 8.4 / 5.7 / 5.4 / 6.5 us, x 5,120
 // x 4,096 29.2 / 20.1 / 19.9 / 22.8; 333 x 768 x 5,120 23.6 / 24.2 / 16.4 / 20.7, x 768 x 768 13.5
 // / 15.6 / 10.1 / 10.1; 130 x 2,576 x 1,440 15.1 / 15.2 / 15.0 / 10.9; 512 x 5,120 x 1,536 35.2 /
@@ -871,7 +874,7 @@ hipError_t launch_fp8b128_backward(const Fp8b128BackwardArgs& args, hipStream_t 
   int kind = dx.kind;
   bool with_dw = false;
   if (a.dw && a.splits > 0) {
-    int64_t least = dx.cost + dw.cost + 110;
+    int64_t least = dx.cost + dw.cost + 250;
     auto offer = [&](int k, int64_t cost) {
       if (cost < least) {
         least = cost;
