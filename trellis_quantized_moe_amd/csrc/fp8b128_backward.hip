@@ -43,8 +43,11 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
 // are issued between its products. A block's products are added from zero and then scaled into the
 // sums; the waves' sums are added in wave order. All workgroups together read 11 to 13 TB/s from
 // L2, a third of what loads alone reach, as a wave's loads, LDS reads and products follow one
-// another: 333 tokens x 768 inputs x 5,120 outputs take 13.1 us. 32 x 5,120 x 4,096 take 10.5 us;
-// with neighbouring strips on different XCDs, each reading the lines they share, it was 17.3.
+// another: 333 tokens x 768 inputs x 5,120 outputs take 12.6 us. 32 x 5,120 x 4,096 take 10.5 us;
+// with neighbouring strips on different XCDs, each reading the lines they share, it was 17.3. The
+// kernel that strips share with dw leaves one workgroup to a compute unit; in a kernel of their own
+// with 84 to 226 registers and 48 to 128 KiB of LDS, of which two of the smaller fit, they took as
+// long (63 calls of 1 to 768 tokens: 0.7 % more on average, within 3 %).
 template <int NS, int TT>
 struct DxStrip {
   static constexpr int IW = 16 * NS, W = 8;
@@ -218,7 +221,7 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, const f32x4 (&acc)[4][N
 // 256 bytes of dy go straight to one of two LDS stages. A wave takes the block strip by strip of 16
 // inputs: the strip's codes become bf16 once, its products with the block's dy (in registers for
 // all strips) are added from zero, and the strip before it is scaled into its sums meanwhile.
-// 8,192 tokens x 5,120 inputs x 1,536 outputs take 120 to 130 us (1.0 to 1.07 PFLOP/s), the matrix
+// 8,192 tokens x 5,120 inputs x 1,536 outputs take 119 to 130 us (1.0 to 1.08 PFLOP/s), the matrix
 // cores busy 56 % of the cycles at 1.88 GHz; in steps of 64 outputs, with the sums of a whole block
 // waiting to be scaled at once, it was 136 us and 48 %.
 struct DxShared {
@@ -423,8 +426,8 @@ __global__ __launch_bounds__(256) void fp8b128_widen_kernel(const uint8_t* __res
 // 64 inputs of 64 (32) channels; steps of 64 tokens through a ring of three LDS stages, two steps
 // ahead. A row's 32-byte chunk c lies at position c ^ swizzle(row): the LDS serves 32 lanes at a
 // time, which read one chunk of rows 8 q + 0..3 and 8 (q + 1) + 0..3 (or + 4..7), and those eight
-// rows get eight different positions. 8,192 tokens x 5,120 inputs x 1,536 channels take 112 to 118
-// us (1.1 PFLOP/s), the matrix cores busy 61 % of the cycles at 1.75 GHz.
+// rows get eight different positions. 8,192 tokens x 5,120 inputs x 1,536 channels take 112 to 122
+// us (1.06 to 1.15 PFLOP/s), the matrix cores busy 61 % of the cycles at 1.75 GHz.
 __device__ __forceinline__ int dw_swizzle(int row) { return (row & 3) | (row >> 1 & 4); }
 
 struct DwShared {

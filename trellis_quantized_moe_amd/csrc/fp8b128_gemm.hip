@@ -20,7 +20,7 @@ namespace {
 // 16 bytes a lane, D such steps ahead; the products are fp32 multiply-adds of the decoded codes
 // (exact products), a lane's 16 are scaled once, and the lanes are added at the end. Bound by
 // latency: the waves of all channels read their few kilobytes at once (one token x 5,120 x 1,536
-// in 4.4 us, 1.8 TB/s).
+// in 4.6 us, 1.7 TB/s).
 constexpr int FR_WAVES = 4;
 
 // Adds v over the 64 lanes (every lane gets the sum; the order is fixed).
@@ -310,10 +310,10 @@ hipError_t launch_strip(const Fp8b128GemmArgs& a, hipStream_t s) {
 // end in one lane) and 4 tiles of 16 tokens. Per block of 128 inputs the rows' 128 bytes go
 // straight to LDS (16-byte chunk c of row r at position c ^ (r % 8), so that eight lanes reading
 // one chunk of eight rows meet eight different banks' worth of LDS), in two or three stages with
-// one barrier per block. 8,192 tokens x 5,120 x 7,168 take 267 to 289 us (2.1 to 2.25 PFLOP/s), the
-// matrix cores busy 57 % of the cycles at 1.74 to 1.8 GHz: without its loads the kernel keeps them
-// busy 65 % at 1.62 GHz, so it is near what power allows; without three quarters of its
-// multiply-adds it takes as long.
+// one barrier per block. 8,192 tokens x 5,120 x 7,168 take 266 to 300 us as the clocks go (2.0 to
+// 2.26 PFLOP/s), the matrix cores busy 57 % of the cycles at 1.74 to 1.8 GHz: without its loads the
+// kernel keeps them busy 65 % at 1.62 GHz, so it is near what power allows; without three quarters
+// of its multiply-adds it takes as long. fp32 results take 527 to 552 us.
 template <int SW, int WT, int ST>
 struct FbTile {
   static constexpr int WAVES = 2 * WT, THREADS = 64 * WAVES, BC = 32 * SW, BT = 64 * WT;
