@@ -60,6 +60,11 @@ extern "C" {
                        /* (MXFP4), or with the T16 values rounded to E4M3 (trellis, FORMAT  */
                        /* F19); prefill mode (TQ_AUTO takes it; with TQ_GEMV an error)      */
 
+#define TQ_FP4 64u     /* MXFP4 only: the fp4 matrix cores. The activations are converted  */
+                       /* to MXFP4 (E2M1, one E8M0 scale per 32 inputs, as                 */
+                       /* mxfp4_quantize; FORMAT F29) and multiplied with the stored codes */
+                       /* (F30). Every mode, not with TQ_FP8                               */
+
 /* ---- flag of the fp8b128 products --------------------------------------------------------- */
 #define TQ_OUT_BF16 32u /* y is bf16 instead of fp32                                           */
 
@@ -245,6 +250,33 @@ int mxfp8_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, uint8
                    void* stream);
 
 /*
+ * mxfp4_quantize — the MXFP4 form of bf16 rows (FORMAT F29): per block of 32 consecutive
+ * elements of a row the E8M0 byte k + 127, k the smallest integer >= -127 with
+ * max|x| <= 7 * 2^k (127 for an all-zero block, 255 with zero codes for a block holding an
+ * infinity or NaN), and each element's E2M1 code, the nearest to x * 2^-k (ties to the even
+ * code, what lies above 6 becomes 6, the sign is kept). No element is off by more than half
+ * the step between the two values around it, or 2^k at the top. The activation conversion of
+ * TQ_FP4, exposed on its own, and the encoder of an expert layer: with rows = out, n = in,
+ * codes = the unit and scales = the unit + out*in/2 it writes one unit of tq_mxfp4_layer
+ * (FORMAT F9), which mxfp4_decode reads back.
+ *   x       device bf16 [rows][n], 16-byte aligned; n a multiple of 32 up to 2^20.
+ *   codes   device uint8 [rows][n / 2], 16-byte aligned: element 2j in the low nibble of byte j.
+ *   scales  device uint8 [rows][n / 32].
+ * rows * n must not exceed 2^33; no output may overlap the input or the other output.
+ */
+int mxfp4_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
+                   void* stream);
+
+/*
+ * mxfp4_expert_gemm with TQ_FP4 (FORMAT F30) — both operands in 4 bits:
+ *   y[t][k][o] = g[t][k] * sum_i xq[t][i] * E2M1[c_e[o][i]] * 2^(b_e[o][i/32] - 127),
+ *   xq[t][i] = E2M1[a[t][i]] * 2^(s[t][i/32] - 127)   (a, s: mxfp4_quantize of x)
+ * The matrix cores add the products of a block of 32 exactly and the blocks in fp32. A block of
+ * a token that holds an infinity or NaN makes that token's slots NaN. T * in must stay below
+ * 2^32.
+ */
+
+/*
  * fp8b32_expert_gemm — routed activations x fp8b32 expert weights.
  *
  *   y[t][k][o] = g[t][k] * sum_i x[t][i] * E4M3[c_e[o][i]] * 2^(b_e[o/32][i/32] - 127)
@@ -271,6 +303,69 @@ int fp8b32_expert_gemm(const tq_fp8b32_layer* L, const void* x, int64_t T,
  */
 int hadamard128(const void* x, void* y, int64_t rows, int64_t n, const int8_t* signs,
                 void* stream);
+
+/*
+ * A router: how the logits of a token choose its experts (FORMAT F27).
+ */
+typedef struct tq_router {
+  int32_t E;           /* experts, 1 .. 4096                                              */
+  int32_t topk;        /* experts per token, 1 .. 64, at most group_topk * E / groups     */
+  int32_t score;       /* TQ_SCORE_SOFTMAX or TQ_SCORE_SIGMOID                            */
+  int32_t groups;      /* equal groups of consecutive experts, 1 .. 64, a divisor of E    */
+  int32_t group_topk;  /* groups a token may choose from, 1 .. groups                     */
+  int32_t group_top;   /* experts whose scores make a group's: 1 (the best) or 2 (the sum */
+                       /* of the best two)                                                */
+  int32_t renorm;      /* 1: the weights are divided by their sum; 0: as scored           */
+  float scale;         /* finite factor of every weight                                   */
+  const float* bias;   /* device fp32 [E], or NULL: added to the scores for the choice    */
+                       /* alone (a bias that balances the experts' load)                  */
+} tq_router;
+#define TQ_SCORE_SOFTMAX 0
+#define TQ_SCORE_SIGMOID 1
+#define TQ_LOGITS_BF16 1u /* flag of the router calls: the logits and their gradients are bf16 */
+
+/*
+ * expert_route — the topk_ids and topk_w of the expert GEMM calls from a router's logits:
+ *   s = softmax(x) over the E experts, or s_e = 1 / (1 + e^-x_e);   c_e = s_e + bias_e
+ *   a group's score: its largest c, or the sum of its two largest (of one, where it has one);
+ *   the group_topk groups of the largest scores stay; topk_ids[t]: the topk largest c in them,
+ *   in descending order; equal ones, of groups too, by the lowest index;
+ *   topk_w[t][k] = scale * s_k / (renorm ? sum over the chosen j of s_j : 1).
+ * The choice is that of the scores in 64 bits (without a bias, that of the logits themselves,
+ * which order where scores round together); weights are fp32, off by a few 2^-24.
+ *   R         host: the router.
+ *   logits    device [T][R->E]: fp32, or bf16 with TQ_LOGITS_BF16; aligned to an element.
+ *   T         tokens (0 is a successful no-op); T * E at most 2^33.
+ *   topk_ids  device int32 [T][topk].   topk_w  device fp32 [T][topk].
+ *   flags     0 or TQ_LOGITS_BF16.
+ * A logit of -inf (or a bias of -inf) takes its expert out of the choice; a token with fewer
+ * than topk experts left gets id -1 and weight 0 in the slots that remain, so a padded token's
+ * row of -inf routes nowhere. A row with a NaN (among the logits, or as a score plus bias), or
+ * +inf under softmax, gets the ids 0 .. topk-1 and NaN weights.
+ */
+int expert_route(const tq_router* R, const void* logits, int64_t T, int32_t* topk_ids,
+                 float* topk_w, uint32_t flags, void* stream);
+
+/*
+ * expert_route_backward — the gradient of expert_route's weights with respect to the logits
+ * (FORMAT F28), the choice held fixed; the bias and the groups enter the choice alone and have
+ * none:
+ *   renorm:  r_k = s_k / sum_j s_j,  g_k = scale * (dw_k - sum_j r_j dw_j) / sum_j s_j
+ *   else     g_k = scale * dw_k;     G_e = the sum of g_k over the slots k with id e
+ *   sigmoid: dlogits_e = G_e s_e (1 - s_e);  softmax: dlogits_e = s_e (G_e - sum_k s_k g_k)
+ * computed in fp32, rounded once to the logits' type. Logits that no slot chose get exactly 0,
+ * except under softmax without renorm.
+ *   topk_ids  device int32 [T][topk]: expert_route's; -1 is an empty slot (its dw is not read);
+ *             an expert that is named twice gets both slots' gradients. An id outside [-1, E)
+ *             makes its row NaN.
+ *   dw        device fp32 [T][topk].
+ *   dlogits   device [T][E], of the logits' type; every entry is written. It may be the logits
+ *             themselves.
+ * Other arguments as expert_route.
+ */
+int expert_route_backward(const tq_router* R, const void* logits, int64_t T,
+                          const int32_t* topk_ids, const float* dw, void* dlogits,
+                          uint32_t flags, void* stream);
 
 /*
  * route_bucket — stable counting sort of the (token, slot) pairs by expert id (FORMAT F11,

@@ -38,5 +38,7 @@ from .codebooks import (MUL1_MULT, PMCGX_MULTS, mul1_value, mul1_value_array, de
                         decode_unit_pmcgx, decode_unit_pmcgx_scalar, pmcgx_values, mul1_e4m3)
 from .mx import (E4M3_MAX, e4m3_all_values, e4m3_round, mx_block_scale, quantize_mxfp8_rows,
                  dequantize_mxfp8_rows, t16_e4m3, t16_e4m3_codes, mxfp8_values)
+from .fp4 import mxfp4_scale_byte, e2m1_round, mxfp4_quantize, mxfp4_pack, mxfp4_values
+from .router import router_scores, route_row, expert_route, expert_route_backward
 
 __all__ = [name for name in dir() if not name.startswith("_")]

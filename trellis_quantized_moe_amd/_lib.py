@@ -28,6 +28,9 @@ TQ_COMBINE = 4
 TQ_ROTATE = 8
 TQ_FP8 = 16
 TQ_OUT_BF16 = 32
+TQ_FP4 = 64
+TQ_SCORE_SOFTMAX, TQ_SCORE_SIGMOID = 0, 1
+TQ_LOGITS_BF16 = 1
 TQ_CODEBOOK_T16, TQ_CODEBOOK_MUL1, TQ_CODEBOOK_PMCGX = 0, 1, 2
 
 TQ_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -73,6 +76,20 @@ class Fp8b128LayerC(ctypes.Structure):
     ]
 
 
+class RouterC(ctypes.Structure):
+    _fields_ = [
+        ("E", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("group_topk", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renorm", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("bias", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -86,6 +103,10 @@ SIGNATURES = {
                                          _P, _U32, _P, _SZ, _P]),
     "hadamard128": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P]),
     "mxfp8_quantize": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
+    "mxfp4_quantize": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
+    "expert_route": (ctypes.c_int, [ctypes.POINTER(RouterC), _P, _I64, _P, _P, _U32, _P]),
+    "expert_route_backward": (ctypes.c_int, [ctypes.POINTER(RouterC), _P, _I64, _P, _P, _P, _U32,
+                                             _P]),
     "route_bucket": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     "trellis_decode": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _I32, _P]),
     "mxfp4_decode": (ctypes.c_int, [_P, _I32, _I32, _P, _P]),

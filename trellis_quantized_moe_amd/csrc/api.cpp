@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -103,8 +104,13 @@ int check_device() {
 }
 
 bool flags_valid(uint32_t flags) {
-  return (flags & ~31u) == 0 && (flags & 3u) != 3u;
+  return (flags & ~(31u | TQ_FP4)) == 0 && (flags & 3u) != 3u;
 }
+
+// Limits of the row-wise calls: a row's elements, and those of one operand of a call (they
+// keep every grid below 2^32 threads).
+constexpr int64_t MAX_ROW = 1 << 20;
+constexpr int64_t MAX_ELEMENTS = (int64_t)1 << 33;
 
 // The prefill GEMM pays off when experts average more than 16 routed slots and its items
 // (128 routed rows of one group) are enough to give every compute unit of the GPU one;
@@ -114,7 +120,7 @@ constexpr int64_t GEMM_MIN_ITEMS = 256;
 bool use_gemm(int64_t T, int topk, int E, int groups, uint32_t flags) {
   const uint32_t mode = flags & 3u;
   if (mode == TQ_GEMV) return false;
-  if (mode == TQ_GEMM || (flags & TQ_FP8)) return true;
+  if (mode == TQ_GEMM || (flags & (TQ_FP8 | TQ_FP4))) return true;
   const int64_t N = T * topk;
   return N > 16LL * E && (int64_t)groups * ((N + 127) / 128) >= GEMM_MIN_ITEMS;
 }
@@ -233,7 +239,12 @@ WsLayout ws_layout(int64_t T, int topk, int E, int out, int in, uint32_t flags, 
     L.n_items = off;
     off += 256;
     L.route_bytes = off - start;
-    if (!mxfp4 && !(flags & TQ_FP8)) {  // the trellis GEMM reads prepared f16 activations
+    if (flags & TQ_FP4) {  // MXFP4 activations
+      L.xa = off;
+      off += round_up((size_t)T * in / 2, 256);
+      L.xs = off;
+      off += round_up((size_t)T * in / 32, 256);
+    } else if (!mxfp4 && !(flags & TQ_FP8)) {  // the trellis GEMM reads prepared f16 activations
       L.xprep = off;
       off += round_up((size_t)T * in * 2, 256);
       L.rowsum = off;
@@ -324,6 +335,110 @@ int mxfp8_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, uint8
   hipError_t err = tq::launch_mxfp8_prep(static_cast<const uint16_t*>(x), rows, (int)n, codes,
                                          scales, static_cast<hipStream_t>(stream));
   if (err != hipSuccess) return hip_fail(err, "mxfp8_quantize launch");
+  return ok();
+}
+
+int mxfp4_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
+                   void* stream) {
+  if (rows < 0) return fail(TQ_EINVAL, "rows = %lld is negative", (long long)rows);
+  if (n <= 0 || n % 32 || n > MAX_ROW)
+    return fail(TQ_EINVAL, "n = %lld is not a multiple of 32 in 32..%lld", (long long)n,
+                (long long)MAX_ROW);
+  if (rows > MAX_ELEMENTS / n)
+    return fail(TQ_EINVAL, "%lld rows of %lld exceed 2^33 elements", (long long)rows, (long long)n);
+  if (rows == 0) return ok();
+  if (!x || !codes || !scales) return fail(TQ_EINVAL, "x, codes or scales is NULL");
+  if (!aligned(x, 16) || !aligned(codes, 16))
+    return fail(TQ_EALIGN, "x and codes must be 16-byte aligned");
+  int rc = check_device();
+  if (rc) return rc;
+  hipError_t err = tq::launch_mxfp4_quantize(static_cast<const uint16_t*>(x), rows, (int)n, codes,
+                                             scales, static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) return hip_fail(err, "mxfp4_quantize launch");
+  return ok();
+}
+
+static int check_router(const tq_router* R, int64_t T, const void* logits, uint32_t flags) {
+  if (!R) return fail(TQ_EINVAL, "router is NULL");
+  if (R->E < 1 || R->E > 4096) return fail(TQ_EINVAL, "E = %d is outside 1..4096", R->E);
+  if (R->groups < 1 || R->groups > 64 || R->E % R->groups)
+    return fail(TQ_EINVAL, "groups = %d is not a divisor of E = %d in 1..64", R->groups, R->E);
+  if (R->group_topk < 1 || R->group_topk > R->groups)
+    return fail(TQ_EINVAL, "group_topk = %d is outside 1..%d", R->group_topk, R->groups);
+  if (R->group_top != 1 && R->group_top != 2)
+    return fail(TQ_EINVAL, "group_top = %d is not 1 or 2", R->group_top);
+  if (R->topk < 1 || R->topk > 64 || R->topk > R->group_topk * (R->E / R->groups))
+    return fail(TQ_EINVAL, "topk = %d is outside 1..64 or above the %d experts of %d groups",
+                R->topk, R->group_topk * (R->E / R->groups), R->group_topk);
+  if (R->score != TQ_SCORE_SOFTMAX && R->score != TQ_SCORE_SIGMOID)
+    return fail(TQ_EINVAL, "score = %d is not TQ_SCORE_SOFTMAX or TQ_SCORE_SIGMOID", R->score);
+  if (R->renorm != 0 && R->renorm != 1) return fail(TQ_EINVAL, "renorm = %d is not 0 or 1", R->renorm);
+  if (!std::isfinite(R->scale)) return fail(TQ_EINVAL, "scale is not finite");
+  if (!aligned(R->bias, 4)) return fail(TQ_EALIGN, "bias must be 4-byte aligned");
+  if (flags & ~TQ_LOGITS_BF16) return fail(TQ_EINVAL, "flags = 0x%x is not valid", flags);
+  if (T < 0) return fail(TQ_EINVAL, "T = %lld is negative", (long long)T);
+  if (T > MAX_ELEMENTS / R->E)
+    return fail(TQ_EINVAL, "%lld tokens of %d logits exceed 2^33", (long long)T, R->E);
+  if (T > 0 && !logits) return fail(TQ_EINVAL, "logits is NULL");
+  if (!aligned(logits, (flags & TQ_LOGITS_BF16) ? 2 : 4))
+    return fail(TQ_EALIGN, "logits must be aligned to an element");
+  return TQ_OK;
+}
+
+static tq::RouterArgs router_args(const tq_router* R, const void* logits, int64_t T, uint32_t flags) {
+  tq::RouterArgs a{};
+  a.logits = logits;
+  a.T = T;
+  a.E = R->E;
+  a.topk = R->topk;
+  a.groups = R->groups;
+  a.group_topk = R->group_topk;
+  a.group_top = R->group_top;
+  a.bf16 = (flags & TQ_LOGITS_BF16) != 0;
+  a.sigmoid = R->score == TQ_SCORE_SIGMOID;
+  a.renorm = R->renorm != 0;
+  a.scale = R->scale;
+  a.bias = R->bias;
+  return a;
+}
+
+int expert_route(const tq_router* R, const void* logits, int64_t T, int32_t* topk_ids,
+                 float* topk_w, uint32_t flags, void* stream) {
+  int rc = check_router(R, T, logits, flags);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (!topk_ids || !topk_w) return fail(TQ_EINVAL, "topk_ids or topk_w is NULL");
+  if (!aligned(topk_ids, 4) || !aligned(topk_w, 4))
+    return fail(TQ_EALIGN, "topk_ids and topk_w must be 4-byte aligned");
+  rc = check_device();
+  if (rc) return rc;
+  tq::RouterArgs a = router_args(R, logits, T, flags);
+  a.ids = topk_ids;
+  a.w = topk_w;
+  hipError_t err = tq::launch_expert_route(a, false, static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) return hip_fail(err, "expert_route launch");
+  return ok();
+}
+
+int expert_route_backward(const tq_router* R, const void* logits, int64_t T,
+                          const int32_t* topk_ids, const float* dw, void* dlogits,
+                          uint32_t flags, void* stream) {
+  int rc = check_router(R, T, logits, flags);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (!topk_ids || !dw || !dlogits) return fail(TQ_EINVAL, "topk_ids, dw or dlogits is NULL");
+  if (!aligned(topk_ids, 4) || !aligned(dw, 4))
+    return fail(TQ_EALIGN, "topk_ids and dw must be 4-byte aligned");
+  if (!aligned(dlogits, (flags & TQ_LOGITS_BF16) ? 2 : 4))
+    return fail(TQ_EALIGN, "dlogits must be aligned to an element");
+  rc = check_device();
+  if (rc) return rc;
+  tq::RouterArgs a = router_args(R, logits, T, flags);
+  a.chosen = topk_ids;
+  a.dw = dw;
+  a.dlogits = dlogits;
+  hipError_t err = tq::launch_expert_route(a, true, static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) return hip_fail(err, "expert_route_backward launch");
   return ok();
 }
 
@@ -568,6 +683,7 @@ int trellis_expert_gemm(const tq_trellis_layer* L, const void* x, int64_t T,
                         uint32_t flags, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_trellis_layer(L);
   if (rc) return rc;
+  if (flags & TQ_FP4) return fail(TQ_EINVAL, "TQ_FP4 applies to MXFP4 layers only");
   if ((flags & TQ_FP8) && (flags & 3u) == TQ_GEMV)
     return fail(TQ_EINVAL, "TQ_FP8 runs in the prefill mode only (not with TQ_GEMV)");
   if ((flags & TQ_FP8) && T * (int64_t)L->in >= ((int64_t)1 << 31))
@@ -759,6 +875,14 @@ int mx_expert_gemm(const MxLayer* L, const void* x, int64_t T, const int32_t* to
     return fail(TQ_EINVAL, "TQ_FP8 runs in the prefill mode only (not with TQ_GEMV)");
   if ((flags & TQ_FP8) && T * (int64_t)L->in >= ((int64_t)1 << 31))
     return fail(TQ_EINVAL, "the MXFP8 activations (T * in bytes) must stay below 2^31");
+  if ((flags & TQ_FP4) && L->fmt != tq::MX_FP4)
+    return fail(TQ_EINVAL, "TQ_FP4 applies to MXFP4 layers only");
+  if ((flags & TQ_FP4) && (flags & TQ_FP8))
+    return fail(TQ_EINVAL, "TQ_FP4 and TQ_FP8 exclude each other");
+  if ((flags & TQ_FP4) && (flags & 3u) == TQ_GEMV)
+    return fail(TQ_EINVAL, "TQ_FP4 runs in the prefill mode only (not with TQ_GEMV)");
+  if ((flags & TQ_FP4) && T * (int64_t)L->in >= ((int64_t)1 << 32))
+    return fail(TQ_EINVAL, "the MXFP4 activations (T * in / 2 bytes) must stay below 2^31");
   const int64_t unit = mx_unit_bytes(L->fmt, L->out, L->in);
   tq::WsLayout W;
   int rc = common_checks(L->E, L->out, L->in, x, T, topk_ids, topk, y, flags, ws, ws_bytes, unit, &W);
@@ -864,6 +988,34 @@ int mx_expert_gemm(const MxLayer* L, const void* x, int64_t T, const int32_t* to
     err = tq::launch_mx8_gemm(a, s);
     if (err == hipSuccess) err = time_end(s);
     if (err != hipSuccess) return hip_fail(err, "FP8 GEMM launch");
+  } else if (flags & TQ_FP4) {
+    err = tq::launch_mxfp4_quantize(xb, T, L->in, at<uint8_t>(ws, W.xa), at<uint8_t>(ws, W.xs), s);
+    if (err != hipSuccess) return hip_fail(err, "MXFP4 activation launch");
+    rc = run_route(W, ws, topk_ids, N, L->E, L->out, y_slots, s);
+    if (rc) return rc;
+    tq::Fp4GemmArgs a{};
+    a.layout = L->layout;
+    a.units = L->units;
+    a.xa = at<uint8_t>(ws, W.xa);
+    a.xa_bytes = (uint32_t)(T * L->in / 2);
+    a.xs = at<uint8_t>(ws, W.xs);
+    a.xs_bytes = (uint32_t)(T * L->in / 32);
+    a.gates = topk_w;
+    a.pairs = at<int32_t>(ws, W.pairs);
+    a.items = at<int32_t>(ws, W.items);
+    a.n_items = at<int32_t>(ws, W.n_items);
+    a.y = y_slots;
+    a.E = L->E;
+    a.out = L->out;
+    a.in = L->in;
+    a.topk = topk;
+    a.groups = W.groups;
+    a.max_items = W.max_items;
+    err = time_begin(s);
+    if (err != hipSuccess) return hip_fail(err, "hipEventRecord");
+    err = tq::launch_fp4_gemm(a, s);
+    if (err == hipSuccess) err = time_end(s);
+    if (err != hipSuccess) return hip_fail(err, "FP4 GEMM launch");
   } else {
     rc = run_route(W, ws, topk_ids, N, L->E, L->out, y_slots, s);
     if (rc) return rc;

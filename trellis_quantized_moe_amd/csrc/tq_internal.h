@@ -241,6 +241,43 @@ struct Mx8GemmArgs {
 };
 hipError_t launch_mx8_gemm(const Mx8GemmArgs& a, hipStream_t s);
 
+// MXFP4 rows (FORMAT F29): bf16 [rows][n] -> E2M1 codes [rows][n / 2] and E8M0 block scales
+// [rows][n / 32].
+hipError_t launch_mxfp4_quantize(const uint16_t* x, int64_t rows, int n, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t s);
+// The MXFP4 x MXFP4 product on the fp4 matrix cores (mxfp4_fp4.hip).
+struct Fp4GemmArgs {
+  int layout;            // 0: codes in store order; 1: repacked
+  const uint8_t* units;
+  const uint8_t* xa;     // E2M1 codes [T][in / 2]
+  uint32_t xa_bytes;     // < 2^31
+  const uint8_t* xs;     // E8M0 scales [T][in / 32]
+  uint32_t xs_bytes;
+  const float* gates;
+  const int32_t* pairs;
+  const int32_t* items;
+  const int32_t* n_items;
+  float* y;
+  int E, out, in, topk, groups, max_items;
+};
+hipError_t launch_fp4_gemm(const Fp4GemmArgs& a, hipStream_t s);
+
+// The router's choice and its gradient (FORMAT F27, F28; expert_route.hip).
+struct RouterArgs {
+  const void* logits;     // fp32 or bf16 [T][E]
+  int64_t T;
+  int E, topk, groups, group_topk, group_top;
+  bool bf16, sigmoid, renorm;
+  float scale;
+  const float* bias;      // [E], or null
+  int32_t* ids;           // [T][topk]
+  float* w;               // [T][topk]
+  const int32_t* chosen;  // backward: [T][topk]
+  const float* dw;        // backward: [T][topk]
+  void* dlogits;          // backward: as logits
+};
+hipError_t launch_expert_route(const RouterArgs& a, bool backward, hipStream_t s);
+
 struct RouteArgs {
   const int32_t* ids;
   int64_t N;

@@ -12,7 +12,8 @@ import torch
 
 from . import _lib
 from ._lib import (TQ_AUTO, TQ_COMBINE, TQ_GEMM, TQ_GEMV, TQ_LAYOUT_GEMV,  # noqa: F401
-                   TQ_LAYOUT_STORE, TQ_LAYOUT_UNIT128, TQ_OUT_BF16, TQ_ROTATE, TQ_FP8, TQ_CODEBOOK_T16,
+                   TQ_LAYOUT_STORE, TQ_LAYOUT_UNIT128, TQ_OUT_BF16, TQ_ROTATE, TQ_FP8, TQ_FP4,
+                   TQ_SCORE_SOFTMAX, TQ_SCORE_SIGMOID, TQ_LOGITS_BF16, TQ_CODEBOOK_T16,
                    TQ_CODEBOOK_MUL1, TQ_CODEBOOK_PMCGX, check)
 
 
@@ -528,6 +529,122 @@ def fp8b128_ffn(gate_up, down, x, flags=0, out=None, ws=None):
     _call_on(dev, lib.fp8b128_ffn, gate_up._ref, down._ref,
              x.data_ptr(), T, out.data_ptr(), flags, ws.data_ptr(), ws.numel())
     return out
+
+
+def mxfp4_quantize(x, codes=None, scales=None):
+    """(codes uint8 [rows, n / 2], scales uint8 [rows, n / 32]): the MXFP4 form of bf16 rows (see
+    mxfp4_quantize in include/tq.h)."""
+    _check_rows("x", x, _BF16)
+    rows, n = x.shape
+    dev = x.device
+    if codes is None:
+        codes = x.new_empty((rows, n // 2), dtype=torch.uint8)
+    else:
+        _check_rows("codes", codes, _U8, dev, (rows, n // 2))
+    if scales is None:
+        scales = x.new_empty((rows, n // 32), dtype=torch.uint8)
+    else:
+        _check_rows("scales", scales, _U8, dev, (rows, n // 32))
+    _call_on(dev, _lib.load().mxfp4_quantize, x.data_ptr(), rows, n, codes.data_ptr(),
+             scales.data_ptr())
+    return codes, scales
+
+
+@dataclass(frozen=True)
+class Router:
+    """How a token's logits choose its experts (see tq_router in include/tq.h)."""
+    E: int
+    topk: int
+    score: str = "softmax"       # or "sigmoid"
+    bias: torch.Tensor = None    # fp32 [E], added to the scores for the choice alone
+    groups: int = 1
+    group_topk: int = 1
+    group_top: int = 1
+    renorm: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in _SCORES:
+            raise ValueError("score is %r, not 'softmax' or 'sigmoid'" % (self.score,))
+        b = self.bias
+        if b is not None:
+            if not b.is_cuda:
+                raise ValueError("tensors must be on the GPU")
+            if b.dtype != torch.float32 or b.shape != (self.E,) or not b.is_contiguous():
+                raise ValueError("bias must be a contiguous float32 tensor of %d values" % self.E)
+        c = _lib.RouterC(self.E, self.topk, _SCORES[self.score], self.groups, self.group_topk,
+                         self.group_top, 1 if self.renorm else 0, self.scale,
+                         None if b is None else b.data_ptr())
+        d = self.__dict__
+        d["_c"], d["_ref"], d["_checked"] = c, ctypes.byref(c), self._state()
+
+    def _state(self):
+        """All that the checks of the bias and its pointer depend on."""
+        b = self.bias
+        return None if b is None else (b.data_ptr(), b.shape, b.dtype, b.device, b.is_contiguous())
+
+    def renew(self):
+        """Checks the bias again if it has been given other memory, another shape or another
+        type. Every call does this before it uses the C struct."""
+        if self.bias is not None and self._state() != self._checked:
+            self.__post_init__()
+
+    def __reduce__(self):
+        return Router, (self.E, self.topk, self.score, self.bias, self.groups, self.group_topk,
+                        self.group_top, self.renorm, self.scale)
+
+
+_SCORES = {"softmax": TQ_SCORE_SOFTMAX, "sigmoid": TQ_SCORE_SIGMOID}
+_U8 = (torch.uint8,)
+_I32 = (torch.int32,)
+_LOGITS = (torch.float32, torch.bfloat16)
+
+
+def _check_logits(router, logits):
+    """(T, device, flags) of logits that fit the router."""
+    router.renew()
+    _check_rows("logits", logits, _LOGITS)
+    T, E = logits.shape
+    dev = logits.device
+    if E != router.E:
+        raise ValueError("logits have %d experts, the router %d" % (E, router.E))
+    if router.bias is not None and router.bias.device != dev:
+        raise ValueError("bias is on %s, not %s" % (router.bias.device, dev))
+    return T, dev, TQ_LOGITS_BF16 if logits.dtype == torch.bfloat16 else 0
+
+
+def expert_route(router, logits, ids=None, w=None):
+    """(topk_ids int32 [T, topk], topk_w fp32 [T, topk]) of fp32 or bf16 logits [T, E] (see
+    expert_route in include/tq.h)."""
+    T, dev, flags = _check_logits(router, logits)
+    shape = (T, router.topk)
+    if ids is None:
+        ids = logits.new_empty(shape, dtype=torch.int32)
+    else:
+        _check_rows("ids", ids, _I32, dev, shape)
+    if w is None:
+        w = logits.new_empty(shape, dtype=torch.float32)
+    else:
+        _check_rows("w", w, _F32, dev, shape)
+    _call_on(dev, _lib.load().expert_route, router._ref, logits.data_ptr(), T, ids.data_ptr(),
+             w.data_ptr(), flags)
+    return ids, w
+
+
+def expert_route_backward(router, logits, ids, dw, dlogits=None):
+    """The gradient [T, E] of expert_route's weights, of the logits' type, from dw [T, topk] (see
+    expert_route_backward in include/tq.h)."""
+    T, dev, flags = _check_logits(router, logits)
+    shape = (T, router.topk)
+    _check_rows("ids", ids, _I32, dev, shape)
+    _check_rows("dw", dw, _F32, dev, shape)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    else:
+        _check_rows("dlogits", dlogits, (logits.dtype,), dev, logits.shape)
+    _call_on(dev, _lib.load().expert_route_backward, router._ref, logits.data_ptr(), T,
+             ids.data_ptr(), dw.data_ptr(), dlogits.data_ptr(), flags)
+    return dlogits
 
 
 def device_status(ws):
