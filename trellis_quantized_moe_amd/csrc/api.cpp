@@ -651,7 +651,7 @@ static int rotate_outputs(const tq_trellis_layer* L, float* y, int64_t rows, hip
 }
 
 static int run_route(const tq::WsLayout& L, void* ws, const int32_t* ids, int64_t N, int E, int out,
-              float* y_slots, hipStream_t s) {
+              float* y_slots, hipStream_t s, int item_rows = tq::GEMM_MT) {
   tq::RouteArgs r{};
   r.ids = ids;
   r.N = N;
@@ -667,7 +667,7 @@ static int run_route(const tq::WsLayout& L, void* ws, const int32_t* ids, int64_
   r.y_special = y_slots;
   r.status = at<uint32_t>(ws, L.status);
   r.blocks = L.route_blocks;
-  r.item_rows = tq::GEMM_MT;
+  r.item_rows = item_rows;
   r.max_items = L.max_items;
   r.split_rows = L.split_rows;
   hipError_t err = tq::launch_route(r, s);
@@ -991,9 +991,11 @@ int mx_expert_gemm(const MxLayer* L, const void* x, int64_t T, const int32_t* to
   } else if (flags & TQ_FP4) {
     err = tq::launch_mxfp4_quantize(xb, T, L->in, at<uint8_t>(ws, W.xa), at<uint8_t>(ws, W.xs), s);
     if (err != hipSuccess) return hip_fail(err, "MXFP4 activation launch");
-    rc = run_route(W, ws, topk_ids, N, L->E, L->out, y_slots, s);
+    const int item_rows = tq::fp4_item_rows(N, L->E, L->out);
+    rc = run_route(W, ws, topk_ids, N, L->E, L->out, y_slots, s, item_rows);
     if (rc) return rc;
     tq::Fp4GemmArgs a{};
+    a.item_rows = item_rows;
     a.layout = L->layout;
     a.units = L->units;
     a.xa = at<uint8_t>(ws, W.xa);

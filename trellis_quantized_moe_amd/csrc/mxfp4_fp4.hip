@@ -2,18 +2,19 @@
 // (FORMAT F30): both operands are their E2M1 codes with their E8M0 scales as stored, nothing is
 // decoded.
 //
-// A work item is up to 128 routed rows of one expert times one group of 128 NB output channels
-// over the whole input range, in steps of 256 inputs, on four waves, wave w owning channels
-// 32 NB w .. 32 NB (w + 1) - 1 for all rows. A step is four v_mfma_scale_f32_32x32x64_f8f6f4 per
-// 32 rows and 32 channels: lane (n, h) supplies the 32 codes of block 2 s + h of the step (16
-// bytes) of row or channel n to product s, and that block's scale byte.
-//   - activations: the item's gathered rows are loaded into a 3-stage LDS ring two steps ahead by
-//     buffer loads that write LDS, 16-byte chunk c of row r at position c ^ (r % 8), so that the 8
-//     lanes the LDS serves together hit 8 chunk columns; with each row's 8 scale bytes;
-//   - weights: straight from the unit into registers, each product's codes replaced by those of
-//     the next step as soon as they have been used, and the channel's 8 scale bytes of a step too.
-// A byte permutation picks the four scale bytes of a lane's blocks, and the products name one of
-// them each.
+// A work item is up to 128 (or 256) routed rows of one expert times a group of as many output
+// channels over the whole input range, in steps of 128 inputs, on 4 (or 8) waves. The waves share
+// out the rows and channels in blocks of 32: a step is two v_mfma_scale_f32_32x32x64_f8f6f4 per
+// pair of blocks, lane (n, h) supplying the 32 codes of block 2 s + h of the step (16 bytes) of row
+// or channel n to product s, and that block's scale byte.
+//   - codes: the item's gathered rows and its channels are loaded into an LDS ring by buffer loads
+//     that write LDS, a step's 64 bytes of a row by 4 neighbouring lanes. (Loaded straight into the
+//     registers of the lanes that multiply them, neighbouring lanes would read 16 bytes of
+//     different rows: the L1 then delivers 16 bytes a clock of its 64, and was busy 86 % of the
+//     time.) Chunk c of row r lies at position c ^ (r / 4 % 4) of the row's 64 bytes, so that the
+//     16 lanes that the LDS serves together hit all of its banks;
+//   - scales: 16 bytes of a row or channel (4 steps) per load, a window of 4 steps ahead. A load's
+//     cost is set by the lines it touches: 4 bytes at a time they took as much as the codes.
 // The epilogue multiplies by the gate and writes each output once.
 #include <type_traits>
 
@@ -27,16 +28,18 @@ namespace {
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int F4_THREADS = 256;
-constexpr int F4_STAGES = 3;
-constexpr int F4_STEP = 256;           // inputs per step
-constexpr int F4_ROW = F4_STEP / 2;    // code bytes of one row per step
+constexpr int F4_ROW = 64;     // code bytes of a row per step of 128 inputs
+constexpr int F4_WINDOW = 4;   // steps whose scales are loaded together (512 inputs)
 
+template <int WAVES>
 struct F4Shared {
-  alignas(16) uint8_t a[F4_STAGES][GEMM_MT * F4_ROW];
-  alignas(16) uint2 s[F4_STAGES][GEMM_MT];  // the row's 8 block scales of the step
-  int slot[GEMM_MT];
-  float gate[GEMM_MT];
+  static constexpr int kRows = 32 * WAVES;  // of an item, and channels of its group
+  static constexpr int kStages = 4;
+  // the rows' codes, then the channels'; one scale window of each, two windows
+  alignas(16) uint8_t codes[kStages][2 * kRows * F4_ROW];
+  alignas(16) uint8_t scales[2][2 * kRows * 16];
+  int slot[kRows];
+  float gate[kRows];
 };
 
 __device__ __forceinline__ i32x8 fp4_operand(u32x4 c) {
@@ -49,187 +52,249 @@ __device__ __forceinline__ f32x16 mfma_fp4(u32x4 a, u32x4 b, f32x16 c, uint32_t 
                                                          (int)sa, S, (int)sb);
 }
 
-// MBK: the blocks of 32 rows that the products run over (rows past the item are zeros).
-template <int LAYOUT, int MBK, int NB>
-__device__ void f4_item(const Fp4GemmArgs& a, F4Shared& sh, const uint8_t* unit, int grp,
+// WR waves share out the rows (MB blocks of 32 each), WAVES / WR the channels (NB blocks each);
+// rows past the item are zeros.
+template <int LAYOUT, int WAVES, int WR, int MB, int NB>
+__device__ __forceinline__ void f4_item(const Fp4GemmArgs& a, F4Shared<WAVES>& sh, const uint8_t* unit, int first,
                         int nrows, int channels) {
   using U = MxUnit<MX_FP4>;
+  using S = F4Shared<WAVES>;
+  static_assert(WAVES / WR * NB * 32 == S::kRows && WR * MB * 32 <= S::kRows, "the item's shape");
+  static_assert(S::kStages == F4_WINDOW, "a step's stage is its place in the window");
+  constexpr int LA = (WR * MB * 2 + WAVES - 1) / WAVES, LB = 2;  // loads of 16 rows per wave and step
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, n = lane & 31;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nsteps = a.in / F4_STEP;  // even (in is a multiple of 512)
+  const int wr = WR == 1 ? 0 : w % WR, wc = w / WR;
+  const int nsteps = a.in / 128;  // a multiple of 4
 
-  // instruction j of wave w fills rows 32 w + 8 j .. + 7 of a stage: lane l writes position l % 8
-  // of row 32 w + 8 j + l / 8, which holds chunk (l % 8) ^ (row % 8). Rows past the item load from
-  // beyond the buffer's end (xa_bytes < 2^31) and read zeros.
+  // Load i of wave w fills rows 16 (w + WAVES i) .. + 15 of a stage: lane l writes position l % 4 of
+  // row l / 4 of them. Rows past the item load from beyond the buffers' ends (below 2^31 bytes) and
+  // read zeros; channels past the group read its last one (their outputs are not stored).
   const GemmRsrc ra = gemm_rsrc(a.xa, a.xa_bytes), rs = gemm_rsrc(a.xs, a.xs_bytes);
-  uint32_t avo[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = 32 * w + 8 * j + (lane >> 3);
-    const int c = (lane & 7) ^ (r & 7);
-    avo[j] = r < nrows ? (uint32_t)(sh.slot[r] / a.topk) * (uint32_t)(a.in / 2) + 16u * c : 0x80000000u;
-  }
-  // scales: lane l loads half l % 2 of the 8 bytes of row 32 w + l / 2
-  const int srow = 32 * w + (lane >> 1);
-  const uint32_t svo = srow < nrows ? (uint32_t)(sh.slot[srow] / a.topk) * (uint32_t)(a.in / 32) + 4u * (lane & 1)
-                                    : 0x80000000u;
-  // past the last step: the last step's again, into a stage no step reads any more, so every step
-  // issues the same loads
-  auto load_a = [&](int st, int kk) {
-    uint8_t* base = sh.a[st] + 32 * w * F4_ROW;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsPtr)(base + 8 * j * F4_ROW), 16, avo[j],
-                                               (uint32_t)(F4_ROW * kk), 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(&sh.s[st][32 * w]), 4, svo,
-                                             (uint32_t)(8 * kk), 0, 0);
-  };
-
-  // weights: channels past the group read its last one (their outputs are not stored). Block
-  // 2 s + h of step kk is, in store order, 128 kk + 32 s bytes after block h; in the read order it
-  // lies in step 2 kk + s / 2 of 128 inputs, 32 (s % 2) bytes further.
   const GemmRsrc rb = gemm_rsrc(unit, (uint32_t)U::unit_bytes(a.out, a.in));
-  const int first = grp * 128 * NB;
-  uint32_t bvo[NB], bso[NB];
+  uint32_t avo[LA], bvo[LB];
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int oc = 32 * (NB * w + nb) + n;
-    const int o = first + (oc < channels ? oc : channels - 1);
-    bvo[nb] = LAYOUT ? U::packed_at(a.out, a.in, o, h) : U::stored_at(a.in, o, h);
-    bso[nb] = U::scale_at(a.out, a.in, o, 0);
+  for (int i = 0; i < LA; ++i) {
+    const int r = 16 * (w + WAVES * i) + (lane >> 2), c = (lane & 3) ^ ((r >> 2) & 3);
+    avo[i] = r < nrows ? (uint32_t)(sh.slot[r] / a.topk) * (uint32_t)(a.in / 2) + 16u * c : 0x80000000u;
   }
-  const int oc0 = 32 * NB * w < channels ? 32 * NB * w : channels - 1;
-  const uint32_t pstep = 1024u * U::group_strips(a.out, (first + oc0) / 128);
-  auto boff = [&](int kk, int s) {
-    return LAYOUT ? pstep * (uint32_t)(2 * kk + (s >> 1)) + 32u * (s & 1) : 128u * (uint32_t)kk + 32u * s;
-  };
-  u32x4 bc[4][NB];
-  u32x2 sw[NB];
-  auto load_b = [&](int s, int kk) {
+  uint32_t pstep = 64;  // a channel's next step, in store order; in the read order, the group's
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-      bc[s][nb] = __builtin_amdgcn_raw_buffer_load_b128(rb, bvo[nb], boff(kk, s), 0);
-  };
-  auto load_s = [&](int kk) {
+  for (int i = 0; i < LB; ++i) {
+    const int r = 16 * (w + WAVES * i) + (lane >> 2), c = (lane & 3) ^ ((r >> 2) & 3);
+    const int o = first + (r < channels ? r : channels - 1);
+    bvo[i] = LAYOUT ? U::packed_at(a.out, a.in, o, c) : U::stored_at(a.in, o, c);
+  }
+  uint32_t bstep[LB];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-      sw[nb] = __builtin_amdgcn_raw_buffer_load_b64(rb, bso[nb], 8u * (uint32_t)kk, 0);
+  for (int i = 0; i < LB; ++i) {
+    const int r = 16 * (w + WAVES * i);
+    const int o = first + (r < channels ? r : channels - 1);
+    bstep[i] = LAYOUT ? __builtin_amdgcn_readfirstlane(1024u * U::group_strips(a.out, o / 128)) : pstep;
+  }
+  // load i of this wave: of rows, then of channels
+  auto load_codes = [&](int i, int st, int kk, uint32_t past) {
+    uint8_t* rows = sh.codes[st] + 16 * F4_ROW * w;
+    if (i < LA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsPtr)(rows + 16 * F4_ROW * WAVES * i), 16, avo[i < LA ? i : 0] | past,
+                                               (uint32_t)(F4_ROW * kk), 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsPtr)(rows + S::kRows * F4_ROW + 16 * F4_ROW * WAVES * (i - LA)), 16,
+                                               bvo[i < LA ? 0 : i - LA] | past, bstep[i < LA ? 0 : i - LA] * (uint32_t)kk, 0, 0);
+  };
+  // scales: wave w loads those of rows 64 w .. + 63 of the item's, then of the group's
+  const int sr = 64 * (w % (WAVES / 2)) + lane;
+  const bool of_rows = w < WAVES / 2;
+  const GemmRsrc rscale = of_rows ? rs : rb;
+  const uint32_t svo =
+      of_rows ? (sr < nrows ? (uint32_t)(sh.slot[sr] / a.topk) * (uint32_t)(a.in / 32) : 0x80000000u)
+              : U::scale_at(a.out, a.in, first + (sr < channels ? sr : channels - 1), 0);
+  auto load_scales = [&](int slot, int kk, uint32_t past) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rscale, (LdsPtr)(sh.scales[slot] + 64 * 16 * w), 16, svo | past,
+                                             (uint32_t)(4 * kk), 0, 0);
   };
 
-  f32x16 acc[MBK][NB];
+  f32x16 acc[MB][NB];
 #pragma unroll
-  for (int mb = 0; mb < MBK; ++mb)
+  for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[mb][nb][i] = 0.0f;
 
-  const uint32_t sel = h ? 0x07050301u : 0x06040200u;  // bytes 2 s + h of eight
-  uint32_t rd[4];  // chunk 2 s + h of row n (row % 8 = n % 8)
+  const int row0 = 32 * MB * wr + n, col0 = 32 * NB * wc + n;
+  uint32_t at[2];  // chunk 2 s + h of row n (blocks start at multiples of 32 rows)
 #pragma unroll
-  for (int s = 0; s < 4; ++s) rd[s] = F4_ROW * n + 16u * ((2 * s + h) ^ (n & 7));
+  for (int s = 0; s < 2; ++s) at[s] = 16u * ((2 * s + h) ^ ((n >> 2) & 3));
 
-  load_a(0, 0);
-  load_s(0);
+  uint32_t sa[MB], sb[NB];
+  u32x4 wa[MB], wb[NB];  // a window's scales
+  u32x4 va[2][MB], vb[2][NB];
+  // read i of the codes of product s of the step in stage st: of channels, then of rows
+  auto read_codes = [&](int i, int st, int s) {
+    if (i < NB)
+      vb[s][i < NB ? i : 0] =
+          *reinterpret_cast<const u32x4*>(sh.codes[st] + F4_ROW * (S::kRows + col0 + 32 * i) + at[s]);
+    else
+      va[s][i < NB ? 0 : i - NB] =
+          *reinterpret_cast<const u32x4*>(sh.codes[st] + F4_ROW * (row0 + 32 * (i - NB)) + at[s]);
+  };
+  auto read_scales = [&](int slot) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s) load_b(s, 0);
-  load_a(1, 1);
-
-  int stage = 0;
+    for (int mb = 0; mb < MB; ++mb)
+      wa[mb] = *reinterpret_cast<const u32x4*>(sh.scales[slot] + 16 * (row0 + 32 * mb));
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+      wb[nb] = *reinterpret_cast<const u32x4*>(sh.scales[slot] + 16 * (S::kRows + col0 + 32 * nb));
+  };
+  load_scales(0, 0, 0);
+#pragma unroll
+  for (int k = 0; k < S::kStages; ++k)
+#pragma unroll
+    for (int i = 0; i < LA + LB; ++i) load_codes(i, k, k, 0);
+  wait_vmcnt<3 * (LA + LB)>();
+  bare_barrier();
+  read_scales(0);
+#pragma unroll
+  for (int i = 0; i < MB + NB; ++i) read_codes(i, 0, 0);
+  // A step's reads from LDS run beside products: those of product 1 beside the products 0, those of
+  // the next step's product 0 beside the products 1. The barrier between them says that every wave
+  // has read all of this step's stage, which the loads of four steps on then fill, and that the
+  // next stage has landed. Reads and loads are spread between the products: a wave whose load finds
+  // the queue full, because all waves load at once, could not multiply meanwhile. All products stay
+  // in the loop: the compiler would sink those behind the last barrier into the epilogue's branches,
+  // where lanes that store nothing do not prepare their operands.
 #pragma unroll 1
-  for (int kk = 0; kk < nsteps; ++kk) {
-    // this wave's loads of stage kk have landed: what may be in flight are those issued since
-    // (5 of stage kk + 1, the weights' scales and codes of step kk)
-    wait_vmcnt<5 + 5 * NB>();
-    bare_barrier();
-    load_a(stage >= 1 ? stage - 1 : F4_STAGES - 1, kk + 2 < nsteps ? kk + 2 : nsteps - 1);
-    const uint8_t* st = sh.a[stage];
-    uint32_t sa[MBK], sb[NB];
+  for (int k0 = 0; k0 < nsteps; k0 += F4_WINDOW) {
+    // in the last window nothing is left to load: the same loads, from beyond the buffers' ends
+    const uint32_t past = k0 + F4_WINDOW >= nsteps ? 0x80000000u : 0u;
+    const int slot = (k0 / F4_WINDOW) & 1;
 #pragma unroll
-    for (int mb = 0; mb < MBK; ++mb) {
-      const uint2 v = sh.s[stage][32 * mb + n];
-      sa[mb] = perm(v.y, v.x, sel);
-    }
+    for (int t = 0; t < F4_WINDOW; ++t) {
+      // bytes h and 2 + h of the step's four scales to bytes 0 and 2
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) sb[nb] = perm(sw[nb].y, sw[nb].x, sel);
-    const int next = kk + 1 < nsteps ? kk + 1 : kk;
-    load_s(next);
-    auto product = [&](auto S) {
-      constexpr int s = decltype(S)::value;
+      for (int mb = 0; mb < MB; ++mb) sa[mb] = wa[mb][t] >> (8 * h);
 #pragma unroll
-      for (int mb = 0; mb < MBK; ++mb) {
-        const u32x4 av = *reinterpret_cast<const u32x4*>(st + 32 * F4_ROW * mb + rd[s]);
+      for (int nb = 0; nb < NB; ++nb) sb[nb] = wb[nb][t] >> (8 * h);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma_fp4<s>(av, bc[s][nb], acc[mb][nb], sa[mb], sb[nb]);
+      for (int mb = 0; mb < MB; ++mb) {
+#pragma unroll
+        for (int i = (MB + NB) * mb / MB; i < (MB + NB) * (mb + 1) / MB; ++i) read_codes(i, t, 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma_fp4<0>(vb[0][nb], va[0][mb], acc[mb][nb], sb[nb], sa[mb]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      load_b(s, next);
-    };
-    product(std::integral_constant<int, 0>{});
-    product(std::integral_constant<int, 1>{});
-    product(std::integral_constant<int, 2>{});
-    product(std::integral_constant<int, 3>{});
-    stage = stage + 1 < F4_STAGES ? stage + 1 : 0;
+      // in flight may be the loads of the two stages after the next
+      wait_vmcnt<2 * (LA + LB)>();
+      bare_barrier();
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        if (mb == 0 && t + 1 == F4_WINDOW) read_scales(slot ^ 1);  // after the last step: of no use
+#pragma unroll
+        for (int i = (MB + NB) * mb / MB; i < (MB + NB) * (mb + 1) / MB; ++i) read_codes(i, (t + 1) % S::kStages, 0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma_fp4<2>(vb[1][nb], va[1][mb], acc[mb][nb], sb[nb], sa[mb]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = (LA + LB) * mb / MB; i < (LA + LB) * (mb + 1) / MB; ++i) load_codes(i, t, k0 + t + S::kStages, past);
+        if (mb == MB - 1 && t == 0) load_scales(slot ^ 1, k0 + F4_WINDOW, past);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
   }
-  // no load may still be writing this workgroup's LDS when it ends
+  // The epilogue: element 4 j + i of lane (n, h) is channel 8 j + 4 h + i of a block, of the block's
+  // row n. Each wave brings its rows together in LDS (its own part of the stages, once no load
+  // writes them any more) and writes them in pieces of 128 NB bytes: stored from the lanes as they
+  // are, 16 bytes of 32 rows at a time, the results of the largest case took 95 us of 352.
   wait_vmcnt<0>();
-
+  bare_barrier();
+  constexpr int kLine = 128 * NB + 16;  // the 16 bytes more put a row's pieces on other banks
+  static_assert(WAVES * 32 * kLine <= (int)sizeof(sh.codes), "the stages hold the waves' rows");
+  uint8_t* part = &sh.codes[0][0] + w * 32 * kLine;
+  constexpr int kLanes = 8 * NB, kRowsAt = 64 / kLanes;  // lanes of a row, rows at a time
+  const int oc = 32 * NB * wc + 4 * (lane % kLanes);
 #pragma unroll
-  for (int mb = 0; mb < MBK; ++mb) {
+  for (int mb = 0; mb < MB; ++mb) {
+    const float gate = sh.gate[row0 + 32 * mb];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 32 * mb + 8 * (i >> 2) + 4 * h + (i & 3);
-      if (r < nrows) {
-        float* dst = a.y + (size_t)sh.slot[r] * a.out + first;
-        const float gate = sh.gate[r];
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int oc = 32 * (NB * w + nb) + n;
-          if (oc < channels) dst[oc] = acc[mb][nb][i] * gate;
-        }
-      }
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f32x4*>(part + n * kLine + 128 * nb + 32 * j + 16 * h) =
+            (f32x4){acc[mb][nb][4 * j] * gate, acc[mb][nb][4 * j + 1] * gate, acc[mb][nb][4 * j + 2] * gate,
+                    acc[mb][nb][4 * j + 3] * gate};
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 32 / kRowsAt; ++i) {
+      const int m = kRowsAt * i + lane / kLanes, r = 32 * (MB * wr + mb) + m;
+      const f32x4 v = *reinterpret_cast<const f32x4*>(part + m * kLine + 16 * (lane % kLanes));
+      if (r < nrows && oc < channels)  // channels is a multiple of 16
+        *reinterpret_cast<f32x4*>(a.y + (size_t)sh.slot[r] * a.out + first + oc) = v;
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int NB>
-__global__ __launch_bounds__(F4_THREADS, NB == 2 ? 2 : 3) void fp4_gemm_kernel(Fp4GemmArgs a) {
-  __shared__ F4Shared sh;
+template <int WAVES, int LAYOUT>
+__device__ __forceinline__ void f4_rows(const Fp4GemmArgs& a, F4Shared<WAVES>& sh, const uint8_t* unit, int first,
+                        int nrows, int channels) {
+  if constexpr (WAVES == 8) {
+    if (nrows > 192)
+      f4_item<LAYOUT, 8, 2, 4, 2>(a, sh, unit, first, nrows, channels);
+    else if (nrows > 128)
+      f4_item<LAYOUT, 8, 2, 3, 2>(a, sh, unit, first, nrows, channels);
+    else if (nrows > 64)
+      f4_item<LAYOUT, 8, 2, 2, 2>(a, sh, unit, first, nrows, channels);
+    else
+      f4_item<LAYOUT, 8, 1, 2, 1>(a, sh, unit, first, nrows, channels);
+  } else {
+    if (nrows > 96)
+      f4_item<LAYOUT, 4, 2, 2, 2>(a, sh, unit, first, nrows, channels);
+    else if (nrows > 64)
+      f4_item<LAYOUT, 4, 1, 3, 1>(a, sh, unit, first, nrows, channels);
+    else if (nrows > 32)
+      f4_item<LAYOUT, 4, 1, 2, 1>(a, sh, unit, first, nrows, channels);
+    else
+      f4_item<LAYOUT, 4, 1, 1, 1>(a, sh, unit, first, nrows, channels);
+  }
+}
+
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void fp4_gemm_kernel(Fp4GemmArgs a) {
+  __shared__ F4Shared<WAVES> sh;
+  constexpr int kRows = F4Shared<WAVES>::kRows;
   int item, grp;
   if (!gemm_unit(a.n_items, a.groups, &item, &grp)) return;
   const int4 itd = reinterpret_cast<const int4*>(a.items)[item];
   const int e = itd.x, nrows = itd.z;
-  for (int m = threadIdx.x; m < GEMM_MT; m += F4_THREADS) {
+  for (int m = threadIdx.x; m < kRows; m += 64 * WAVES) {
     const int slot = m < nrows ? a.pairs[itd.y + m] : 0;
     sh.slot[m] = slot;
     sh.gate[m] = (m < nrows && a.gates) ? a.gates[slot] : 1.0f;
   }
   __syncthreads();
-  const int channels = min(128 * NB, a.out - grp * 128 * NB);
+  const int channels = min(kRows, a.out - grp * kRows);
   const uint8_t* unit = a.units + (size_t)e * MxUnit<MX_FP4>::unit_bytes(a.out, a.in);
-  auto run = [&](auto MBK) {
-    if (a.layout)
-      f4_item<1, decltype(MBK)::value, NB>(a, sh, unit, grp, nrows, channels);
-    else
-      f4_item<0, decltype(MBK)::value, NB>(a, sh, unit, grp, nrows, channels);
-  };
-  switch ((nrows + 31) >> 5) {
-    case 1: run(std::integral_constant<int, 1>{}); break;
-    case 2: run(std::integral_constant<int, 2>{}); break;
-    case 3: run(std::integral_constant<int, 3>{}); break;
-    default: run(std::integral_constant<int, 4>{}); break;
-  }
+  if (a.layout)
+    f4_rows<WAVES, 1>(a, sh, unit, grp * kRows, nrows, channels);
+  else
+    f4_rows<WAVES, 0>(a, sh, unit, grp * kRows, nrows, channels);
 }
 
 }  // namespace
 
+int fp4_item_rows(int64_t N, int E, int out) { return out > 128 && N >= 160 * (int64_t)E ? 256 : 128; }
+
 hipError_t launch_fp4_gemm(const Fp4GemmArgs& args, hipStream_t s) {
   Fp4GemmArgs a = args;
-  const bool wide = a.out > 128;
-  a.groups = (a.out + (wide ? 255 : 127)) / (wide ? 256 : 128);
+  a.groups = (a.out + a.item_rows - 1) / a.item_rows;
   const int blocks = gemm_grid(a.max_items, a.groups);
   if (blocks == 0) return hipSuccess;
-  if (wide) return launch_timed(fp4_gemm_kernel<2>, dim3(blocks), dim3(F4_THREADS), s, a);
-  return launch_timed(fp4_gemm_kernel<1>, dim3(blocks), dim3(F4_THREADS), s, a);
+  if (a.item_rows == 256) return launch_timed(fp4_gemm_kernel<8>, dim3(blocks), dim3(512), s, a);
+  return launch_timed(fp4_gemm_kernel<4>, dim3(blocks), dim3(256), s, a);
 }
 
 }  // namespace tq

@@ -259,7 +259,10 @@ struct Fp4GemmArgs {
   const int32_t* n_items;
   float* y;
   int E, out, in, topk, groups, max_items;
+  int item_rows;         // of the route: fp4_item_rows
 };
+// The rows of a work item, and the channels of its group: 128 or 256.
+int fp4_item_rows(int64_t N, int E, int out);
 hipError_t launch_fp4_gemm(const Fp4GemmArgs& a, hipStream_t s);
 
 // The router's choice and its gradient (FORMAT F27, F28; expert_route.hip).
