@@ -63,7 +63,8 @@ extern "C" {
 #define TQ_FP4 64u     /* MXFP4 only: the fp4 matrix cores. The activations are converted  */
                        /* to MXFP4 (E2M1, one E8M0 scale per 32 inputs, as                 */
                        /* mxfp4_quantize; FORMAT F29) and multiplied with the stored codes */
-                       /* (F30). Every mode, not with TQ_FP8                               */
+                       /* (F30). Not with TQ_FP8. TQ_GEMV takes at most 1,024 slots        */
+                       /* (T * topk) and 2^17 pairs of a slot and 128 channels             */
 
 /* ---- flag of the fp8b128 products --------------------------------------------------------- */
 #define TQ_OUT_BF16 32u /* y is bf16 instead of fp32                                           */

@@ -63,7 +63,9 @@ def test_sizes(E, T, topk, out, in_, repack):
     L = L.repacked() if repack else L
     y, a = reference(layer, x, ids, gates)
     xd, idd, gd = to_dev(x, np.int16), to_dev(ids), to_dev(gates)
-    for mode in (o.TQ_AUTO, o.TQ_GEMM):
+    for mode in (o.TQ_AUTO, o.TQ_GEMM, o.TQ_GEMV):
+        if mode == o.TQ_GEMV and T * topk > 1024:
+            continue
         for combine in (0, o.TQ_COMBINE):
             flags = o.TQ_FP4 | mode | combine
             guard = torch.full((T + 2,) + ((out,) if combine else (topk, out)), 7.0, device=dev())
@@ -78,7 +80,7 @@ def test_no_gates_bad_ids_and_no_experts():
     ids[5, 1], ids[6, 0] = 6, -2
     L = o.Mxfp4Layer.from_host(layer)
     y, a = reference(layer, x, ids, None)
-    for mode in (o.TQ_AUTO, o.TQ_GEMM):
+    for mode in (o.TQ_GEMV, o.TQ_GEMM):
         ws = o.workspace(40, 3, 6, 144, 512, o.TQ_FP4 | mode)
         got = o.mxfp4_expert_gemm(L, to_dev(x, np.int16), to_dev(ids), flags=o.TQ_FP4 | mode, ws=ws)
         compare(got, y, a, 512, 3, 0)
@@ -109,7 +111,7 @@ def test_special_activations_and_scales(T):
         x[3, 5] = 0x7FC0
         x[4, ::3] = 0x0001  # the smallest subnormal
     y, a = reference(layer, x, ids, gates)
-    for mode in (o.TQ_AUTO, o.TQ_GEMM):
+    for mode in (o.TQ_GEMV, o.TQ_GEMM):
         got = o.mxfp4_expert_gemm(L, to_dev(x, np.int16), to_dev(ids), to_dev(gates), flags=o.TQ_FP4 | mode)
         got = got.cpu().numpy().astype(np.float64)
         assert np.array_equal(np.isnan(got), np.isnan(y))
@@ -125,12 +127,12 @@ def test_a_nan_scale_of_the_weights_reaches_its_channel():
     units[1, 48 * 256 + 16 * 7 + 3] = 255
     L = o.Mxfp4Layer.from_host(layer)
     y, a = reference(layer, x, ids, gates)
-    for mode in (o.TQ_AUTO, o.TQ_GEMM):
+    for mode in (o.TQ_GEMV, o.TQ_GEMM):
         got = o.mxfp4_expert_gemm(L, to_dev(x, np.int16), to_dev(ids), to_dev(gates), flags=o.TQ_FP4 | mode)
         compare(got, y, a, 512, 1, 0)
 
 
-@pytest.mark.parametrize("T,mode", [(1, 0), (40, 0), (400, 0), (40, 2)])
+@pytest.mark.parametrize("T,mode", [(1, 0), (40, 1), (256, 1), (400, 0), (40, 2)])
 def test_the_same_bits_again_and_in_any_order_of_tokens(T, mode):
     o = ops()
     layer, x, ids, gates = case(934, 12, T, 4, 144, 1024)
@@ -146,7 +148,7 @@ def test_the_same_bits_again_and_in_any_order_of_tokens(T, mode):
     assert torch.equal(moved, first[order])
 
 
-@pytest.mark.parametrize("T,mode", [(1, 0), (24, 0), (300, 0)])
+@pytest.mark.parametrize("T,mode", [(1, 0), (24, 1), (24, 2), (300, 0)])
 def test_replayed_graph_with_changing_routes(T, mode):
     o = ops()
     E, topk, out, in_ = 10, 3, 272, 1024

@@ -120,6 +120,13 @@ def test_fp4_sizes(lib):
     assert experts(lib, T=0, x=None, y=None, ids=None, ws=None) == _lib.TQ_OK
 
 
+def test_fp4_decode_batches_are_small(lib):
+    assert experts(lib, T=513, topk=2, flags=FP4 | _lib.TQ_GEMV) == _lib.TQ_EINVAL
+    assert b"1024" in lib.tq_last_error()
+    assert lib.tq_workspace_bytes(512, 2, 4, 128, 1024, FP4 | _lib.TQ_GEMV) == 256
+    assert experts(lib, T=512, topk=2, flags=FP4 | _lib.TQ_GEMV, ws_bytes=255) == _lib.TQ_EWORKSPACE
+
+
 @pytest.mark.parametrize("mode", [0, _lib.TQ_GEMM])
 def test_fp4_workspace(lib, mode):
     for extra in (0, _lib.TQ_COMBINE):

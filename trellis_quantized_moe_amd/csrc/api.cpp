@@ -117,11 +117,18 @@ constexpr int64_t MAX_ELEMENTS = (int64_t)1 << 33;
 // otherwise the decode batch, whose waves take 8 or 16 slots each, spreads the work wider.
 constexpr int64_t GEMM_MIN_ITEMS = 256;
 
+// What one launch of the 4-bit decode takes: its slots, and its workgroups (one per slot and 16
+// channels, of which a group of 128 has 8 at most).
+bool fp4_decode_fits(int64_t N, int groups) {
+  return N <= tq::FP4_DECODE_SLOTS && N * groups * 8 <= (int64_t)1 << 20;
+}
+
 bool use_gemm(int64_t T, int topk, int E, int groups, uint32_t flags) {
   const uint32_t mode = flags & 3u;
   if (mode == TQ_GEMV) return false;
-  if (mode == TQ_GEMM || (flags & (TQ_FP8 | TQ_FP4))) return true;
+  if (mode == TQ_GEMM || (flags & TQ_FP8)) return true;
   const int64_t N = T * topk;
+  if (flags & TQ_FP4) return !fp4_decode_fits(N, groups) || N > 8LL * E;
   return N > 16LL * E && (int64_t)groups * ((N + 127) / 128) >= GEMM_MIN_ITEMS;
 }
 
@@ -186,10 +193,13 @@ WsLayout ws_layout(int64_t T, int topk, int E, int out, int in, uint32_t flags, 
   L.groups = (out + 127) / 128;
   L.gemm = use_gemm(T, topk, E, L.groups, flags);
   // a decode batch gives every active expert group and chunk at least one piece of its own
-  if ((flags & 3u) == TQ_AUTO && gemv_chunk_bound(N, E, L.groups, mxfp4) > tq::GEMV_MAX_G)
+  if ((flags & 3u) == TQ_AUTO && !(flags & TQ_FP4) &&
+      gemv_chunk_bound(N, E, L.groups, mxfp4) > tq::GEMV_MAX_G)
     L.gemm = true;
   size_t off = 256;  // status word
-  if (!L.gemm) {
+  if (!L.gemm && (flags & TQ_FP4)) {
+    // one launch, which needs nothing but the status word (and slots for the combine)
+  } else if (!L.gemm) {
     // planned decode batch: plan records, prepared activations (trellis), per-piece partial
     // sums (at most in / 256 pieces per slot for trellis steps of 64 inputs, in / 512 for
     // MXFP4 steps of 128)
@@ -256,7 +266,7 @@ WsLayout ws_layout(int64_t T, int topk, int E, int out, int in, uint32_t flags, 
       off += round_up((size_t)T * in / 32, 256);
     }
   }
-  if ((flags & TQ_COMBINE) && L.gemm) {
+  if ((flags & TQ_COMBINE) && (L.gemm || (flags & TQ_FP4))) {
     L.slots = off;
     L.slots_bytes = round_up((size_t)N * out * 4, 256);
     off += L.slots_bytes;
@@ -627,7 +637,8 @@ static int common_checks(int E, int out, int in, const void* x, int64_t T, const
   *layout = tq::ws_layout(T, topk, E, out, in, flags, mxfp4);
   if ((layout->gemm || !mxfp4) && E > 4096)
     return fail(TQ_EINVAL, "this path supports E <= 4096 (E = %d)", E);
-  if (!layout->gemm && tq::gemv_chunk_bound(T * topk, E, layout->groups, mxfp4) > tq::GEMV_MAX_G)
+  if (!layout->gemm && !(flags & TQ_FP4) &&
+      tq::gemv_chunk_bound(T * topk, E, layout->groups, mxfp4) > tq::GEMV_MAX_G)
     return fail(TQ_EINVAL,
                 "decode batches take at most %d (group, chunk) pairs: (E + T*topk/%d) * out/128",
                 tq::GEMV_MAX_G, tq::gemv_rows(mxfp4));
@@ -879,8 +890,10 @@ int mx_expert_gemm(const MxLayer* L, const void* x, int64_t T, const int32_t* to
     return fail(TQ_EINVAL, "TQ_FP4 applies to MXFP4 layers only");
   if ((flags & TQ_FP4) && (flags & TQ_FP8))
     return fail(TQ_EINVAL, "TQ_FP4 and TQ_FP8 exclude each other");
-  if ((flags & TQ_FP4) && (flags & 3u) == TQ_GEMV)
-    return fail(TQ_EINVAL, "TQ_FP4 runs in the prefill mode only (not with TQ_GEMV)");
+  if ((flags & TQ_FP4) && (flags & 3u) == TQ_GEMV && !fp4_decode_fits(T * topk, (L->out + 127) / 128))
+    return fail(TQ_EINVAL,
+                "decode batches with TQ_FP4 take at most %d slots (T * topk = %lld) and 2^20 / 8 "
+                "(slot, 128 channels) pairs", tq::FP4_DECODE_SLOTS, (long long)(T * topk));
   if ((flags & TQ_FP4) && T * (int64_t)L->in >= ((int64_t)1 << 32))
     return fail(TQ_EINVAL, "the MXFP4 activations (T * in / 2 bytes) must stay below 2^31");
   const int64_t unit = mx_unit_bytes(L->fmt, L->out, L->in);
@@ -895,7 +908,26 @@ int mx_expert_gemm(const MxLayer* L, const void* x, int64_t T, const int32_t* to
   float* y_slots = (flags & TQ_COMBINE) ? at<float>(ws, W.slots) : y;
   const uint16_t* xb = static_cast<const uint16_t*>(x);
   hipError_t err;
-  if (!W.gemm) {
+  if (!W.gemm && (flags & TQ_FP4)) {
+    tq::Fp4DecodeArgs a{};
+    a.layout = L->layout;
+    a.units = L->units;
+    a.x = xb;
+    a.ids = topk_ids;
+    a.gates = topk_w;
+    a.y = y_slots;
+    a.status = at<uint32_t>(ws, W.status);
+    a.N = (int)N;
+    a.E = L->E;
+    a.out = L->out;
+    a.in = L->in;
+    a.topk = topk;
+    err = time_begin(s);
+    if (err != hipSuccess) return hip_fail(err, "hipEventRecord");
+    err = tq::launch_fp4_decode(a, s);
+    if (err == hipSuccess) err = time_end(s);
+    if (err != hipSuccess) return hip_fail(err, "FP4 decode launch");
+  } else if (!W.gemm) {
     const int G = tq::mxfp4_gemv_grid(L->fmt);
     if (G <= 0) return fail(TQ_EHIP, "could not size the GEMV grid");
     const int Gl = (int)std::max<int64_t>(G, tq::gemv_chunk_bound(N, L->E, W.groups, true));

@@ -265,6 +265,20 @@ struct Fp4GemmArgs {
 int fp4_item_rows(int64_t N, int E, int out);
 hipError_t launch_fp4_gemm(const Fp4GemmArgs& a, hipStream_t s);
 
+// Its decode batches in one launch, of at most FP4_DECODE_SLOTS routed slots (mxfp4_fp4_decode.hip).
+constexpr int FP4_DECODE_SLOTS = 1024;
+struct Fp4DecodeArgs {
+  int layout;
+  const uint8_t* units;
+  const uint16_t* x;     // bf16 [T][in]
+  const int32_t* ids;    // [N]
+  const float* gates;    // [N] or null
+  float* y;              // [N][out]
+  uint32_t* status;
+  int N, E, out, in, topk, groups;
+};
+hipError_t launch_fp4_decode(const Fp4DecodeArgs& a, hipStream_t s);
+
 // The router's choice and its gradient (FORMAT F27, F28; expert_route.hip).
 struct RouterArgs {
   const void* logits;     // fp32 or bf16 [T][E]
