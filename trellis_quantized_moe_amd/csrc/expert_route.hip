@@ -3,16 +3,22 @@
 // expert_route: one wave per token. Expert e = 64 j + lane is value j of its lane, so a row is
 // read by contiguous loads and the lowest index of equal keys is the lowest j, then the lowest
 // lane. The wave
-//   1. finds the row's largest logit (a row without experts ends here; a NaN, or +inf under
-//      softmax, makes it a row of NaN weights);
+//   1. looks for a NaN, or +inf under softmax, which makes a row of NaN weights;
 //   2. makes the keys of the choice: the logits themselves where no bias enters (a score grows
-//      with its logit), else score + bias in 64 bits, because keys that differ by less than
-//      fp32 shows decide which expert is chosen;
+//      with its logit), else score + bias in fp32, each off by less than KEY_ERROR;
 //   3. keeps the best groups: each group's lanes take its one or two best keys, a group's rank
 //      is the number of groups before it;
-//   4. takes the largest key topk times; lane r keeps the r-th expert;
-//   5. weighs: lane r computes its score from its logit in fp32, relative to the largest
+//   4. takes the largest key topk times, and further ones within the errors of the last of those;
+//      lane r keeps the r-th expert;
+//   5. checks that fp32 has decided: no further ones, and neighbours in the order either differ by
+//      more than their errors or have the same logit and bias. If not (a row in a hundred), each
+//      lane computes its expert's key in 64 bits, where the definition lies, and the lanes change
+//      places. Where the last group kept is not ahead of the next by more than the errors, or more
+//      than 64 experts are candidates, steps 2 to 4 run once more in 64 bits throughout. (All rows
+//      in 64 bits took 29 us for 8,192 rows of 384, one wave alone 8.5.);
+//   6. weighs: lane r computes its score from its logit in fp32, relative to the largest
 //      chosen one where they are renormalised, so that no sum of scores can underflow.
+// One row a wave: a chunk's rows fill the GPU eight times over, and a single row ends soonest.
 //
 // expert_route_backward: one wave per token; lane r holds slot r. Where the weights are
 // renormalised, and under sigmoid, only chosen logits have a gradient: the row is zeros in LDS
@@ -44,26 +50,57 @@ __device__ __forceinline__ void store_grad(uint16_t* p, int64_t i, float v) {
   p[i] = (uint16_t)f32_to_bf16_rne(v);
 }
 
-template <typename K>
-__device__ __forceinline__ K wave_max(K v) {
+// Value of another lane by DPP; lanes without a source (or outside the row mask) keep `old`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float lane63(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+// Largest value (no NaN) and sum over the wave: row shifts 1, 2, 4, 8, then row broadcasts 15 and 31.
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<0x111, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x112, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x114, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x118, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x142, 0xA>(v, v));
+  v = fmaxf(v, dpp<0x143, 0xC>(v, v));
+  return lane63(v);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0x111, 0xF>(0.0f, v);
+  v += dpp<0x112, 0xF>(0.0f, v);
+  v += dpp<0x114, 0xF>(0.0f, v);
+  v += dpp<0x118, 0xF>(0.0f, v);
+  v += dpp<0x142, 0xA>(0.0f, v);
+  v += dpp<0x143, 0xC>(0.0f, v);
+  return lane63(v);
+}
+__device__ __forceinline__ double wave_max(double v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
-    const K o = __shfl_xor(v, d, 64);
+    const double o = __shfl_xor(v, d, 64);
     v = o > v ? o : v;
   }
   return v;
 }
-template <typename K>
-__device__ __forceinline__ K wave_sum(K v) {
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
   return v;
 }
 
-// The score of a logit that is not NaN, and not +inf under softmax.
-__device__ __forceinline__ double score64(float x, bool sigmoid, float top, double z) {
-  return sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / z;
-}
+// e^x by the hardware's 2^x: off by 2^-22 of it and by 2^-23 |x| of it (the argument's rounding); 0
+// where it is below 2^-126.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// How far a score in fp32 is off: the exponential's error, at most 2^-22 of a score and 2^-24 in
+// all from its argument (|x| e^-|x| stays below 0.37), a sum's 2^-21, the reciprocal's 2^-23; a
+// score is at most 1. The sum with a bias rounds by 2^-24 of itself. Two keys are told apart where
+// they differ by more than twice that (with a factor of two to spare).
+constexpr float KEY_ERROR = 0x1p-20f;
+__device__ __forceinline__ float key_gap(float v) { return 4.0f * KEY_ERROR + 0x1p-22f * fabsf(v); }
 
 // The best two of a set of keys, -inf where there are none.
 template <typename K>
@@ -75,46 +112,109 @@ struct Best2 {
   }
 };
 
-// topk times the largest key of the row: lane r gets the r-th choice (its index, or -1).
-template <typename K, int PER>
-__device__ __forceinline__ int choose(K key[PER], int topk) {
+// What a lane knows after the choice: the expert that came up in its turn (or -1) and that one's
+// key; all lanes: how many came up, and whether more would have to (they do not fit a wave).
+struct Choice {
+  int e;
+  float key;
+  int count;
+  bool more;
+};
+
+// fp32 values as integers of the same order (both zeros are one value), and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max_dpp<0x111, 0xF>(v);
+  v = max_dpp<0x112, 0xF>(v);
+  v = max_dpp<0x114, 0xF>(v);
+  v = max_dpp<0x118, 0xF>(v);
+  v = max_dpp<0x142, 0xA>(v);
+  v = max_dpp<0x143, 0xC>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// topk times the largest key of the row: lane r gets the r-th. With `near`, further ones as long as
+// they are within the errors of the last of those. A turn is a handful of instructions: each lane has
+// its best two at hand, and one that gives both away (2 % of rows at 8 of 384) looks through its keys
+// again for those behind the last one it gave.
+template <int PER>
+__device__ __forceinline__ Choice choose(const float (&value)[PER], int topk, bool near) {
   const int lane = threadIdx.x & 63;
-  const K none = (K)NEG;
-  int mine = -1;
-  K best = none;
-  int bj = 0;
-  auto refresh = [&]() {
-    best = none;
+  const uint32_t none = ordered(NEG);
+  uint32_t key[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        bj = j;
-      }
-  };
-  refresh();
-  for (int r = 0; r < topk; ++r) {
-    const K top = wave_max(best);
-    if (!(top > none)) break;  // uniform
-    const int e = best == top ? 64 * bj + lane : 0x7FFFFFFF;
-    int first = e;
+  for (int j = 0; j < PER; ++j) key[j] = ordered(value[j]);
+  uint32_t best = none, second = none;
+  int bj = 0, sj = 0;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) first = min(first, __shfl_xor(first, d, 64));
-    if (lane == r) mine = first;
-    if (e == first) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if (j == bj) key[j] = none;
-      refresh();
-    }
+  for (int j = 0; j < PER; ++j) {
+    const bool first = key[j] > best, next = key[j] > second;
+    sj = first ? bj : next ? j : sj;
+    second = first ? best : next ? key[j] : second;
+    bj = first ? j : bj;
+    best = first ? key[j] : best;
   }
-  return mine;
+  uint32_t limit = none, mine = none;  // keys up to the limit are not chosen
+  int e = -1, count = 0;
+  bool more = false;
+  uint64_t gave = 0;  // lanes whose second is gone
+  for (int r = 0; r < topk || near; ++r) {
+    const uint32_t top = wave_max(best);
+    if (!(top > limit)) break;  // uniform
+    if (r == 64) {
+      more = true;
+      break;
+    }
+    count = r + 1;
+    if (r == topk - 1 && near) {
+      const float v = unordered(top);
+      limit = ordered(v - key_gap(v));
+    }
+    const uint64_t m = __ballot(best == top);
+    int winner = __builtin_ctzll(m);
+    if (m & (m - 1)) {  // several lanes hold it: the lowest index
+      int first = best == top ? 64 * bj + lane : 0x7FFFFFFF;
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) first = min(first, __shfl_xor(first, d, 64));
+      winner = __builtin_amdgcn_readfirstlane(first) & 63;
+    }
+    const int j = __builtin_amdgcn_readlane(bj, winner);
+    const bool turn = lane == r;
+    e = turn ? 64 * j + winner : e;
+    mine = turn ? top : mine;
+    const bool won = lane == winner;
+    best = won ? second : best;
+    bj = won ? sj : bj;
+    if ((gave >> winner) & 1) {  // uniform
+      uint32_t b = none;
+      int k = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if ((key[i] < top || (key[i] == top && i > j)) && key[i] > b) {
+          b = key[i];
+          k = i;
+        }
+      best = won ? b : best;
+      bj = won ? k : bj;
+    }
+    gave |= 1ull << winner;
+  }
+  return Choice{e, unordered(mine), count, more};
 }
 
-// Closes the experts outside the group_topk best groups. keys: this wave's LDS, E entries
-// holding the row's keys of the group scores.
-template <typename K, int PER>
-__device__ __forceinline__ void keep_groups(const RouterArgs& a, const K* keys, uint64_t& kept) {
+// The groups that stay, as bits. keys: this wave's LDS, E entries holding the row's keys of the
+// group scores. gap: how far the last group kept is ahead of the next (+inf if none is dropped).
+template <typename K>
+__device__ __forceinline__ uint64_t keep_groups(const RouterArgs& a, const K* keys, K& gap) {
   const int lane = threadIdx.x & 63;
   const int size = a.E / a.groups;
   int per = 64;  // lanes per group: the largest power of two with groups * per <= 64
@@ -136,104 +236,241 @@ __device__ __forceinline__ void keep_groups(const RouterArgs& a, const K* keys, 
     const K o = __shfl(score, h * per, 64);
     rank += o > score || (o == score && h < g);
   }
-  const uint64_t m = __ballot(g < a.groups && sub == 0 && rank < a.group_topk);
-  // bit g of kept: lane g * per of m
-  kept = 0;
+  const bool leads = g < a.groups && sub == 0;
+  gap = -none;
+  if (a.group_topk < a.groups) {
+    const int last = __builtin_ctzll(__ballot(leads && rank == a.group_topk - 1));
+    const int next = __builtin_ctzll(__ballot(leads && rank == a.group_topk));
+    const K dropped = __shfl(score, next, 64);
+    if (dropped > none) gap = __shfl(score, last, 64) - dropped;
+  }
+  const uint64_t m = __ballot(leads && rank < a.group_topk);
+  uint64_t kept = 0;  // bit g: lane g * per of m
   for (int h = 0; h < a.groups; ++h) kept |= ((m >> (h * per)) & 1ull) << h;
+  return kept;
 }
 
 template <typename L, int PER>
+__device__ __forceinline__ void load_row(const RouterArgs& a, const L* row, float (&x)[PER]) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = 64 * j + (threadIdx.x & 63);
+    x[j] = e < a.E ? load_logit(row, e) : NEG;
+  }
+}
+
+// The sum of the softmax in 64 bits. (What hardly any row needs is in loops: its code and registers
+// would cost every row.)
+template <typename L>
+__device__ __forceinline__ double sum64(const RouterArgs& a, const L* row, float top) {
+  double s = 0.0;
+#pragma unroll 1
+  for (int e = threadIdx.x & 63; e < a.E; e += 64) s += exp((double)load_logit(row, e) - (double)top);
+  return wave_sum(s);
+}
+
+// The key in 64 bits of an expert that is open, given the reciprocal of the sum.
+template <bool SIGMOID>
+__device__ __forceinline__ double key64(const RouterArgs& a, float x, int e, float top, double rz) {
+  const double s = SIGMOID ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) * rz;
+  return a.bias ? s + (double)a.bias[e] : s;
+}
+
+// The choice in 64 bits throughout. keys: this wave's LDS, E entries.
+template <typename L, bool SIGMOID>
+__device__ __forceinline__ int choose64(const RouterArgs& a, const L* row, float top, double* keys) {
+  const int lane = threadIdx.x & 63;
+  const double rz = SIGMOID ? 1.0 : 1.0 / sum64(a, row, top);
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) {
+    const float x = load_logit(row, e);
+    keys[e] = x > NEG ? key64<SIGMOID>(a, x, e, top, rz) : (double)NEG;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  uint64_t kept = ~0ull;
+  const int size = a.E / a.groups;
+  if (a.groups > 1) {
+    double gap;
+    kept = keep_groups<double>(a, keys, gap);
+  }
+  double last = -(double)NEG;  // the last key taken, and its expert
+  int last_e = -1, mine = -1;
+#pragma unroll 1
+  for (int r = 0; r < a.topk; ++r) {
+    double best = NEG;
+    int be = 0x7FFFFFFF;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      if (a.groups > 1 && !((kept >> (e / size)) & 1)) continue;
+      double k = keys[e];
+      if (!a.bias && k > NEG) k = load_logit(row, e);
+      if (k > best && (k < last || (k == last && e > last_e))) {
+        best = k;
+        be = e;
+      }
+    }
+    last = wave_max(best);
+    if (!(last > NEG)) break;  // uniform
+    last_e = best == last ? be : 0x7FFFFFFF;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) last_e = min(last_e, __shfl_xor(last_e, d, 64));
+    mine = lane == r ? last_e : mine;
+  }
+  __builtin_amdgcn_wave_barrier();
+  return mine;
+}
+
+// The candidates of a choice in the order of their keys in 64 bits, equal ones by the lowest index:
+// lane r gets the r-th.
+template <typename L, bool SIGMOID>
+__device__ __forceinline__ int in_order(const RouterArgs& a, const L* row, float top, int e, int count) {
+  const int lane = threadIdx.x & 63;
+  const double rz = SIGMOID ? 1.0 : 1.0 / sum64(a, row, top);
+  const double key = e >= 0 ? key64<SIGMOID>(a, load_logit(row, e), e, top, rz) : (double)NEG;
+  int rank = lane < count ? 0 : lane;  // the others keep their places
+#pragma unroll 1
+  for (int o = 0; o < count; ++o) {
+    const double k = __shfl(key, o, 64);
+    const int i = __shfl(e, o, 64);
+    rank += lane < count && (k > key || (k == key && i < e));
+  }
+  return __builtin_amdgcn_ds_permute(4 * rank, e);
+}
+
+// Steps 2 to 4 in fp32. nan: a key is NaN (the choice is then without meaning). sure: the groups that
+// stay are those of the exact keys.
+template <int PER, bool SIGMOID, bool SCORED>
+__device__ __forceinline__ Choice pick(const RouterArgs& a, const float (&x)[PER], float top, float* keys,
+                                       bool near, bool& nan, bool& sure) {
+  const int lane = threadIdx.x & 63;
+  float key[PER];
+  if constexpr (SCORED) {
+    float rz = 1.0f;
+    if constexpr (!SIGMOID) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) s += fast_exp(x[j] - top);
+      rz = 1.0f / wave_sum(s);
+    }
+    float bias[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) bias[j] = 0.0f;
+    if (a.bias) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (64 * j + lane < a.E) bias[j] = a.bias[64 * j + lane];
+    }
+    bool none = false;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const float v = (SIGMOID ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[j])) : fast_exp(x[j] - top) * rz) + bias[j];
+      key[j] = x[j] > NEG ? v : NEG;
+      none |= !(key[j] == key[j]);
+    }
+    nan = __ballot(none) != 0;
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) key[j] = x[j];
+    nan = false;
+  }
+  sure = true;
+  if (a.groups > 1 && !nan) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (64 * j + lane < a.E) keys[64 * j + lane] = key[j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    float gap;
+    const uint64_t kept = keep_groups<float>(a, keys, gap);
+    const float inverse = 1.0f / (float)(a.E / a.groups);
+    float most = 0.0f;  // the largest magnitude of a key, which bounds the errors of the groups' scores
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (SCORED && x[j] > NEG) most = fmaxf(most, fabsf(key[j]));
+      if (SCORED && !a.bias) key[j] = x[j];
+      // the group of e: e and the size are at most 2^12, so that (e + 1/2) / size falls on the right
+      // side of every whole number
+      const uint32_t g = (uint32_t)(((float)(64 * j + lane) + 0.5f) * inverse);
+      if (!((kept >> (g & 63)) & 1) || 64 * j + lane >= a.E) key[j] = NEG;
+    }
+    if (SCORED && a.group_topk < a.groups) sure = gap > 3.0f * key_gap(wave_max(most));
+    __builtin_amdgcn_wave_barrier();
+  }
+  return choose<PER>(key, a.topk, near);
+}
+
+// SCORED: scores enter the choice (a bias, or groups by two scores); else it goes by the logits.
+template <typename L, int PER, bool SIGMOID, bool SCORED>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_kernel(RouterArgs a) {
-  extern __shared__ double group_keys[];  // [waves of the workgroup][E], grouped routers only
+  extern __shared__ double row_keys[];  // [waves of the workgroup][E], with groups or scores only
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const bool sigmoid = a.sigmoid;
   const L* logits = static_cast<const L*>(a.logits);
   for (int64_t t = (int64_t)blockIdx.x * waves + w; t < a.T; t += (int64_t)gridDim.x * waves) {
     const L* row = logits + t * a.E;
     float x[PER];
+    load_row(a, row, x);
+    bool odd = false;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = 64 * j + lane;
-      x[j] = e < a.E ? load_logit(row, e) : NEG;
-    }
-    float top = NEG;
-    bool nan = false;
+    for (int j = 0; j < PER; ++j) odd |= !(x[j] == x[j]) || (!SIGMOID && x[j] == -NEG);
+    bool bad = __ballot(odd) != 0;
+    float top = 0.0f;  // the softmax's largest logit; 0 in a row without experts
+    if (!SIGMOID && (SCORED || !a.renorm)) {
+      top = x[0];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      nan |= !(x[j] == x[j]) || (!sigmoid && x[j] == -NEG);
-      top = fmaxf(top, x[j]);
+      for (int j = 1; j < PER; ++j) top = fmaxf(top, x[j]);
+      top = wave_max(top);
+      top = top > NEG ? top : 0.0f;
     }
-    top = wave_max(top);
-    const bool by_logit = !a.bias;
-    const bool scored = !by_logit || (a.groups > 1 && a.group_top == 2);
-    double z = 1.0;
-    double key[PER];
     int mine = -1;
-    bool bad = __ballot(nan) != 0;
-    if (!bad && top > NEG) {
-      if (!sigmoid && scored) {
-        double s = 0.0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) s += exp((double)x[j] - (double)top);
-        z = wave_sum(s);
-      }
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int e = 64 * j + lane;
-        key[j] = NEG;
-        if (x[j] > NEG) {
-          key[j] = scored ? score64(x[j], sigmoid, top, z) : (double)x[j];
-          if (a.bias) key[j] += (double)a.bias[e];
+    if (!bad) {
+      double* keys = row_keys + (size_t)w * a.E;
+      const bool near = SCORED && a.bias;
+      bool sure;
+      const Choice c = pick<PER, SIGMOID, SCORED>(a, x, top, reinterpret_cast<float*>(keys), near, bad, sure);
+      mine = c.e;
+      if constexpr (SCORED) {
+        bool again = false;
+        if (near) {
+          // lane r's key against the next one's
+          const float below = __shfl_down(c.key, 1, 64);
+          const float xe = mine >= 0 ? load_logit(row, mine) : 0.0f, be = mine >= 0 ? a.bias[mine] : 0.0f;
+          const float xn = __shfl_down(xe, 1, 64), bn = __shfl_down(be, 1, 64);
+          const bool apart = lane + 1 >= c.count || c.key - below > key_gap(c.key) || (xe == xn && be == bn);
+          again = c.count > a.topk || __ballot(!apart) != 0;
         }
-        nan |= !(key[j] == key[j]);
-      }
-      bad = __ballot(nan) != 0;
-      if (!bad) {
-        if (a.groups > 1) {
-          double* keys = group_keys + (size_t)w * a.E;
-#pragma unroll
-          for (int j = 0; j < PER; ++j)
-            if (64 * j + lane < a.E) keys[64 * j + lane] = key[j];
-          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-          __builtin_amdgcn_wave_barrier();
-          uint64_t kept;
-          keep_groups<double, PER>(a, keys, kept);
-          const int size = a.E / a.groups;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const int g = (64 * j + lane) / size;
-            if (by_logit) key[j] = (double)x[j];
-            if (g >= a.groups || !((kept >> g) & 1)) key[j] = NEG;
-          }
-          __builtin_amdgcn_wave_barrier();
+        if (!bad) {
+          if (!sure || c.more)
+            mine = choose64<L, SIGMOID>(a, row, top, keys);
+          else if (again)
+            mine = in_order<L, SIGMOID>(a, row, top, mine, c.count);
         }
-        mine = choose<double, PER>(key, a.topk);
+        mine = lane < a.topk ? mine : -1;
       }
     }
     // the weights, slot r in lane r
-    float weight = 0.0f;
+    float weight = 0.0f, sum = 1.0f;
     const float xs = mine >= 0 ? load_logit(row, mine) : NEG;
-    const float most = wave_max(xs);
-    if (sigmoid) {
+    if (a.renorm) top = wave_max(xs);
+    if constexpr (SIGMOID) {
       // e^min(x, 0) / (1 + e^-|x|), the numerator relative to the largest chosen one
-      const float ref = a.renorm && most > NEG ? fminf(most, 0.0f) : 0.0f;
+      const float ref = a.renorm && top > NEG ? fminf(top, 0.0f) : 0.0f;
       if (mine >= 0) weight = expf(fminf(xs, 0.0f) - ref) / (1.0f + expf(-fabsf(xs)));
     } else if (mine >= 0) {
-      weight = expf(xs - (a.renorm ? most : top));
+      weight = expf(xs - top);
     }
-    float sum = 1.0f;
     if (a.renorm) {
       sum = wave_sum(weight);
-    } else if (!sigmoid) {
-      float s = 0.0f;
+    } else if constexpr (!SIGMOID) {
+      sum = 0.0f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) s += top > NEG ? expf(x[j] - top) : 0.0f;
-      sum = wave_sum(s);
+      for (int j = 0; j < PER; ++j) sum += fast_exp(x[j] - top);
+      sum = wave_sum(sum);
     }
-    weight = mine >= 0 ? a.scale * (weight / sum) : 0.0f;
     if (lane < a.topk) {
+      weight = mine >= 0 ? a.scale * (weight / sum) : 0.0f;
       a.ids[t * a.topk + lane] = bad ? lane : mine;
       a.w[t * a.topk + lane] = bad ? __builtin_nanf("") : weight;
     }
@@ -258,9 +495,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
     const float dw = id >= 0 ? a.dw[t * a.topk + lane] : 0.0f;
     const float xs = id >= 0 ? load_logit(row, id) : NEG;
     const float most = wave_max(xs);
-    float top = most, z = 1.0f;
+    float top = most, rz = 1.0f;
     const bool dense = !sigmoid && !a.renorm;
-    float x[PER];
+    float x[PER];  // logits, then their exponentials
     if (dense) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
@@ -271,8 +508,11 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
       top = wave_max(top);
       float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) s += top > NEG ? expf(x[j] - top) : 0.0f;
-      z = wave_sum(s);
+      for (int j = 0; j < PER; ++j) {
+        x[j] = top > NEG ? fast_exp(x[j] - top) : 0.0f;
+        s += x[j];
+      }
+      rz = 1.0f / wave_sum(s);
     }
     // g: the gradient of the slot's score times the score, or (dense) the gradient alone
     float g = 0.0f, c = 0.0f;
@@ -296,7 +536,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
       g = id >= 0 ? a.scale * r * (dw - mean) : 0.0f;
     } else {
       g = a.scale * dw;
-      c = wave_sum(id >= 0 ? expf(xs - top) / z * g : 0.0f);
+      c = wave_sum(id >= 0 ? expf(xs - top) * rz * g : 0.0f);
     }
     // slots of the same expert add up, in slot order
     float total = 0.0f;
@@ -316,7 +556,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
       const int e = 64 * j + lane;
       if (e < a.E) {
         float v = grad[e];
-        if (dense) v = top > NEG ? expf(x[j] - top) / z * (v - c) : 0.0f;
+        if (dense) v = top > NEG ? x[j] * rz * (v - c) : 0.0f;
         store_grad(dst, t * a.E + e, bad ? __builtin_nanf("") : v);
       }
     }
@@ -335,15 +575,21 @@ int route_waves(size_t bytes) {
 
 template <typename L, int PER>
 hipError_t start(const RouterArgs& a, bool backward, hipStream_t s) {
-  const size_t row = backward ? sizeof(float) * a.E : a.groups > 1 ? sizeof(double) * a.E : 0;
+  const bool scored = a.bias || (a.groups > 1 && a.group_top == 2);
+  const size_t row = backward ? sizeof(float) * a.E : a.groups > 1 || scored ? sizeof(double) * a.E : 0;
   const int waves = route_waves(row);
-  const int64_t blocks = std::min<int64_t>((a.T + waves - 1) / waves, ROUTE_MAX_BLOCKS);
+  const dim3 grid((unsigned)std::min<int64_t>((a.T + waves - 1) / waves, ROUTE_MAX_BLOCKS));
+  const dim3 block(64 * waves);
   if (backward)
-    hipLaunchKernelGGL((expert_route_backward_kernel<L, PER>), dim3((unsigned)blocks),
-                       dim3(64 * waves), row * waves, s, a);
+    hipLaunchKernelGGL((expert_route_backward_kernel<L, PER>), grid, block, row * waves, s, a);
+  else if (a.sigmoid && scored)
+    hipLaunchKernelGGL((expert_route_kernel<L, PER, true, true>), grid, block, row * waves, s, a);
+  else if (a.sigmoid)
+    hipLaunchKernelGGL((expert_route_kernel<L, PER, true, false>), grid, block, row * waves, s, a);
+  else if (scored)
+    hipLaunchKernelGGL((expert_route_kernel<L, PER, false, true>), grid, block, row * waves, s, a);
   else
-    hipLaunchKernelGGL((expert_route_kernel<L, PER>), dim3((unsigned)blocks), dim3(64 * waves),
-                       row * waves, s, a);
+    hipLaunchKernelGGL((expert_route_kernel<L, PER, false, false>), grid, block, row * waves, s, a);
   return hipGetLastError();
 }
 
