@@ -661,8 +661,8 @@ static int rotate_outputs(const tq_trellis_layer* L, float* y, int64_t rows, hip
   return ok();
 }
 
-static int run_route(const tq::WsLayout& L, void* ws, const int32_t* ids, int64_t N, int E, int out,
-              float* y_slots, hipStream_t s, int item_rows = tq::GEMM_MT) {
+static tq::RouteArgs route_args(const tq::WsLayout& L, void* ws, const int32_t* ids, int64_t N,
+                                int E, int out, float* y_slots) {
   tq::RouteArgs r{};
   r.ids = ids;
   r.N = N;
@@ -678,14 +678,18 @@ static int run_route(const tq::WsLayout& L, void* ws, const int32_t* ids, int64_
   r.y_special = y_slots;
   r.status = at<uint32_t>(ws, L.status);
   r.blocks = L.route_blocks;
-  r.item_rows = item_rows;
+  r.item_rows = tq::GEMM_MT;
   r.max_items = L.max_items;
   r.split_rows = L.split_rows;
-  hipError_t err = tq::launch_route(r, s);
+  return r;
+}
+
+static int run_route(const tq::WsLayout& L, void* ws, const int32_t* ids, int64_t N, int E, int out,
+              float* y_slots, hipStream_t s) {
+  hipError_t err = tq::launch_route(route_args(L, ws, ids, N, E, out, y_slots), s);
   if (err != hipSuccess) return hip_fail(err, "route launch");
   return TQ_OK;
 }
-
 
 }  // namespace
 
@@ -1021,13 +1025,16 @@ int mx_expert_gemm(const MxLayer* L, const void* x, int64_t T, const int32_t* to
     if (err == hipSuccess) err = time_end(s);
     if (err != hipSuccess) return hip_fail(err, "FP8 GEMM launch");
   } else if (flags & TQ_FP4) {
-    err = tq::launch_mxfp4_quantize(xb, T, L->in, at<uint8_t>(ws, W.xa), at<uint8_t>(ws, W.xs), s);
-    if (err != hipSuccess) return hip_fail(err, "MXFP4 activation launch");
-    const int item_rows = tq::fp4_item_rows(N, L->E, L->out);
-    rc = run_route(W, ws, topk_ids, N, L->E, L->out, y_slots, s, item_rows);
-    if (rc) return rc;
+    tq::RouteArgs r = route_args(W, ws, topk_ids, N, L->E, L->out, y_slots);
+    r.item_rows = tq::fp4_item_rows(N, L->E, L->out);
+    r.qx = xb;
+    r.qblocks = T * (L->in / 32);
+    r.qcodes = at<uint8_t>(ws, W.xa);
+    r.qscales = at<uint8_t>(ws, W.xs);
+    err = N <= tq::ROUTE_SMALL_SLOTS ? tq::launch_route_small(r, s) : tq::launch_route(r, s);
+    if (err != hipSuccess) return hip_fail(err, "route and MXFP4 activation launch");
     tq::Fp4GemmArgs a{};
-    a.item_rows = item_rows;
+    a.item_rows = r.item_rows;
     a.layout = L->layout;
     a.units = L->units;
     a.xa = at<uint8_t>(ws, W.xa);

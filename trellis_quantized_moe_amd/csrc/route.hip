@@ -22,6 +22,12 @@
 // fill the segments up to an equal share. The items are the same either way (each expert's
 // slots in runs of item_rows); without a split the list is in expert order. Which item
 // computes a slot changes nothing in its result.
+//
+// The 4-bit product converts its activations beside the routing: in further blocks of the scan's
+// launch, which is one block, or of the one launch that routes few slots.
+#include <algorithm>
+
+#include "mxfp4_quant.h"
 #include "tq_device.h"
 #include "tq_internal.h"
 
@@ -318,7 +324,26 @@ __device__ __forceinline__ void hist_bases(__amdgpu_buffer_rsrc_t rh, int E, int
   }
 }
 
+// Blocks 1 .. gridDim.x - 1 of 1,024 threads: the rows in MXFP4 (FORMAT F29), a block of 32 inputs
+// per thread.
+__device__ __forceinline__ void quantize_beside(const RouteArgs& a) {
+  const u32x4* x = reinterpret_cast<const u32x4*>(a.qx);
+  for (int64_t i = (int64_t)(blockIdx.x - 1) * 1024 + threadIdx.x; i < a.qblocks;
+       i += (int64_t)(gridDim.x - 1) * 1024) {
+    u32x4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = x[4 * i + q];
+    const Fp4Block r = fp4_block(v);
+    reinterpret_cast<u32x4*>(a.qcodes)[i] = r.codes;
+    a.qscales[i] = (uint8_t)r.scale;
+  }
+}
+
 __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
+  if (blockIdx.x > 0) {
+    quantize_beside(a);
+    return;
+  }
   __shared__ int wave_sums[16];
   __shared__ int total;
   __shared__ int carry[2];
@@ -373,6 +398,10 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
 // The same with the items placed by token range (a.items set, a.split_rows > 0, a.E <=
 // 1024: one expert per thread).
 __global__ __launch_bounds__(1024) void route_scan_split_kernel(RouteArgs a) {
+  if (blockIdx.x > 0) {
+    quantize_beside(a);
+    return;
+  }
   __shared__ int wave_sums[16];
   __shared__ int total;
   __shared__ int sums8[16][XCDS];
@@ -503,6 +532,70 @@ __global__ __launch_bounds__(256) void route_scatter_kernel(RouteArgs a) {
   }
 }
 
+// Block 0 routes N <= ROUTE_SMALL_SLOTS slots: counts by LDS atomics, which also give each slot its
+// place among its expert's (in arrival order: no output depends on it), a scan of counts and items,
+// then pairs and items. The other blocks write the rows of empty and invalid slots, eight slots to a
+// wave, and convert the activations.
+__global__ __launch_bounds__(1024) void route_small_kernel(RouteArgs a) {
+  constexpr int PER = (int)(ROUTE_SMALL_SLOTS / 1024), EPER = MAX_E / 1024;
+  __shared__ int cnt[MAX_E];
+  __shared__ int wave_sums[16];
+  __shared__ int total;
+  const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {
+    const int lane = tid & 63, wave = (int)(blockIdx.x - 1) * 16 + (tid >> 6);
+    for (int first = 8 * wave; first < a.N; first += 8 * 16 * (int)(gridDim.x - 1)) {  // uniform
+      const int j = first + (lane & 7), id = j < a.N ? a.ids[j] : 0;
+      const bool valid = id >= 0 && id < a.E;
+      if (!valid && id != -1) set_status(a.status, STATUS_BAD_EXPERT);
+      for (uint32_t m = (uint32_t)__ballot(!valid) & 0xFFu; m; m &= m - 1) {
+        const int s = __builtin_ctz(m);
+        const float v = __builtin_amdgcn_readlane(id, s) == -1 ? 0.0f : __builtin_nanf("");
+        float4* row = reinterpret_cast<float4*>(a.y_special + (size_t)(first + s) * a.out);
+        for (int o = lane; o < a.out / 4; o += 64) row[o] = make_float4(v, v, v, v);
+      }
+    }
+    quantize_beside(a);
+    return;
+  }
+  int id[PER], rank[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) id[j] = 1024 * j + tid < a.N ? a.ids[1024 * j + tid] : -1;
+#pragma unroll
+  for (int j = 0; j < EPER; ++j)
+    if (1024 * j < a.E) cnt[1024 * j + tid] = 0;  // uniform
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    rank[j] = 0;
+    if (id[j] >= 0 && id[j] < a.E) rank[j] = atomicAdd(&cnt[id[j]], 1);
+  }
+  __syncthreads();
+  const int R = a.item_rows;
+  int slots = 0, items = 0;  // of the passes before
+#pragma unroll
+  for (int j = 0; j < EPER; ++j) {
+    if (1024 * j >= a.E) break;  // uniform
+    const int e = 1024 * j + tid, c = e < a.E ? cnt[e] : 0, ni = (c + R - 1) / R;
+    const int off = slots + block_scan_1024(c, wave_sums, &total);
+    slots += total;
+    __syncthreads();
+    const int ib = items + block_scan_1024(ni, wave_sums, &total);
+    items += total;
+    __syncthreads();
+    if (e < a.E) {
+      cnt[e] = off;
+      for (int k = 0; k < ni; ++k)
+        reinterpret_cast<int4*>(a.items)[ib + k] = make_int4(e, off + k * R, min(R, c - k * R), 0);
+    }
+  }
+  if (tid == 0) *a.n_items = items;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (id[j] >= 0 && id[j] < a.E) a.pairs[cnt[id[j]] + rank[j]] = 1024 * j + tid;
+}
+
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ slots,
                                                       float* __restrict__ y, int64_t T,
                                                       int topk, int out) {
@@ -530,6 +623,19 @@ hipError_t launch_fill_i32(int32_t* p, int64_t n, int32_t v, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Blocks that convert activations beside the routing, of 1,024 threads which each take blocks of 32
+// inputs in turn.
+static unsigned quantize_blocks(const RouteArgs& a) {
+  return a.qx ? (unsigned)std::min<int64_t>((a.qblocks + 1023) / 1024, 4096) : 0u;
+}
+
+hipError_t launch_route_small(const RouteArgs& a, hipStream_t s) {
+  if (a.N == 0) return hipSuccess;
+  const unsigned others = std::max(quantize_blocks(a), (unsigned)((a.N + 127) / 128));
+  hipLaunchKernelGGL(route_small_kernel, dim3(1 + others), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   if (a.N == 0) return hipSuccess;
   // the scan addresses hist with 32-bit byte offsets
@@ -540,10 +646,11 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
                      (int)a.N, a.E, idbits, a.rank, a.hist);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
+  const dim3 scan(1 + quantize_blocks(a));
   if (a.items && a.split_rows > 0 && a.E <= 1024)
-    hipLaunchKernelGGL(route_scan_split_kernel, dim3(1), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(route_scan_split_kernel, scan, dim3(1024), 0, s, a);
   else
-    hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(route_scan_kernel, scan, dim3(1024), 0, s, a);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(route_scatter_kernel, dim3((unsigned)((a.N + SCATTER_SLOTS - 1) / SCATTER_SLOTS)),

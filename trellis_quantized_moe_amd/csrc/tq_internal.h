@@ -310,8 +310,17 @@ struct RouteArgs {
   float* y_special;   // per-slot output rows for empty / invalid slots, or null
   uint32_t* status;
   int blocks, item_rows, max_items;
+  // bf16 rows converted to MXFP4 beside the routing (launch_mxfp4_quantize's), or null
+  const uint16_t* qx;
+  int64_t qblocks;    // blocks of 32 inputs
+  uint8_t* qcodes;
+  uint8_t* qscales;
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+// The same in one launch for few slots, without hist, rank and the placement of items: counts,
+// offsets, pairs and items (in expert order) as there, but an expert's slots in any order.
+constexpr int64_t ROUTE_SMALL_SLOTS = 4096;
+hipError_t launch_route_small(const RouteArgs& a, hipStream_t s);
 
 hipError_t launch_fill_i32(int32_t* p, int64_t n, int32_t v, hipStream_t s);
 
