@@ -132,6 +132,49 @@ def test_a_nan_scale_of_the_weights_reaches_its_channel():
         compare(got, y, a, 512, 1, 0)
 
 
+# (E, T, topk, out, in): items of 256 rows and channels, full and with 1
+# to 255 rows, channels that end in and past the second half; more slots than one launch routes
+@pytest.mark.parametrize("E,T,topk,out,in_", [(2, 1025, 1, 8208, 512), (3, 1500, 1, 6800, 512), (4, 2100, 2, 2448, 1024),
+                                              (1, 4200, 1, 2576, 512), (20, 2049, 2, 2064, 512)])
+@pytest.mark.parametrize("repack", [False, True])
+def test_large_items(E, T, topk, out, in_, repack):
+    """Outputs of some rows (all experts, the ends of their lists) against FP64, every output against
+    the call of the token alone."""
+    o = ops()
+    layer, x, ids, gates = case(950 + E, E, T, topk, out, in_)
+    L = o.Mxfp4Layer.from_host(layer)
+    L = L.repacked() if repack else L
+    xd, idd, gd = to_dev(x, np.int16), to_dev(ids), to_dev(gates)
+    got = o.mxfp4_expert_gemm(L, xd, idd, gd, flags=o.TQ_FP4 | o.TQ_GEMM)
+    pick = sorted({0, 1, 2, T - 1, T - 2} | {int(t) for e in range(E) for t in (lambda r: (r[0], r[-1], r[len(r) // 2]))(
+        np.nonzero((ids == e).any(1))[0])})
+    y, a = reference(layer, x[pick], ids[pick], gates[pick])
+    compare(got[torch.tensor(pick, device=dev())], y, a, in_, topk, 0)
+    # other tiles hold the same rows: the sums are in the same order
+    for t0 in range(0, T, 512):
+        part = slice(t0, t0 + 512)
+        same = o.mxfp4_expert_gemm(L, xd[part], idd[part], gd[part], flags=o.TQ_FP4 | o.TQ_GEMM)
+        assert torch.equal(got[part], same)
+
+
+@pytest.mark.parametrize("E,T,topk", [(1500, 300, 4), (4096, 130, 8), (4096, 1200, 4), (1025, 1, 6), (300, 2, 64)])
+def test_many_experts(E, T, topk):
+    """Units of few channels, so that thousands of experts fit."""
+    o = ops()
+    layer, x, ids, gates = case(960 + T, E, T, topk, 16, 512)
+    if T > 4:
+        ids[3, :2] = E - 1, E
+    L = o.Mxfp4Layer.from_host(layer)
+    y, a = reference(layer, x, ids, gates)
+    for mode in (o.TQ_AUTO, o.TQ_GEMM, o.TQ_GEMV):
+        if mode == o.TQ_GEMV and T * topk > 1024:
+            continue
+        ws = o.workspace(T, topk, E, 16, 512, o.TQ_FP4 | mode)
+        got = o.mxfp4_expert_gemm(L, to_dev(x, np.int16), to_dev(ids), to_dev(gates), flags=o.TQ_FP4 | mode, ws=ws)
+        compare(got, y, a, 512, topk, 0)
+        assert o.device_status(ws) == (1 if T > 4 else 0)
+
+
 @pytest.mark.parametrize("T,mode", [(1, 0), (40, 1), (256, 1), (400, 0), (40, 2)])
 def test_the_same_bits_again_and_in_any_order_of_tokens(T, mode):
     o = ops()

@@ -1,17 +1,24 @@
 // Decode batches of the routed 4-bit product (FORMAT F30) in one launch (gfx950): no plan, no
 // routing and no conversion of the activations come before it.
 //
-// A workgroup has one routed slot and a group of 16 S output channels. Each of its waves looks
-// through all route ids: the workgroup of an expert's first slot takes all of the expert's slots,
-// those of the later ones leave at once, so every touched weight is read once (per 16 rows). The
-// four waves share out the inputs. Per window of 4 steps of 128 inputs a wave
+// A workgroup has 16 S output channels of one expert. With fewer experts than slots there is a
+// workgroup for every expert (and one per 16 slots for the rows of empty and invalid ones), else one
+// for every slot, of which those of an expert's first slot work and the others leave at once. Each of
+// its waves looks through all route ids for the expert's slots, so every touched weight is read once
+// (per 16 rows). The four waves share out the inputs. Per window of 4 steps of 128 inputs a wave
 //   - has asked for the window's codes and scales of its channels one window ahead: lane (n, q)
 //     loads the 16 bytes of block q of a step of channel n, and 16 scale bytes (4 steps) of it;
-//   - converts the rows' inputs to MXFP4 (F29): lane p block p % 16 of row p / 16, into LDS, from
-//     which lane (n, q) reads block q of row n;
+//   - converts the rows' inputs to MXFP4 (F29): lane p block p % 16 of row p / 16, loaded one
+//     conversion ahead, into LDS, from which lane (n, q) reads block q of row n;
 //   - multiplies: v_mfma_scale_f32_16x16x128_f8f6f4 per step and 16 channels.
-// The waves' sums are added in order, multiplied by the gate and written once. The kernel is bound
-// by the weights' bytes where there are many, else by the latency of its few dependent loads.
+// The waves' sums are added in order, multiplied by the gate and written once.
+//
+// Bound by the weights' bytes where there are many (64 tokens x 8 of 384 experts, 128 x 5,120: 22.7 us
+// for about 98 MB), else by the latency of its dependent loads (one token, 1,536 x 5,120: 9.8 us; 128
+// x 5,120: 6.0). 32 channels a workgroup convert the rows half as often, 16 make twice as many
+// workgroups, which is faster until there are two for every compute unit (16 and 32 channels: one
+// token x 8 of 128 outputs 6.0 and 7.0 us, of 1,536 outputs 9.9 and 10.1; two tokens 17.0 and 14.3; 64
+// tokens x 8 of 128 outputs 25.4 and 22.7).
 #include "gemm_core.h"
 #include "mx_unit.h"
 #include "mxfp4_quant.h"
@@ -44,34 +51,53 @@ __global__ __launch_bounds__(64 * FD_WAVES) void fp4_decode_kernel(Fp4DecodeArgs
   __shared__ FdShared<S> sh;
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, n = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int i0 = blockIdx.x / a.groups;
+  const int row = blockIdx.x / a.groups;
   const int first = (blockIdx.x % a.groups) * 16 * S;
   const int channels = min(16 * S, a.out - first);
-  const int e = __builtin_amdgcn_readfirstlane(a.ids[i0]);
+  const bool by_expert = a.E < a.N;
+  if (by_expert && row >= a.E) {  // empty and invalid slots of 16
+    for (int v = tid; v < 16 * 16 * S; v += 64 * FD_WAVES) {
+      const int j = 16 * (row - a.E) + v / (16 * S), o = v % (16 * S);
+      if (j >= a.N) break;
+      const int id = a.ids[j];
+      if (id >= 0 && id < a.E) continue;
+      if (o < channels) a.y[(size_t)j * a.out + first + o] = id == -1 ? 0.0f : __builtin_nanf("");
+      if (id != -1 && o == 0) set_status(a.status, STATUS_BAD_EXPERT);
+    }
+    return;
+  }
+  const int e = by_expert ? row : __builtin_amdgcn_readfirstlane(a.ids[row]);
   if (e < 0 || e >= a.E) {  // an empty or invalid slot
     const float v = e == -1 ? 0.0f : __builtin_nanf("");
-    if (tid < channels) a.y[(size_t)i0 * a.out + first + tid] = v;
+    if (tid < channels) a.y[(size_t)row * a.out + first + tid] = v;
     if (e != -1 && tid == 0) set_status(a.status, STATUS_BAD_EXPERT);
     return;
   }
-  // the expert's slots; every wave writes the same list
+  // the expert's slots, 512 ids asked for at a time; every wave writes the same list
+  const GemmRsrc ri = gemm_rsrc(a.ids, 4u * (uint32_t)a.N);
   int cnt = 0, lead = -1;
-  for (int j0 = 0; j0 < a.N; j0 += 64) {
-    const int j = j0 + lane;
-    const bool hit = j < a.N && a.ids[j] == e;
-    const uint64_t m = __ballot(hit);
-    if (m && lead < 0) lead = j0 + __builtin_ctzll(m);
-    if (hit)
-      sh.list[cnt + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = j;
-    cnt += __builtin_popcountll(m);
+  for (int j0 = 0; j0 < a.N; j0 += 512) {
+    uint32_t id[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) id[u] = __builtin_amdgcn_raw_buffer_load_b32(ri, 4 * (j0 + 64 * u + lane), 0, 0);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + 64 * u + lane;
+      const bool hit = j < a.N && (int)id[u] == e;
+      const uint64_t m = __ballot(hit);
+      if (m && lead < 0) lead = j0 + 64 * u + __builtin_ctzll(m);
+      if (hit)
+        sh.list[cnt + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = j;
+      cnt += __builtin_popcountll(m);
+    }
+    if (!by_expert && lead >= 0 && lead != row) return;  // uniform
   }
-  if (lead != i0) return;  // uniform
+  if (cnt == 0) return;  // uniform
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
-
   const uint8_t* unit = a.units + (size_t)e * U::unit_bytes(a.out, a.in);
   const GemmRsrc rb = gemm_rsrc(unit, (uint32_t)U::unit_bytes(a.out, a.in));
-  const int steps = a.in / 128 / FD_WAVES, s0 = w * steps;  // this wave's (in is a multiple of 512)
+  const int s0 = a.in / 128 * w / FD_WAVES, steps = a.in / 128 * (w + 1) / FD_WAVES - s0;  // this wave's
   uint32_t bvo[S], bso[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
@@ -98,6 +124,7 @@ __global__ __launch_bounds__(64 * FD_WAVES) void fp4_decode_kernel(Fp4DecodeArgs
     for (int s = 0; s < S; ++s)
       b.scale[s] = __builtin_amdgcn_raw_buffer_load_b128(rb, bso[s], 4u * (uint32_t)(s0 + k), 0);
   };
+  Weights b;
   uint8_t* wcodes = sh.codes[w];
   uint8_t* wscales = sh.scales[w];
   for (int c0 = 0; c0 < cnt; c0 += 16) {
@@ -114,26 +141,25 @@ __global__ __launch_bounds__(64 * FD_WAVES) void fp4_decode_kernel(Fp4DecodeArgs
     f32x4 acc[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) acc[s] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    Weights b;
     u32x4 xv[4];
     load_weights(b, 0);
     load_x(xv, 0, 0);
     for (int k = 0; k < steps; k += FD_WINDOW) {
       for (int p = 0; p < passes; ++p) {
-        if (p > 0) load_x(xv, p, k);
+        u32x4 nv[4];
+        const bool more = p + 1 < passes;
+        load_x(nv, more ? p + 1 : 0, more ? k : k + FD_WINDOW);
         const Fp4Block v = fp4_block(xv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xv[j] = nv[j];
         const int r = 4 * p + q;
         *reinterpret_cast<u32x4*>(wcodes + 256 * r + 16 * n) = v.codes;
         wscales[16 * r + n] = (uint8_t)v.scale;
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
       __builtin_amdgcn_wave_barrier();
-      Weights cur = b;
-      const int next = k + FD_WINDOW;
-      if (next < steps) {
-        load_weights(b, next);
-        load_x(xv, 0, next);
-      }
+      const Weights cur = b;
+      load_weights(b, k + FD_WINDOW);
       const u32x4 sa = *reinterpret_cast<const u32x4*>(wscales + 16 * n);
 #pragma unroll
       for (int t = 0; t < FD_WINDOW; ++t) {
@@ -170,10 +196,10 @@ __global__ __launch_bounds__(64 * FD_WAVES) void fp4_decode_kernel(Fp4DecodeArgs
 
 hipError_t launch_fp4_decode(const Fp4DecodeArgs& args, hipStream_t s) {
   Fp4DecodeArgs a = args;
-  const int strips = a.out / 16;
-  const int S = 1;
-  a.groups = (strips + S - 1) / S;
-  const dim3 grid((unsigned)(a.N * a.groups)), block(64 * FD_WAVES);
+  const int64_t strips = a.out / 16, rows = a.E < a.N ? a.E + (a.N + 15) / 16 : a.N;
+  const int S = (strips + 1) / 2 * a.N < 512 ? 1 : 2;
+  a.groups = (int)(strips + S - 1) / S;
+  const dim3 grid((unsigned)(rows * a.groups)), block(64 * FD_WAVES);
   if (S == 1) return launch_timed(fp4_decode_kernel<1>, grid, block, s, a);
   return launch_timed(fp4_decode_kernel<2>, grid, block, s, a);
 }
