@@ -266,3 +266,32 @@ def test_what_ran_before_keeps_its_results():
     for flags in (o.TQ_GEMV, o.TQ_GEMM):
         got = o.mxfp4_expert_gemm(L, to_dev(x, np.int16), to_dev(ids), to_dev(gates), flags=flags).cpu().numpy()
         assert np.linalg.norm(got - ref) <= 1e-3 * np.linalg.norm(ref)
+
+
+def test_refusals():
+    """Arguments whose memory the kernels would read as something else; nothing is launched."""
+    o = ops()
+    layer, x, ids, gates = case(942, 4, 6, 2, 48, 512)
+    L = o.Mxfp4Layer.from_host(layer)
+    x, ids, gates = to_dev(x, np.int16), to_dev(ids), to_dev(gates)
+    flags = o.TQ_FP4
+    good = o.mxfp4_expert_gemm(L, x, ids, gates, flags=flags)
+    bad = [dict(x=x.float()), dict(x=x[:, :256]), dict(x=x[:5]), dict(x=x.t().contiguous().t()), dict(x=x.cpu()),
+           dict(topk_ids=ids.long()), dict(topk_ids=ids[0]), dict(topk_ids=ids.t().contiguous().t()),
+           dict(topk_w=gates.double()), dict(topk_w=gates[:, :1]), dict(topk_w=gates.bfloat16()),
+           dict(out=torch.empty((6, 2, 48), device=dev(), dtype=torch.bfloat16)), dict(out=torch.empty((6, 48), device=dev())),
+           dict(out=torch.empty((6, 2, 64), device=dev())[:, :, :48]),
+           dict(out=torch.empty((6, 2, 48), device=dev()), flags=flags | o.TQ_COMBINE),
+           dict(ws=torch.empty(1 << 20, device=dev())), dict(ws=torch.empty(1 << 20, dtype=torch.uint8))]
+    for b in bad:
+        args = dict(x=x, topk_ids=ids, topk_w=gates, flags=flags)
+        args.update(b)
+        with pytest.raises(ValueError):
+            o.mxfp4_expert_gemm(L, **args)
+    small = torch.zeros(256, dtype=torch.uint8, device=dev())
+    for b in (dict(ws=small, flags=flags | o.TQ_GEMM), dict(flags=flags | o.TQ_FP8), dict(flags=flags | 3)):
+        args = dict(x=x, topk_ids=ids, topk_w=gates, flags=flags)
+        args.update(b)
+        with pytest.raises(RuntimeError):
+            o.mxfp4_expert_gemm(L, **args)
+    assert torch.equal(o.mxfp4_expert_gemm(L, x, ids, gates, flags=flags), good)

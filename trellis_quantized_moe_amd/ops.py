@@ -191,8 +191,9 @@ def _gemm(fn, layer_c, E, out_ch, in_, x, topk_ids, topk_w, flags, out, ws, mxfp
         out = torch.empty(shape, dtype=torch.float32, device=x.device)
     if ws is None:
         ws = workspace(T, topk, E, out_ch, in_, flags, device=x.device)
-    check(fn(ctypes.byref(layer_c), _ptr(x), T, _ptr(topk_ids), _ptr(topk_w), topk, _ptr(out),
-             flags, _ptr(ws), ws.numel(), _stream(x.device)))
+    _call_on(x.device, fn, ctypes.byref(layer_c), x.data_ptr(), T, topk_ids.data_ptr(),
+             None if topk_w is None else topk_w.data_ptr(), topk, out.data_ptr(), flags,
+             ws.data_ptr(), ws.numel())
     return out
 
 
@@ -219,6 +220,10 @@ def trellis_expert_gemm_noalloc(layer, x, topk_ids, topk_w=None, flags=TQ_AUTO, 
 
 
 def mxfp4_expert_gemm(layer, x, topk_ids, topk_w=None, flags=TQ_AUTO, out=None, ws=None):
+    """fp32 per-slot outputs [T, topk, out] (or [T, out] with TQ_COMBINE) of bf16 x [T, in]; TQ_FP4
+    multiplies in 4 bits on both sides (see mxfp4_expert_gemm in include/tq.h)."""
+    if flags & TQ_FP4:
+        _check_fp4(layer, x, topk_ids, topk_w, flags, out, ws)
     return _gemm(_lib.load().mxfp4_expert_gemm, layer.c_struct(), layer.E, layer.out,
                  layer.in_, x, topk_ids, topk_w, flags, out, ws, True)
 
@@ -257,7 +262,7 @@ def mxfp4_decode(unit, out_ch, in_):
     """bf16 bit patterns (int16) [out, in] of one MXFP4 unit."""
     _require_cuda(unit)
     w = torch.empty((out_ch, in_), dtype=torch.int16, device=unit.device)
-    check(_lib.load().mxfp4_decode(_ptr(unit), out_ch, in_, _ptr(w), _stream(unit.device)))
+    _call_on(unit.device, _lib.load().mxfp4_decode, unit.data_ptr(), out_ch, in_, w.data_ptr())
     return w
 
 
@@ -372,8 +377,9 @@ def _check_rows(name, t, dtypes, device=None, shape=None):
         raise ValueError("tensors must be on the GPU")
     if t.dtype not in dtypes:
         raise ValueError("%s is %s, not %s" % (name, t.dtype, dtypes[0]))
-    if t.dim() != 2 or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous 2-D tensor" % name)
+    dims = 2 if shape is None else len(shape)
+    if t.dim() != dims or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %d-D tensor" % (name, dims))
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, not %s" % (name, t.device, device))
     raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), shape))
@@ -529,6 +535,20 @@ def fp8b128_ffn(gate_up, down, x, flags=0, out=None, ws=None):
     _call_on(dev, lib.fp8b128_ffn, gate_up._ref, down._ref,
              x.data_ptr(), T, out.data_ptr(), flags, ws.data_ptr(), ws.numel())
     return out
+
+
+def _check_fp4(layer, x, topk_ids, topk_w, flags, out, ws):
+    dev = layer.units.device
+    _check_rows("topk_ids", topk_ids, _I32, dev)
+    T, topk = topk_ids.shape
+    _check_rows("x", x, _BF16, dev, (T, layer.in_))
+    if topk_w is not None:
+        _check_rows("topk_w", topk_w, _F32, dev, (T, topk))
+    if out is not None:
+        _check_rows("out", out, _F32, dev,
+                    (T, layer.out) if flags & TQ_COMBINE else (T, topk, layer.out))
+    if ws is not None:
+        _check_ws(ws, dev, 0)
 
 
 def mxfp4_quantize(x, codes=None, scales=None):
