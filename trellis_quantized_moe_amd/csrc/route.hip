@@ -23,8 +23,8 @@
 // slots in runs of item_rows); without a split the list is in expert order. Which item
 // computes a slot changes nothing in its result.
 //
-// The 4-bit product converts its activations beside the routing: in further blocks of the scan's
-// launch, which is one block, or of the one launch that routes few slots.
+// The 4-bit product converts its activations beside the routing: in further blocks of the launches of
+// the ranks and of the scan, which is one block, or of the one launch that routes few slots.
 #include <algorithm>
 
 #include "mxfp4_quant.h"
@@ -43,6 +43,25 @@ constexpr int XCDS = 8;
 constexpr int XCD_CUS = 32;        // compute units per XCD
 constexpr int ORDER_ROUNDS = 2;    // item lists of up to 2048 are put in snake order
 
+// Blocks first .. gridDim.x - 1 of a launch: rows in MXFP4 (FORMAT F29), the blocks of 32 inputs from
+// begin to end, one per thread at a time.
+__device__ __forceinline__ void quantize_beside(const RouteArgs& a, int first, int64_t begin, int64_t end) {
+  const u32x4* x = reinterpret_cast<const u32x4*>(a.qx);
+  for (int64_t i = begin + (int64_t)(blockIdx.x - first) * blockDim.x + threadIdx.x; i < end;
+       i += (int64_t)(gridDim.x - first) * blockDim.x) {
+    u32x4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = x[4 * i + q];
+    const Fp4Block r = fp4_block(v);
+    reinterpret_cast<u32x4*>(a.qcodes)[i] = r.codes;
+    a.qscales[i] = (uint8_t)r.scale;
+  }
+}
+// A quarter of them beside the ranks, about what those have time for, the rest beside the scan (both
+// launches, 8,192 rows of 5,120: 27.2 us; with a sixth and a third 28.2 and 27.1, with none 29.2; over
+// 32 experts, after larger outputs, 31.9, 33.1, 32.8 and 34.9).
+__host__ __device__ inline int64_t beside_rank(const RouteArgs& a) { return a.qblocks / 4; }
+
 // Wave w of rank block b ranks slots b * RANK_BLOCK + w * (RANK_BLOCK / RANK_WAVES) .. in
 // rounds of 64: the lanes holding the same expert are found with one ballot per id bit, and a
 // slot's rank among the wave's earlier slots of its expert comes from the wave's running count
@@ -50,7 +69,11 @@ constexpr int ORDER_ROUNDS = 2;    // item lists of up to 2048 are put in snake 
 // the waves, in order), adds them, and writes its per-expert totals to hist.
 __global__ __launch_bounds__(64 * RANK_WAVES) void route_rank_kernel(
     const int32_t* __restrict__ ids, int N, int E, int idbits, int32_t* __restrict__ rank,
-    int32_t* __restrict__ hist) {
+    int32_t* __restrict__ hist, RouteArgs a) {
+  if ((int)blockIdx.x >= a.blocks) {
+    quantize_beside(a, a.blocks, 0, beside_rank(a));
+    return;
+  }
   __shared__ int cnt[RANK_WAVES][MAX_E];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int b = blockIdx.x;
@@ -324,24 +347,9 @@ __device__ __forceinline__ void hist_bases(__amdgpu_buffer_rsrc_t rh, int E, int
   }
 }
 
-// Blocks 1 .. gridDim.x - 1 of 1,024 threads: the rows in MXFP4 (FORMAT F29), a block of 32 inputs
-// per thread.
-__device__ __forceinline__ void quantize_beside(const RouteArgs& a) {
-  const u32x4* x = reinterpret_cast<const u32x4*>(a.qx);
-  for (int64_t i = (int64_t)(blockIdx.x - 1) * 1024 + threadIdx.x; i < a.qblocks;
-       i += (int64_t)(gridDim.x - 1) * 1024) {
-    u32x4 v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = x[4 * i + q];
-    const Fp4Block r = fp4_block(v);
-    reinterpret_cast<u32x4*>(a.qcodes)[i] = r.codes;
-    a.qscales[i] = (uint8_t)r.scale;
-  }
-}
-
 __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
   if (blockIdx.x > 0) {
-    quantize_beside(a);
+    quantize_beside(a, 1, beside_rank(a), a.qblocks);
     return;
   }
   __shared__ int wave_sums[16];
@@ -399,7 +407,7 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
 // 1024: one expert per thread).
 __global__ __launch_bounds__(1024) void route_scan_split_kernel(RouteArgs a) {
   if (blockIdx.x > 0) {
-    quantize_beside(a);
+    quantize_beside(a, 1, beside_rank(a), a.qblocks);
     return;
   }
   __shared__ int wave_sums[16];
@@ -555,7 +563,7 @@ __global__ __launch_bounds__(1024) void route_small_kernel(RouteArgs a) {
         for (int o = lane; o < a.out / 4; o += 64) row[o] = make_float4(v, v, v, v);
       }
     }
-    quantize_beside(a);
+    quantize_beside(a, 1, 0, a.qblocks);
     return;
   }
   int id[PER], rank[PER];
@@ -623,15 +631,14 @@ hipError_t launch_fill_i32(int32_t* p, int64_t n, int32_t v, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Blocks that convert activations beside the routing, of 1,024 threads which each take blocks of 32
-// inputs in turn.
-static unsigned quantize_blocks(const RouteArgs& a) {
-  return a.qx ? (unsigned)std::min<int64_t>((a.qblocks + 1023) / 1024, 4096) : 0u;
+// Blocks of some threads that convert n blocks of 32 inputs beside the routing.
+static unsigned quantize_blocks(int64_t n, int threads) {
+  return (unsigned)std::min<int64_t>((n + threads - 1) / threads, 4096);
 }
 
 hipError_t launch_route_small(const RouteArgs& a, hipStream_t s) {
   if (a.N == 0) return hipSuccess;
-  const unsigned others = std::max(quantize_blocks(a), (unsigned)((a.N + 127) / 128));
+  const unsigned others = std::max(quantize_blocks(a.qblocks, 1024), (unsigned)((a.N + 127) / 128));
   hipLaunchKernelGGL(route_small_kernel, dim3(1 + others), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
@@ -642,11 +649,12 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   if ((int64_t)a.blocks * a.E * 4 >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
   int idbits = 1;
   while ((1 << idbits) < a.E) ++idbits;
-  hipLaunchKernelGGL(route_rank_kernel, dim3(a.blocks), dim3(64 * RANK_WAVES), 0, s, a.ids,
-                     (int)a.N, a.E, idbits, a.rank, a.hist);
+  const int64_t early = beside_rank(a);
+  hipLaunchKernelGGL(route_rank_kernel, dim3(a.blocks + quantize_blocks(early, 64 * RANK_WAVES)),
+                     dim3(64 * RANK_WAVES), 0, s, a.ids, (int)a.N, a.E, idbits, a.rank, a.hist, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const dim3 scan(1 + quantize_blocks(a));
+  const dim3 scan(1 + quantize_blocks(a.qblocks - early, 1024));
   if (a.items && a.split_rows > 0 && a.E <= 1024)
     hipLaunchKernelGGL(route_scan_split_kernel, scan, dim3(1024), 0, s, a);
   else
