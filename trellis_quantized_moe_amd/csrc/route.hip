@@ -580,24 +580,23 @@ __global__ __launch_bounds__(1024) void route_small_kernel(RouteArgs a) {
   }
   __syncthreads();
   const int R = a.item_rows;
-  int slots = 0, items = 0;  // of the passes before
+  // slots in the low half, items in the high half: both stay below 2^16
+  static_assert(ROUTE_SMALL_SLOTS < 1 << 16, "a half holds every count");
+  int before = 0;  // of the passes before
 #pragma unroll
   for (int j = 0; j < EPER; ++j) {
     if (1024 * j >= a.E) break;  // uniform
     const int e = 1024 * j + tid, c = e < a.E ? cnt[e] : 0, ni = (c + R - 1) / R;
-    const int off = slots + block_scan_1024(c, wave_sums, &total);
-    slots += total;
-    __syncthreads();
-    const int ib = items + block_scan_1024(ni, wave_sums, &total);
-    items += total;
-    __syncthreads();
+    const int at = before + block_scan_1024(c | ni << 16, wave_sums, &total);
+    before += total;
+    const int off = at & 0xFFFF, ib = at >> 16;
     if (e < a.E) {
       cnt[e] = off;
       for (int k = 0; k < ni; ++k)
         reinterpret_cast<int4*>(a.items)[ib + k] = make_int4(e, off + k * R, min(R, c - k * R), 0);
     }
   }
-  if (tid == 0) *a.n_items = items;
+  if (tid == 0) *a.n_items = before >> 16;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < PER; ++j)
