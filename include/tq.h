@@ -274,7 +274,7 @@ int mxfp4_quantize(const void* x, int64_t rows, int64_t n, uint8_t* codes, uint8
  *   xq[t][i] = E2M1[a[t][i]] * 2^(s[t][i/32] - 127)   (a, s: mxfp4_quantize of x)
  * The matrix cores add the products of a block of 32 exactly and the blocks in fp32. A block of
  * a token that holds an infinity or NaN makes that token's slots NaN. T * in must stay below
- * 2^32.
+ * 2^30.
  */
 
 /*

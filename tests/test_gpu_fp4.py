@@ -295,3 +295,44 @@ def test_refusals():
         with pytest.raises(RuntimeError):
             o.mxfp4_expert_gemm(L, **args)
     assert torch.equal(o.mxfp4_expert_gemm(L, x, ids, gates, flags=flags), good)
+
+
+def random_units(E, out, in_, seed):
+    g = torch.Generator(device=dev()).manual_seed(seed)
+    units = torch.randint(0, 256, (E, out * in_ // 2 + out * in_ // 32), dtype=torch.uint8, device=dev(), generator=g)
+    units[:, out * in_ // 2:] %= 8
+    units[:, out * in_ // 2:] += 118
+    return units
+
+
+def test_offsets_past_32_bits():
+    """Activations of nearly 2^30 elements, results and units past 2^32 bytes: the last rows and
+    experts against small calls of them alone."""
+    o = ops()
+    g = torch.Generator(device=dev()).manual_seed(7)
+
+    def rows(T, in_, n):  # the last n tokens are random, the others zero (padding)
+        x = torch.zeros((T, in_), dtype=torch.bfloat16, device=dev())
+        x[-n:] = torch.randn((n, in_), dtype=torch.bfloat16, device=dev(), generator=g)
+        return x
+
+    for T, E, out, in_ in (((1 << 20) - 1, 3, 16, 1024), (135001, 1, 8208, 512)):
+        L = o.Mxfp4Layer(E, out, in_, random_units(E, out, in_, T).reshape(-1))
+        x = rows(T, in_, 300)
+        ids = (torch.arange(T, device=dev(), dtype=torch.int32) % E).view(T, 1)
+        got = o.mxfp4_expert_gemm(L, x, ids, flags=o.TQ_FP4)
+        want = o.mxfp4_expert_gemm(L, x[-300:], ids[-300:], flags=o.TQ_FP4 | o.TQ_GEMM)
+        assert torch.equal(got[-300:], want) and bool(want.any())
+        assert not bool(got[:-300].any())
+        del x, got
+
+    E, out, in_ = 800, 2048, 5120
+    units = random_units(E, out, in_, 3)
+    L = o.Mxfp4Layer(E, out, in_, units.view(-1))
+    last = o.Mxfp4Layer(1, out, in_, units[-1])
+    for T, mode in ((3, o.TQ_GEMV), (3, o.TQ_GEMM), (40, o.TQ_AUTO)):
+        x = rows(T, in_, T)
+        got = o.mxfp4_expert_gemm(L, x, torch.full((T, 1), E - 1, dtype=torch.int32, device=dev()), flags=o.TQ_FP4 | mode)
+        want = o.mxfp4_expert_gemm(last, x, torch.zeros((T, 1), dtype=torch.int32, device=dev()),
+                                   flags=o.TQ_FP4 | (mode or o.TQ_GEMM))
+        assert torch.equal(got, want) and bool(want.any())

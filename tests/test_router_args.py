@@ -113,6 +113,9 @@ def test_fp4_sizes(lib):
     assert experts(lib, in_=768) == _lib.TQ_EINVAL
     assert experts(lib, out=24) == _lib.TQ_EINVAL
     assert experts(lib, T=1 << 24, topk=1) == _lib.TQ_EINVAL
+    for mode in (0, _lib.TQ_GEMM):
+        assert experts(lib, T=1 << 20, topk=1, flags=FP4 | mode) == _lib.TQ_EINVAL
+        assert b"2^30" in lib.tq_last_error()
     assert experts(lib, topk=65) == _lib.TQ_EINVAL
     assert experts(lib, ids=None) == _lib.TQ_EINVAL
     assert experts(lib, x=P + 8) == _lib.TQ_EALIGN

@@ -905,8 +905,8 @@ int mx_expert_gemm(const MxLayer* L, const void* x, int64_t T, const int32_t* to
     return fail(TQ_EINVAL,
                 "decode batches with TQ_FP4 take at most %d slots (T * topk = %lld) and 2^20 / 8 "
                 "(slot, 128 channels) pairs", tq::FP4_DECODE_SLOTS, (long long)(T * topk));
-  if ((flags & TQ_FP4) && T * (int64_t)L->in >= ((int64_t)1 << 32))
-    return fail(TQ_EINVAL, "the MXFP4 activations (T * in / 2 bytes) must stay below 2^31");
+  if ((flags & TQ_FP4) && T * (int64_t)L->in >= ((int64_t)1 << 30))
+    return fail(TQ_EINVAL, "the activations of TQ_FP4 (T * in) must stay below 2^30");
   const int64_t unit = mx_unit_bytes(L->fmt, L->out, L->in);
   tq::WsLayout W;
   int rc = common_checks(L->E, L->out, L->in, x, T, topk_ids, topk, y, flags, ws, ws_bytes, unit, &W);

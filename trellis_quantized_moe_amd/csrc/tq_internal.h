@@ -229,7 +229,7 @@ struct Mx8GemmArgs {
   int layout;            // 0: codes in store order; 1: repacked
   const uint8_t* units;
   const uint8_t* xa;     // E4M3 codes [T][in]
-  uint32_t xa_bytes;     // < 2^31
+  uint32_t xa_bytes;     // < 2^29
   const uint8_t* xs;     // E8M0 scales [T][in / 32]
   uint32_t xs_bytes;
   const float* gates;
@@ -250,7 +250,7 @@ struct Fp4GemmArgs {
   int layout;            // 0: codes in store order; 1: repacked
   const uint8_t* units;
   const uint8_t* xa;     // E2M1 codes [T][in / 2]
-  uint32_t xa_bytes;     // < 2^31
+  uint32_t xa_bytes;     // < 2^29
   const uint8_t* xs;     // E8M0 scales [T][in / 32]
   uint32_t xs_bytes;
   const float* gates;
