@@ -1,5 +1,6 @@
 // bf16 rows in MXFP4 (gfx950; FORMAT F29): one thread per block of 32 inputs (mxfp4_quant.h).
-// Bound by memory: 2 bytes read and 17 / 32 written per element.
+// Bound by memory: 2 bytes read and 17 / 32 written per element (49,152 x 5,120: 135 us, 4.7 TB/s; 64 x
+// 5,120: 2.6 us, latency). Four lanes to a block, which load and store whole lines, took 138 and 2.9.
 #include "mxfp4_quant.h"
 #include "tq_internal.h"
 
