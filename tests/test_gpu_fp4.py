@@ -316,15 +316,18 @@ def test_offsets_past_32_bits():
         x[-n:] = torch.randn((n, in_), dtype=torch.bfloat16, device=dev(), generator=g)
         return x
 
-    for T, E, out, in_ in (((1 << 20) - 1, 3, 16, 1024), (135001, 1, 8208, 512)):
+    # (the last: more outputs than a launch has threads, combined)
+    for T, E, out, in_, flags in (((1 << 20) - 1, 3, 16, 1024, 0), (135001, 1, 8208, 512, 0),
+                                  (525001, 1, 8208, 512, o.TQ_COMBINE)):
         L = o.Mxfp4Layer(E, out, in_, random_units(E, out, in_, T).reshape(-1))
         x = rows(T, in_, 300)
         ids = (torch.arange(T, device=dev(), dtype=torch.int32) % E).view(T, 1)
-        got = o.mxfp4_expert_gemm(L, x, ids, flags=o.TQ_FP4)
-        want = o.mxfp4_expert_gemm(L, x[-300:], ids[-300:], flags=o.TQ_FP4 | o.TQ_GEMM)
+        got = o.mxfp4_expert_gemm(L, x, ids, flags=o.TQ_FP4 | flags)
+        want = o.mxfp4_expert_gemm(L, x[-300:], ids[-300:], flags=o.TQ_FP4 | o.TQ_GEMM | flags)
         assert torch.equal(got[-300:], want) and bool(want.any())
         assert not bool(got[:-300].any())
-        del x, got
+        del x, got, want
+        torch.cuda.empty_cache()
 
     E, out, in_ = 800, 2048, 5120
     units = random_units(E, out, in_, 3)

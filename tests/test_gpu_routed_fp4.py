@@ -76,3 +76,19 @@ def test_router_to_experts_and_back(T, score, renorm):
         want = o.mxfp4_expert_gemm(layer, x, i, v, flags=flags)
         torch.cuda.synchronize()
         assert torch.equal(slots, want) and torch.equal(ids, i)
+
+
+def test_routes_of_more_slots_than_fit_one_grid():
+    """2^29 slots and more: the placement's workgroups of 32 slots would be more than 2^32 threads."""
+    o = ops()
+    T, topk, E = (1 << 23) + 3, 64, 5
+    N = T * topk
+    ids = (torch.arange(N, device=dev()) % E).int()
+    ids[N - 7] = -1
+    counts, offsets, pairs = o.route_bucket(ids.view(T, topk), E)
+    gone = (N - 7) % E
+    for e in range(E):
+        want = torch.arange(e, N, E, device=dev(), dtype=torch.int32)
+        want = want[want != N - 7] if e == gone else want
+        assert int(counts[e]) == want.numel()
+        assert torch.equal(pairs[int(offsets[e]):int(offsets[e + 1])], want)

@@ -518,25 +518,27 @@ __global__ __launch_bounds__(1024) void route_scan_split_kernel(RouteArgs a) {
 constexpr int SCATTER_SLOTS = 32;
 
 __global__ __launch_bounds__(256) void route_scatter_kernel(RouteArgs a) {
-  const int first = blockIdx.x * SCATTER_SLOTS;
-  const int lane = threadIdx.x & 63, j = lane & (SCATTER_SLOTS - 1), i = first + j;
-  const int id = i < a.N ? a.ids[i] : 0;
-  const bool valid = id >= 0 && id < a.E;
-  if ((int)threadIdx.x < SCATTER_SLOTS && i < a.N) {
-    if (valid)
-      a.pairs[a.hist[(size_t)(i / RANK_BLOCK) * a.E + id] + a.rank[i]] = i;
-    else if (id != -1)
-      set_status(a.status, STATUS_BAD_EXPERT);
-  }
-  if (!a.y_special) return;
+  const int lane = threadIdx.x & 63, j = lane & (SCATTER_SLOTS - 1);
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint32_t m = (uint32_t)__ballot(!valid);  // a slot past the last one counts as valid
-  for (int k = 0; m; m &= m - 1, ++k) {     // uniform
-    if ((k & 3) != w) continue;
-    const int s = __builtin_ctz(m);
-    const float v = __builtin_amdgcn_readlane(id, s) == -1 ? 0.0f : __builtin_nanf("");
-    float4* row = reinterpret_cast<float4*>(a.y_special + (size_t)(first + s) * a.out);
-    for (int o = lane; o < a.out / 4; o += 64) row[o] = make_float4(v, v, v, v);
+  for (int64_t first = (int64_t)blockIdx.x * SCATTER_SLOTS; first < a.N; first += (int64_t)gridDim.x * SCATTER_SLOTS) {
+    const int64_t i = first + j;
+    const int id = i < a.N ? a.ids[i] : 0;
+    const bool valid = id >= 0 && id < a.E;
+    if ((int)threadIdx.x < SCATTER_SLOTS && i < a.N) {
+      if (valid)
+        a.pairs[a.hist[(size_t)(i / RANK_BLOCK) * a.E + id] + a.rank[i]] = (int)i;
+      else if (id != -1)
+        set_status(a.status, STATUS_BAD_EXPERT);
+    }
+    if (!a.y_special) continue;
+    uint32_t m = (uint32_t)__ballot(!valid);  // a slot past the last one counts as valid
+    for (int k = 0; m; m &= m - 1, ++k) {     // uniform
+      if ((k & 3) != w) continue;
+      const int s = __builtin_ctz(m);
+      const float v = __builtin_amdgcn_readlane(id, s) == -1 ? 0.0f : __builtin_nanf("");
+      float4* row = reinterpret_cast<float4*>(a.y_special + (size_t)(first + s) * a.out);
+      for (int o = lane; o < a.out / 4; o += 64) row[o] = make_float4(v, v, v, v);
+    }
   }
 }
 
@@ -606,14 +608,14 @@ __global__ __launch_bounds__(1024) void route_small_kernel(RouteArgs a) {
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ slots,
                                                       float* __restrict__ y, int64_t T,
                                                       int topk, int out) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (idx >= T * out) return;
-  const int64_t t = idx / out;
-  const int o = (int)(idx % out);
-  const float* src = slots + (size_t)t * topk * out + o;
-  float acc = 0.0f;
-  for (int k = 0; k < topk; ++k) acc += src[(size_t)k * out];
-  y[idx] = acc;
+  for (int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x; idx < T * out; idx += (int64_t)gridDim.x * 256) {
+    const int64_t t = idx / out;
+    const int o = (int)(idx % out);
+    const float* src = slots + (size_t)t * topk * out + o;
+    float acc = 0.0f;
+    for (int k = 0; k < topk; ++k) acc += src[(size_t)k * out];
+    y[idx] = acc;
+  }
 }
 
 __global__ __launch_bounds__(256) void fill_i32_kernel(int32_t* __restrict__ p, int64_t n,
@@ -660,8 +662,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(route_scan_kernel, scan, dim3(1024), 0, s, a);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(route_scatter_kernel, dim3((unsigned)((a.N + SCATTER_SLOTS - 1) / SCATTER_SLOTS)),
-                     dim3(256), 0, s, a);
+  // (a launch may have 2^32 threads)
+  const int64_t blocks = std::min<int64_t>((a.N + SCATTER_SLOTS - 1) / SCATTER_SLOTS, 1 << 20);
+  hipLaunchKernelGGL(route_scatter_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -669,8 +672,8 @@ hipError_t launch_combine(const float* slots, float* y, int64_t T, int topk, int
                           hipStream_t s) {
   const int64_t total = T * out;
   if (total == 0) return hipSuccess;
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s,
-                     slots, y, T, topk, out);
+  const int64_t blocks = std::min<int64_t>((total + 255) / 256, 1 << 23);  // (2^32 threads at most)
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)blocks), dim3(256), 0, s, slots, y, T, topk, out);
   return hipGetLastError();
 }
 
