@@ -50,33 +50,45 @@ __device__ __forceinline__ void store_grad(uint16_t* p, int64_t i, float v) {
   p[i] = (uint16_t)f32_to_bf16_rne(v);
 }
 
-// Value of another lane by DPP; lanes without a source (or outside the row mask) keep `old`.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp(float old, float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROWS, 0xF, false));
-}
-__device__ __forceinline__ float lane63(float v) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-// Largest value (no NaN) and sum over the wave: row shifts 1, 2, 4, 8, then row broadcasts 15 and 31.
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, dpp<0x111, 0xF>(v, v));
-  v = fmaxf(v, dpp<0x112, 0xF>(v, v));
-  v = fmaxf(v, dpp<0x114, 0xF>(v, v));
-  v = fmaxf(v, dpp<0x118, 0xF>(v, v));
-  v = fmaxf(v, dpp<0x142, 0xA>(v, v));
-  v = fmaxf(v, dpp<0x143, 0xC>(v, v));
-  return lane63(v);
+// Reductions over the wave in moves that the compiler makes part of the operation: row shifts 1, 2, 4,
+// 8, then row broadcasts 15 and 31, after which lane 63 has the result. A lane without a source takes a
+// 0, which changes no sum and no maximum of unsigned integers.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 __device__ __forceinline__ float wave_sum(float v) {
-  v += dpp<0x111, 0xF>(0.0f, v);
-  v += dpp<0x112, 0xF>(0.0f, v);
-  v += dpp<0x114, 0xF>(0.0f, v);
-  v += dpp<0x118, 0xF>(0.0f, v);
-  v += dpp<0x142, 0xA>(0.0f, v);
-  v += dpp<0x143, 0xC>(0.0f, v);
-  return lane63(v);
+  v = add_dpp<0x111>(v);
+  v = add_dpp<0x112>(v);
+  v = add_dpp<0x114>(v);
+  v = add_dpp<0x118>(v);
+  v = add_dpp<0x142>(v);
+  v = add_dpp<0x143>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
+// fp32 values as integers of the same order (both zeros are one value), and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max_dpp<0x111>(v);
+  v = max_dpp<0x112>(v);
+  v = max_dpp<0x114>(v);
+  v = max_dpp<0x118>(v);
+  v = max_dpp<0x142>(v);
+  v = max_dpp<0x143>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// The largest value (no NaN among them).
+__device__ __forceinline__ float wave_max(float v) { return unordered(wave_max(ordered(v))); }
 __device__ __forceinline__ double wave_max(double v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
@@ -121,27 +133,6 @@ struct Choice {
   bool more;
 };
 
-// fp32 values as integers of the same order (both zeros are one value), and back.
-__device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t u) {
-  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROWS, 0xF, false));
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max_dpp<0x111, 0xF>(v);
-  v = max_dpp<0x112, 0xF>(v);
-  v = max_dpp<0x114, 0xF>(v);
-  v = max_dpp<0x118, 0xF>(v);
-  v = max_dpp<0x142, 0xA>(v);
-  v = max_dpp<0x143, 0xC>(v);
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
 // topk times the largest key of the row: lane r gets the r-th. With `near`, further ones as long as
 // they are within the errors of the last of those. A turn is a handful of instructions: each lane has
 // its best two at hand, and one that gives both away (2 % of rows at 8 of 384) looks through its keys
@@ -541,8 +532,8 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
     // slots of the same expert add up, in slot order
     float total = 0.0f;
     for (int k = 0; k < a.topk; ++k) {
-      const int ik = __shfl(id, k, 64);
-      const float gk = __shfl(g, k, 64);
+      const int ik = __builtin_amdgcn_readlane(id, k);
+      const float gk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), k));
       if (ik == id) total += gk;
     }
     for (int e = lane; e < a.E; e += 64) grad[e] = 0.0f;
