@@ -125,7 +125,7 @@ bool fp4_decode_fits(int64_t N, int groups) {
 
 // Its one launch saves the GEMM's routing (2.5 to 5 us) but reads weights less evenly, and an expert's
 // rows 16 at a time. Decode against route and GEMM in us, by slots and groups of 128 channels: 8 x 12
-// of 5,120 inputs 9.9 and 13.7; 512 x 1 23 and 25; 64 x 8 of 2,048 inputs 11.9 and 11.3; 64 x 12 over
+// of 5,120 inputs 9.3 and 13.7; 512 x 1 22 and 25; 64 x 8 of 2,048 inputs 11.9 and 11.3; 64 x 12 over
 // 384 experts 56 and 53, over 8 experts 12.2 and 14; 1,024 x 1 30 and 27; 128 x 12 99 and 90; 512 x 20
 // 46 and 32; 1,024 x 12 132 and 108. Two launches cost a call a little more than one.
 constexpr int64_t FP4_DECODE_PAIRS = 1024;

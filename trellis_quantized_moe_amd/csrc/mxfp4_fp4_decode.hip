@@ -6,16 +6,17 @@
 // for every slot, of which those of an expert's first slot work and the others leave at once. Each of
 // its waves looks through all route ids for the expert's slots, so every touched weight is read once
 // (per 16 rows). The four waves share out the inputs. Per window of 4 steps of 128 inputs a wave
-//   - has asked for the window's codes and scales of its channels one window ahead: lane (n, q)
+//   - has asked for the window's codes and scales of its channels one window ahead (two windows ahead
+//     were slower, one token 10.6 us instead of 9.3): lane (n, q)
 //     loads the 16 bytes of block q of a step of channel n, and 16 scale bytes (4 steps) of it;
 //   - converts the rows' inputs to MXFP4 (F29): lane p block p % 16 of row p / 16, loaded one
 //     conversion ahead, into LDS, from which lane (n, q) reads block q of row n;
 //   - multiplies: v_mfma_scale_f32_16x16x128_f8f6f4 per step and 16 channels.
 // The waves' sums are added in order, multiplied by the gate and written once.
 //
-// Bound by the weights' bytes where there are many (64 tokens x 8 of 384 experts, 128 x 5,120: 22.7 us
-// for about 98 MB), else by the latency of its dependent loads (one token, 1,536 x 5,120: 9.8 us; 128
-// x 5,120: 6.0). 32 channels a workgroup convert the rows half as often, 16 make twice as many
+// Bound by the weights' bytes where there are many (64 tokens x 8 of 384 experts, 128 x 5,120: 22.0 us
+// for about 98 MB), else by the latency of its dependent loads (one token, 1,536 x 5,120: 9.3 us; 128
+// x 5,120: 5.6). 32 channels a workgroup convert the rows half as often, 16 make twice as many
 // workgroups, which is faster until there are two for every compute unit (16 and 32 channels: one
 // token x 8 of 128 outputs 6.0 and 7.0 us, of 1,536 outputs 9.9 and 10.1; two tokens 17.0 and 14.3; 64
 // tokens x 8 of 128 outputs 25.4 and 22.7).
@@ -66,6 +67,14 @@ __global__ __launch_bounds__(64 * FD_WAVES) void fp4_decode_kernel(Fp4DecodeArgs
     }
     return;
   }
+  // 512 ids at a time, the first of them asked for together with this slot's
+  const GemmRsrc ri = gemm_rsrc(a.ids, 4u * (uint32_t)a.N);
+  uint32_t id[8];
+  auto load_ids = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) id[u] = __builtin_amdgcn_raw_buffer_load_b32(ri, 4 * (j0 + 64 * u + lane), 0, 0);
+  };
+  load_ids(0);
   const int e = by_expert ? row : __builtin_amdgcn_readfirstlane(a.ids[row]);
   if (e < 0 || e >= a.E) {  // an empty or invalid slot
     const float v = e == -1 ? 0.0f : __builtin_nanf("");
@@ -73,15 +82,13 @@ __global__ __launch_bounds__(64 * FD_WAVES) void fp4_decode_kernel(Fp4DecodeArgs
     if (e != -1 && tid == 0) set_status(a.status, STATUS_BAD_EXPERT);
     return;
   }
-  // the expert's slots, 512 ids asked for at a time; every wave writes the same list
-  const GemmRsrc ri = gemm_rsrc(a.ids, 4u * (uint32_t)a.N);
+  // the expert's slots; every wave writes the same list
   int cnt = 0, lead = -1;
   for (int j0 = 0; j0 < a.N; j0 += 512) {
-    uint32_t id[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) id[u] = __builtin_amdgcn_raw_buffer_load_b32(ri, 4 * (j0 + 64 * u + lane), 0, 0);
+    if (j0 > 0) load_ids(j0);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
+      if (j0 + 64 * u >= a.N) break;  // uniform
       const int j = j0 + 64 * u + lane;
       const bool hit = j < a.N && (int)id[u] == e;
       const uint64_t m = __ballot(hit);
@@ -159,7 +166,7 @@ __global__ __launch_bounds__(64 * FD_WAVES) void fp4_decode_kernel(Fp4DecodeArgs
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
       __builtin_amdgcn_wave_barrier();
       const Weights cur = b;
-      load_weights(b, k + FD_WINDOW);
+      if (k + FD_WINDOW < steps) load_weights(b, k + FD_WINDOW);
       const u32x4 sa = *reinterpret_cast<const u32x4*>(wscales + 16 * n);
 #pragma unroll
       for (int t = 0; t < FD_WINDOW; ++t) {
