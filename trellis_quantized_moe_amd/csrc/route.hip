@@ -67,10 +67,12 @@ __host__ __device__ inline int64_t beside_rank(const RouteArgs& a) { return a.qb
 // slot's rank among the wave's earlier slots of its expert comes from the wave's running count
 // in LDS. The block then turns the per-wave counts into per-wave bases (exclusive prefix over
 // the waves, in order), adds them, and writes its per-expert totals to hist.
+// BESIDE: with activations to convert in further blocks (as in the scans).
+template <bool BESIDE>
 __global__ __launch_bounds__(64 * RANK_WAVES) void route_rank_kernel(
     const int32_t* __restrict__ ids, int N, int E, int idbits, int32_t* __restrict__ rank,
     int32_t* __restrict__ hist, RouteArgs a) {
-  if ((int)blockIdx.x >= a.blocks) {
+  if (BESIDE && (int)blockIdx.x >= a.blocks) {
     quantize_beside(a, a.blocks, 0, beside_rank(a));
     return;
   }
@@ -347,8 +349,9 @@ __device__ __forceinline__ void hist_bases(__amdgpu_buffer_rsrc_t rh, int E, int
   }
 }
 
+template <bool BESIDE>
 __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
-  if (blockIdx.x > 0) {
+  if (BESIDE && blockIdx.x > 0) {
     quantize_beside(a, 1, beside_rank(a), a.qblocks);
     return;
   }
@@ -405,8 +408,9 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
 
 // The same with the items placed by token range (a.items set, a.split_rows > 0, a.E <=
 // 1024: one expert per thread).
+template <bool BESIDE>
 __global__ __launch_bounds__(1024) void route_scan_split_kernel(RouteArgs a) {
-  if (blockIdx.x > 0) {
+  if (BESIDE && blockIdx.x > 0) {
     quantize_beside(a, 1, beside_rank(a), a.qblocks);
     return;
   }
@@ -644,23 +648,28 @@ hipError_t launch_route_small(const RouteArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-  if (a.N == 0) return hipSuccess;
-  // the scan addresses hist with 32-bit byte offsets
-  if ((int64_t)a.blocks * a.E * 4 >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+template <bool BESIDE>
+static hipError_t launch_rank_and_scan(const RouteArgs& a, hipStream_t s) {
   int idbits = 1;
   while ((1 << idbits) < a.E) ++idbits;
   const int64_t early = beside_rank(a);
-  hipLaunchKernelGGL(route_rank_kernel, dim3(a.blocks + quantize_blocks(early, 64 * RANK_WAVES)),
+  hipLaunchKernelGGL(route_rank_kernel<BESIDE>, dim3(a.blocks + quantize_blocks(early, 64 * RANK_WAVES)),
                      dim3(64 * RANK_WAVES), 0, s, a.ids, (int)a.N, a.E, idbits, a.rank, a.hist, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const dim3 scan(1 + quantize_blocks(a.qblocks - early, 1024));
   if (a.items && a.split_rows > 0 && a.E <= 1024)
-    hipLaunchKernelGGL(route_scan_split_kernel, scan, dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(route_scan_split_kernel<BESIDE>, scan, dim3(1024), 0, s, a);
   else
-    hipLaunchKernelGGL(route_scan_kernel, scan, dim3(1024), 0, s, a);
-  err = hipGetLastError();
+    hipLaunchKernelGGL(route_scan_kernel<BESIDE>, scan, dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  if (a.N == 0) return hipSuccess;
+  // the scan addresses hist with 32-bit byte offsets
+  if ((int64_t)a.blocks * a.E * 4 >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  hipError_t err = a.qx ? launch_rank_and_scan<true>(a, s) : launch_rank_and_scan<false>(a, s);
   if (err != hipSuccess) return err;
   // (a launch may have 2^32 threads)
   const int64_t blocks = std::min<int64_t>((a.N + SCATTER_SLOTS - 1) / SCATTER_SLOTS, 1 << 20);
