@@ -207,7 +207,7 @@ __device__ __forceinline__ void f4_item(const Fp4GemmArgs& a, F4Shared<WAVES>& s
   // The epilogue: element 4 j + i of lane (n, h) is channel 8 j + 4 h + i of a block, of the block's
   // row n. Each wave brings its rows together in LDS (its own part of the stages, once no load
   // writes them any more) and writes them in pieces of 128 NB bytes: stored from the lanes as they
-  // are, 16 bytes of 32 rows at a time, the results of the largest case took 95 us of 352.
+  // are, 16 bytes of 32 rows at a time, the results of 8,192 tokens x 8 of 32, 1,536 x 5,120, took 95 us of 352.
   wait_vmcnt<0>();
   bare_barrier();
   constexpr int kLine = 128 * NB + 16;  // the 16 bytes more put a row's pieces on other banks
