@@ -5,7 +5,7 @@
 // lane. The wave
 //   1. looks for a NaN, or +inf under softmax, which makes a row of NaN weights;
 //   2. makes the keys of the choice: the logits themselves where no bias enters (a score grows
-//      with its logit), else score + bias in fp32, each off by less than KEY_ERROR;
+//      with its logit), else score + bias in fp32, with a bound of their errors;
 //   3. keeps the best groups: each group's lanes take its one or two best keys, a group's rank
 //      is the number of groups before it;
 //   4. takes the largest key topk times, and further ones within the errors of the last of those;
@@ -15,7 +15,8 @@
 //      lane computes its expert's key in 64 bits, where the definition lies, and the lanes change
 //      places. Where the last group kept is not ahead of the next by more than the errors, or more
 //      than 64 experts are candidates, steps 2 to 4 run once more in 64 bits throughout. (All rows
-//      in 64 bits took 29 us for 8,192 rows of 384, one wave alone 8.5.);
+//      in 64 bits took 29 us for 8,192 rows of 384, one wave alone 8.5; now 12.2, in 8 groups 16.6, of
+//      which one row that runs again takes up to 9; rows that all tie 88.);
 //   6. weighs: lane r computes its score from its logit in fp32, relative to the largest
 //      chosen one where they are renormalised, so that no sum of scores can underflow.
 // One row a wave: a chunk's rows fill the GPU eight times over, and a single row ends soonest.
@@ -89,14 +90,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 }
 // The largest value (no NaN among them).
 __device__ __forceinline__ float wave_max(float v) { return unordered(wave_max(ordered(v))); }
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const double o = __shfl_xor(v, d, 64);
-    v = o > v ? o : v;
-  }
-  return v;
-}
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
@@ -107,12 +100,19 @@ __device__ __forceinline__ double wave_sum(double v) {
 // where it is below 2^-126.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
-// How far a score in fp32 is off: the exponential's error, at most 2^-22 of a score and 2^-24 in
-// all from its argument (|x| e^-|x| stays below 0.37), a sum's 2^-21, the reciprocal's 2^-23; a
-// score is at most 1. The sum with a bias rounds by 2^-24 of itself. Two keys are told apart where
-// they differ by more than twice that (with a factor of two to spare).
-constexpr float KEY_ERROR = 0x1p-20f;
-__device__ __forceinline__ float key_gap(float v) { return 4.0f * KEY_ERROR + 0x1p-22f * fabsf(v); }
+// How far a score in fp32 is off, in units of 2^-24.
+// Sigmoid, 1 / (1 + e): e's relative error of 4 and 2 |x| counts by s (1 - s) <= 1/4 and s (1 - s) |x| <=
+// 0.23, the sum's rounding and the reciprocal are 1 and 2 of s: 4.5 in all.
+// Softmax, e^d / Z with d = x - top: the exponential 4 of s and 2.5 |d| (its argument rounds twice), of
+// which s |d| stays below 0.37; Z's exponentials 4 of it and 2.5 times the mean of |d|, which is at most
+// ln 4,096 = 8.4, and its PER + 6 sums 1 each; division and product 1 each: 1 + s (37 + PER), where s is
+// at most 1 / Z.
+template <int PER>
+__device__ __forceinline__ float softmax_error(float rz) { return 0x1p-24f * (1.0f + rz * (37 + PER)); }
+constexpr float SIGMOID_ERROR = 4.5f * 0x1p-24f;
+// The sum with a bias rounds by 2^-24 of itself. Two keys are told apart where they differ by more than
+// twice all that (with a factor of two to spare).
+__device__ __forceinline__ float key_gap(float v, float error) { return 4.0f * error + 0x1p-22f * fabsf(v); }
 
 // The best two of a set of keys, -inf where there are none.
 template <typename K>
@@ -138,7 +138,7 @@ struct Choice {
 // its best two at hand, and one that gives both away (2 % of rows at 8 of 384) looks through its keys
 // again for those behind the last one it gave.
 template <int PER>
-__device__ __forceinline__ Choice choose(const float (&value)[PER], int topk, bool near) {
+__device__ __forceinline__ Choice choose(const float (&value)[PER], int topk, bool near, float error) {
   const int lane = threadIdx.x & 63;
   const uint32_t none = ordered(NEG);
   uint32_t key[PER];
@@ -168,7 +168,7 @@ __device__ __forceinline__ Choice choose(const float (&value)[PER], int topk, bo
     count = r + 1;
     if (r == topk - 1 && near) {
       const float v = unordered(top);
-      limit = ordered(v - key_gap(v));
+      limit = ordered(v - key_gap(v, error));
     }
     const uint64_t m = __ballot(best == top);
     int winner = __builtin_ctzll(m);
@@ -279,11 +279,17 @@ __device__ __forceinline__ int choose64(const RouterArgs& a, const L* row, float
   }
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
-  uint64_t kept = ~0ull;
-  const int size = a.E / a.groups;
   if (a.groups > 1) {
     double gap;
-    kept = keep_groups<double>(a, keys, gap);
+    const uint64_t kept = keep_groups<double>(a, keys, gap);
+    const int size = a.E / a.groups;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      if (!((kept >> (e / size)) & 1))
+        keys[e] = NEG;
+      else if (!a.bias && keys[e] > NEG)
+        keys[e] = load_logit(row, e);
+    }
   }
   double last = -(double)NEG;  // the last key taken, and its expert
   int last_e = -1, mine = -1;
@@ -293,19 +299,22 @@ __device__ __forceinline__ int choose64(const RouterArgs& a, const L* row, float
     int be = 0x7FFFFFFF;
 #pragma unroll 1
     for (int e = lane; e < a.E; e += 64) {
-      if (a.groups > 1 && !((kept >> (e / size)) & 1)) continue;
-      double k = keys[e];
-      if (!a.bias && k > NEG) k = load_logit(row, e);
+      const double k = keys[e];
       if (k > best && (k < last || (k == last && e > last_e))) {
         best = k;
         be = e;
       }
     }
-    last = wave_max(best);
+    // the largest key as an integer of the same order, half by half, then its lowest index
+    const uint64_t u = __builtin_bit_cast(uint64_t, best + 0.0);
+    const uint64_t o = u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+    const uint32_t hi = wave_max((uint32_t)(o >> 32));
+    const bool tops = (uint32_t)(o >> 32) == hi;
+    const uint32_t lo = wave_max(tops ? (uint32_t)o : 0u);
+    const uint64_t top_o = (uint64_t)hi << 32 | lo;
+    last = __builtin_bit_cast(double, top_o ^ ((top_o >> 63) ? 1ull << 63 : ~0ull));
     if (!(last > NEG)) break;  // uniform
-    last_e = best == last ? be : 0x7FFFFFFF;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) last_e = min(last_e, __shfl_xor(last_e, d, 64));
+    last_e = (int)~wave_max(o == top_o ? ~(uint32_t)be : 0u);
     mine = lane == r ? last_e : mine;
   }
   __builtin_amdgcn_wave_barrier();
@@ -330,12 +339,13 @@ __device__ __forceinline__ int in_order(const RouterArgs& a, const L* row, float
 }
 
 // Steps 2 to 4 in fp32. nan: a key is NaN (the choice is then without meaning). sure: the groups that
-// stay are those of the exact keys.
+// stay are those of the exact keys. error: the scores' bound.
 template <int PER, bool SIGMOID, bool SCORED>
 __device__ __forceinline__ Choice pick(const RouterArgs& a, const float (&x)[PER], float top, float* keys,
-                                       bool near, bool& nan, bool& sure) {
+                                       bool near, bool& nan, bool& sure, float& error) {
   const int lane = threadIdx.x & 63;
   float key[PER];
+  error = SIGMOID ? SIGMOID_ERROR : 0.0f;
   if constexpr (SCORED) {
     float rz = 1.0f;
     if constexpr (!SIGMOID) {
@@ -343,6 +353,7 @@ __device__ __forceinline__ Choice pick(const RouterArgs& a, const float (&x)[PER
 #pragma unroll
       for (int j = 0; j < PER; ++j) s += fast_exp(x[j] - top);
       rz = 1.0f / wave_sum(s);
+      error = softmax_error<PER>(rz);
     }
     float bias[PER];
 #pragma unroll
@@ -385,10 +396,10 @@ __device__ __forceinline__ Choice pick(const RouterArgs& a, const float (&x)[PER
       const uint32_t g = (uint32_t)(((float)(64 * j + lane) + 0.5f) * inverse);
       if (!((kept >> (g & 63)) & 1) || 64 * j + lane >= a.E) key[j] = NEG;
     }
-    if (SCORED && a.group_topk < a.groups) sure = gap > 3.0f * key_gap(wave_max(most));
+    if (SCORED && a.group_topk < a.groups) sure = gap > 3.0f * key_gap(wave_max(most), error);
     __builtin_amdgcn_wave_barrier();
   }
-  return choose<PER>(key, a.topk, near);
+  return choose<PER>(key, a.topk, near, error);
 }
 
 // SCORED: scores enter the choice (a bias, or groups by two scores); else it goes by the logits.
@@ -420,7 +431,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_kernel(RouterAr
       double* keys = row_keys + (size_t)w * a.E;
       const bool near = SCORED && a.bias;
       bool sure;
-      const Choice c = pick<PER, SIGMOID, SCORED>(a, x, top, reinterpret_cast<float*>(keys), near, bad, sure);
+      float error;
+      const Choice c =
+          pick<PER, SIGMOID, SCORED>(a, x, top, reinterpret_cast<float*>(keys), near, bad, sure, error);
       mine = c.e;
       if constexpr (SCORED) {
         bool again = false;
@@ -429,7 +442,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_kernel(RouterAr
           const float below = __shfl_down(c.key, 1, 64);
           const float xe = mine >= 0 ? load_logit(row, mine) : 0.0f, be = mine >= 0 ? a.bias[mine] : 0.0f;
           const float xn = __shfl_down(xe, 1, 64), bn = __shfl_down(be, 1, 64);
-          const bool apart = lane + 1 >= c.count || c.key - below > key_gap(c.key) || (xe == xn && be == bn);
+          const bool apart = lane + 1 >= c.count || c.key - below > key_gap(c.key, error) || (xe == xn && be == bn);
           again = c.count > a.topk || __ballot(!apart) != 0;
         }
         if (!bad) {
