@@ -105,10 +105,25 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // 0.23, the sum's rounding and the reciprocal are 1 and 2 of s: 4.5 in all.
 // Softmax, e^d / Z with d = x - top: the exponential 4 of s and 2.5 |d| (its argument rounds twice), of
 // which s |d| stays below 0.37; Z's exponentials 4 of it and 2.5 times the mean of |d|, which is at most
-// ln 4,096 = 8.4, and its PER + 6 sums 1 each; division and product 1 each: 1 + s (37 + PER), where s is
-// at most 1 / Z.
+// ln 4,096 = 8.4, and its sums 1 each, those of a lane and 6; division and product 1 each: 1 + s (37 +
+// the lane's), where s is at most 1 / Z.
 template <int PER>
-__device__ __forceinline__ float softmax_error(float rz) { return 0x1p-24f * (1.0f + rz * (37 + PER)); }
+__device__ __forceinline__ float softmax_error(float rz) {
+  return 0x1p-24f * (1.0f + rz * (37 + (PER > 8 ? 8 + PER / 8 : PER)));
+}
+// The sum of a lane's terms, in runs of 8.
+template <int PER, typename F>
+__device__ __forceinline__ float lane_sum(F term) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; i += 8) {
+    float run = 0.0f;
+#pragma unroll
+    for (int j = i; j < i + 8 && j < PER; ++j) run += term(j);
+    sum += run;
+  }
+  return sum;
+}
 constexpr float SIGMOID_ERROR = 4.5f * 0x1p-24f;
 // The sum with a bias rounds by 2^-24 of itself. Two keys are told apart where they differ by more than
 // twice all that (with a factor of two to spare).
@@ -349,10 +364,7 @@ __device__ __forceinline__ Choice pick(const RouterArgs& a, const float (&x)[PER
   if constexpr (SCORED) {
     float rz = 1.0f;
     if constexpr (!SIGMOID) {
-      float s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) s += fast_exp(x[j] - top);
-      rz = 1.0f / wave_sum(s);
+      rz = 1.0f / wave_sum(lane_sum<PER>([&](int j) { return fast_exp(x[j] - top); }));
       error = softmax_error<PER>(rz);
     }
     float bias[PER];
@@ -468,10 +480,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_kernel(RouterAr
     if (a.renorm) {
       sum = wave_sum(weight);
     } else if constexpr (!SIGMOID) {
-      sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) sum += fast_exp(x[j] - top);
-      sum = wave_sum(sum);
+      sum = wave_sum(lane_sum<PER>([&](int j) { return fast_exp(x[j] - top); }));
     }
     if (lane < a.topk) {
       weight = mine >= 0 ? a.scale * (weight / sum) : 0.0f;
@@ -510,13 +519,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
         top = fmaxf(top, x[j]);
       }
       top = wave_max(top);
-      float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        x[j] = top > NEG ? fast_exp(x[j] - top) : 0.0f;
-        s += x[j];
-      }
-      rz = 1.0f / wave_sum(s);
+      for (int j = 0; j < PER; ++j) x[j] = top > NEG ? fast_exp(x[j] - top) : 0.0f;
+      rz = 1.0f / wave_sum(lane_sum<PER>([&](int j) { return x[j]; }));
     }
     // g: the gradient of the slot's score times the score, or (dense) the gradient alone
     float g = 0.0f, c = 0.0f;
