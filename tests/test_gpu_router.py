@@ -375,3 +375,15 @@ def test_offsets_past_32_bits():
     want = torch.tensor([r * (1 - r), -r * (1 - r)])
     assert torch.allclose(x[-1, [4000, 17]].float().cpu(), want, rtol=BF16 * 1.01, atol=0)
     assert x[:-1].abs().max().item() == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (4, 1), (4, 2)])
+def test_huge_and_infinite_biases(score, groups, group_top):
+    """Keys that round together (a bias far above every score), infinite ones, and none at all."""
+    x = logits_for(391, 40, 64, torch.float32)
+    for values in ([float("inf")], [1e30, -1e30], [float("inf"), float("-inf"), 3e38, -3e38, 0.0], [65536.0]):
+        bias = torch.tensor([values[(5 * e) % len(values)] for e in range(64)], dtype=torch.float32)
+        for some in (1, 3):
+            b = torch.where(torch.arange(64) % some == 0, bias, torch.zeros(64))
+            check_route(x, topk=6, score=score, bias=b, groups=groups, group_topk=max(1, groups // 2), group_top=group_top)
