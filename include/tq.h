@@ -332,9 +332,10 @@ typedef struct tq_router {
  *   the group_topk groups of the largest scores stay; topk_ids[t]: the topk largest c in them,
  *   in descending order; equal ones, of groups too, by the lowest index;
  *   topk_w[t][k] = scale * s_k / (renorm ? sum over the chosen j of s_j : 1).
- * The choice is that of the scores in 64 bits (without a bias, that of the logits themselves,
- * which order where scores round together). Weights are fp32, off by less than 2^-18 of themselves,
- * and 2^-22 times how far the logit lies below the row's largest (2^-23 in all where measured).
+ * The choice is that of the scores in 64 bits. Without a bias it is that of the logits themselves,
+ * which order where scores round together, of groups by their largest too; sums of two are of
+ * scores. Weights are fp32, off by less than 2^-18 of themselves, and 2^-22 times how far the
+ * logit lies below the row's largest (2^-23 in all where measured).
  *   R         host: the router.
  *   logits    device [T][R->E]: fp32, or bf16 with TQ_LOGITS_BF16; aligned to an element.
  *   T         tokens (0 is a successful no-op); T * E at most 2^33.

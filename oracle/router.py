@@ -37,15 +37,16 @@ def route_row(x, topk, score="softmax", bias=None, groups=1, group_topk=1, group
     if undefined:
         return np.arange(topk), np.full(topk, math.nan)
     open_ = [e for e in range(E) if x[e] > -math.inf and b[e] > -math.inf]
+    key = x if bias is None else c  # logits order also where scores round together
     if groups > 1:
         size = E // groups
+        part = key if group_top == 1 else c
         totals = []
         for g in range(groups):
-            best = sorted((c[e] for e in open_ if e // size == g), reverse=True)[:group_top]
+            best = sorted((part[e] for e in open_ if e // size == g), reverse=True)[:group_top]
             totals.append((-sum(best), g) if best else (math.inf, g))
         kept = {g for _, g in sorted(totals)[:group_topk]}
         open_ = [e for e in open_ if e // size in kept]
-    key = x if bias is None else c
     ids = [e for _, e in sorted((-key[e], e) for e in open_)][:topk]
     if renorm and ids:
         # relative to the largest chosen logit: exact where the scores themselves underflow

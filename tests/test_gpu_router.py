@@ -387,3 +387,20 @@ def test_huge_and_infinite_biases(score, groups, group_top):
         for some in (1, 3):
             b = torch.where(torch.arange(64) % some == 0, bias, torch.zeros(64))
             check_route(x, topk=6, score=score, bias=b, groups=groups, group_topk=max(1, groups // 2), group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_groups_whose_scores_round_together(score, group_top):
+    """Logits whose scores are equal in 64 bits (all 1, or all 0), in groups: by one score the groups go
+    by their logits, by two they tie."""
+    rng = np.random.default_rng(400)
+    x = np.empty((30, 96), dtype=np.float32)
+    x[:] = rng.permuted(np.tile(np.arange(96, dtype=np.float32), (30, 1)), axis=1)
+    x = x + 40 if score == "sigmoid" else -900 - x  # one expert of softmax has the whole of it
+    if score == "softmax":
+        x[:, 50] = 0.0
+    for groups, group_topk in ((2, 1), (8, 3), (24, 5)):
+        for renorm in (True, False):
+            check_route(torch.from_numpy(x), topk=4, score=score, groups=groups, group_topk=group_topk, group_top=group_top,
+                        renorm=renorm)

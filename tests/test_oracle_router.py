@@ -72,3 +72,16 @@ def test_gradient_against_central_differences(score, renorm):
         h[t, e] = 1e-5
         # the error of a central difference: h^2 / 6 of a third derivative of order 10
         assert abs((loss(x + h) - loss(x - h)) / 2e-5 - got[t, e]) < 1e-8
+
+
+@pytest.mark.parametrize("score,x", [("sigmoid", [40.0, 39.0, 60.0, 59.0]), ("softmax", [0.0, -900.0, -950.0, -901.0, -890.0, -960.0])])
+def test_groups_whose_scores_round_together(score, x):
+    """1 / (1 + e^-40) and 1 / (1 + e^-60) are 1 in 64 bits, e^-890 is 0: without a bias and by one score the
+    groups go by their logits, as the experts do; sums of two scores tie, and go by the lowest index."""
+    n = len(x) // 2
+    order = sorted(range(n), key=lambda g: -max(x[2 * g:2 * g + 2]))
+    for keep in range(1, n):
+        ids, _ = oracle.route_row(x, 2 * keep, score=score, groups=n, group_topk=keep)
+        assert {e // 2 for e in ids} == set(order[:keep])
+        ids, _ = oracle.route_row(x, 2 * keep, score=score, groups=n, group_topk=keep, group_top=2)
+        assert {e // 2 for e in ids} == set(range(keep))
