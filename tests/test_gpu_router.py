@@ -404,3 +404,18 @@ def test_groups_whose_scores_round_together(score, group_top):
         for renorm in (True, False):
             check_route(torch.from_numpy(x), topk=4, score=score, groups=groups, group_topk=group_topk, group_top=group_top,
                         renorm=renorm)
+
+
+@pytest.mark.parametrize("E", [1, 5, 8, 33, 63, 65, 100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_an_infinite_bias_closes_the_choice(E, score):
+    """The last key chosen is +inf: no lane past the last expert takes part, and equal ones go by index."""
+    x = logits_for(401, 9, E, torch.float32)
+    for many in sorted({1, min(3, E), E}):
+        b = torch.zeros(E)
+        b[torch.arange(many) * E // many] = float("inf")
+        b[E // 2] = -1e30 if many < E else b[E // 2]
+        for topk in sorted({1, min(2, E), min(many, 64), min(many + 1, E, 64)}):
+            check_route(x, topk=topk, score=score, bias=b)
+            if E % 5 == 0 and topk <= E // 5 * 2:
+                check_route(x, topk=topk, score=score, bias=b, groups=5, group_topk=2, group_top=2)

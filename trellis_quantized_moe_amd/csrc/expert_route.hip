@@ -182,8 +182,10 @@ __device__ __forceinline__ Choice choose(const float (&value)[PER], int topk, bo
     }
     count = r + 1;
     if (r == topk - 1 && near) {
+      // (an infinite key has no error, and less an infinite gap it would be a NaN, whose sign bit makes
+      // it less than no key at all: lanes past the last expert would be chosen)
       const float v = unordered(top);
-      limit = ordered(v - key_gap(v, error));
+      limit = ordered(v < -NEG ? v - key_gap(v, error) : v);
     }
     const uint64_t m = __ballot(best == top);
     int winner = __builtin_ctzll(m);
