@@ -419,3 +419,24 @@ def test_an_infinite_bias_closes_the_choice(E, score):
             check_route(x, topk=topk, score=score, bias=b)
             if E % 5 == 0 and topk <= E // 5 * 2:
                 check_route(x, topk=topk, score=score, bias=b, groups=5, group_topk=2, group_top=2)
+
+
+@pytest.mark.parametrize("group_topk", [1, 2, 3])
+@pytest.mark.parametrize("big", [3e38, 1.7014118e38, 1.8e38])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_sums_of_two_keys_past_fp32(score, big, group_topk):
+    """Finite biases whose sums are beyond fp32, in groups before and behind ones without experts."""
+    x = logits_for(410, 20, 16, torch.float32)
+    low = float(torch.finfo(torch.float32).min)
+    lists = [[0.0, -big, -0.9 * big, -0.99 * big], [0.0, big, 0.9 * big, 0.99 * big],
+             [-big, -0.99 * big, low, 0.0], [0.0, low, -0.97 * big, low], [low] * 4]
+    for values in lists:
+        b = torch.tensor(values, dtype=torch.float32).repeat_interleave(4)
+        check_route(x, topk=4, score=score, bias=b, groups=4, group_topk=group_topk, group_top=2)
+        y = x.clone()
+        y[:, :4] = -float("inf")  # a group without experts before one masked by the lowest value
+        check_route(y, topk=4, score=score, bias=b, groups=4, group_topk=group_topk, group_top=2)
+        y[::2, 4:8] = -float("inf")
+        check_route(y, topk=4, score=score, bias=b, groups=4, group_topk=group_topk, group_top=2)
+        b[9] = -float("inf")
+        check_route(y, topk=4, score=score, bias=b, groups=4, group_topk=group_topk, group_top=2)

@@ -251,6 +251,9 @@ __device__ __forceinline__ uint64_t keep_groups(const RouterArgs& a, const K* ke
     const int next = __builtin_ctzll(__ballot(leads && rank == a.group_topk));
     const K dropped = __shfl(score, next, 64);
     if (dropped > none) gap = __shfl(score, last, 64) - dropped;
+    // a group with experts whose sum is infinite (two biases beyond half of fp32's range): by it the group
+    // ties with others, or with those that have no expert
+    if (__ballot(leads && t.a > none && !(score > none && score < -none))) gap = none;
   }
   const uint64_t m = __ballot(leads && rank < a.group_topk);
   uint64_t kept = 0;  // bit g: lane g * per of m
