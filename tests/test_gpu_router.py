@@ -440,3 +440,51 @@ def test_sums_of_two_keys_past_fp32(score, big, group_topk):
         check_route(y, topk=4, score=score, bias=b, groups=4, group_topk=group_topk, group_top=2)
         b[9] = -float("inf")
         check_route(y, topk=4, score=score, bias=b, groups=4, group_topk=group_topk, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_masked_expert_costs_no_certainty(score):
+    """One expert taken out by its bias leaves the groups as sure as before: a chunk is not chosen in 64
+    bits throughout (twice the time), which the largest magnitude among all keys had asked for. The least
+    times of calls in turn, sixteen at a time."""
+    o = ops()
+    T, E = 8192, 384
+    x = logits_for(420, T, E, torch.float32).to(dev())
+    routers = []
+    for value in (None, -float("inf"), -1e9, torch.finfo(torch.float32).min):
+        b = bias_for(1, E)
+        if value is not None:
+            b[100] = value
+        routers.append(o.Router(E, 8, score=score, bias=b.to(dev()), groups=8, group_topk=4, group_top=2))
+    ids, w = o.expert_route(routers[0], x)
+    best = [1e9] * len(routers)
+    for _ in range(20):
+        for i, R in enumerate(routers):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            torch.cuda.synchronize()
+            o.expert_route(R, x, ids=ids, w=w)
+            e[0].record()
+            for _ in range(16):
+                o.expert_route(R, x, ids=ids, w=w)
+            e[1].record()
+            torch.cuda.synchronize()
+            best[i] = min(best[i], e[0].elapsed_time(e[1]) / 16 * 1e3)
+    print(" ".join("%.1f" % t for t in best))
+    assert max(best[1:]) <= 1.4 * best[0], best
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("value", [-float("inf"), -1e9, -65536.0, 1e9])
+def test_masked_experts_in_groups(score, group_top, value):
+    """Some experts of every group, whole groups, and all but one expert of a group masked by the bias."""
+    x = logits_for(430, 40, 96, torch.float32)
+    b = bias_for(7, 96)
+    b[::7] = value
+    for groups in (4, 8, 32):
+        size = 96 // groups
+        for m in (b, torch.where(torch.arange(96) // size == 1, torch.full((96,), value), b),
+                  torch.where((torch.arange(96) // size == 2) & (torch.arange(96) % size > 0), torch.full((96,), value), b)):
+            for group_topk in (1, groups // 2, groups - 1):
+                check_route(x, topk=min(6, size * group_topk), score=score, bias=m, groups=groups, group_topk=group_topk,
+                            group_top=group_top)

@@ -25,6 +25,7 @@
 // renormalised, and under sigmoid, only chosen logits have a gradient: the row is zeros in LDS
 // into which the lanes write theirs. Softmax without it has one for every logit.
 #include <algorithm>
+#include <type_traits>
 
 #include "tq_device.h"
 #include "tq_internal.h"
@@ -219,10 +220,12 @@ __device__ __forceinline__ Choice choose(const float (&value)[PER], int topk, bo
   return Choice{e, unordered(mine), count, more};
 }
 
-// The groups that stay, as bits. keys: this wave's LDS, E entries holding the row's keys of the
-// group scores. gap: how far the last group kept is ahead of the next (+inf if none is dropped).
+// The groups that stay, as bits. keys: this wave's LDS, E entries holding the row's keys of the group
+// scores. sure (of fp32 keys): the groups are those of the exact keys. A key plus or minus its error's
+// bound orders as the keys do, so the exact best two of a group lie within the bounds of its best two
+// here, and no other key counts: an expert out of service costs no certainty.
 template <typename K>
-__device__ __forceinline__ uint64_t keep_groups(const RouterArgs& a, const K* keys, K& gap) {
+__device__ __forceinline__ uint64_t keep_groups(const RouterArgs& a, const K* keys, float error, bool& sure) {
   const int lane = threadIdx.x & 63;
   const int size = a.E / a.groups;
   int per = 64;  // lanes per group: the largest power of two with groups * per <= 64
@@ -237,25 +240,26 @@ __device__ __forceinline__ uint64_t keep_groups(const RouterArgs& a, const K* ke
     t.add(oa);
     t.add(ob);
   }
-  K score = t.a;
-  if (a.group_top == 2 && t.b > none) score += t.b;
+  const bool two = a.group_top == 2 && t.b > none;
+  const K score = two ? t.a + t.b : t.a;
   int rank = 0;
   for (int h = 0; h < a.groups; ++h) {
     const K o = __shfl(score, h * per, 64);
     rank += o > score || (o == score && h < g);
   }
   const bool leads = g < a.groups && sub == 0;
-  gap = -none;
-  if (a.group_topk < a.groups) {
-    const int last = __builtin_ctzll(__ballot(leads && rank == a.group_topk - 1));
-    const int next = __builtin_ctzll(__ballot(leads && rank == a.group_topk));
-    const K dropped = __shfl(score, next, 64);
-    if (dropped > none) gap = __shfl(score, last, 64) - dropped;
-    // a group with experts whose sum is infinite (two biases beyond half of fp32's range): by it the group
-    // ties with others, or with those that have no expert
-    if (__ballot(leads && t.a > none && !(score > none && score < -none))) gap = none;
+  const bool stays = leads && rank < a.group_topk;
+  if constexpr (std::is_same<K, float>::value) {
+    // the least that a group which stays can have, the most that one with experts which goes can have;
+    // of an infinite score (two biases beyond half of fp32's range, or no expert) nothing is known
+    const float off = key_gap(t.a, error) + (two ? key_gap(t.b, error) : 0.0f);
+    const bool known = fabsf(score) < -NEG;
+    const bool goes = leads && !stays && t.a > none;
+    const float least = -wave_max(stays ? (known ? off - score : -NEG) : NEG);
+    const float most = wave_max(goes ? (known ? score + off : -NEG) : NEG);
+    sure = __ballot(goes) == 0 || least > most;
   }
-  const uint64_t m = __ballot(leads && rank < a.group_topk);
+  const uint64_t m = __ballot(stays);
   uint64_t kept = 0;  // bit g: lane g * per of m
   for (int h = 0; h < a.groups; ++h) kept |= ((m >> (h * per)) & 1ull) << h;
   return kept;
@@ -300,8 +304,8 @@ __device__ __forceinline__ int choose64(const RouterArgs& a, const L* row, float
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
   if (a.groups > 1) {
-    double gap;
-    const uint64_t kept = keep_groups<double>(a, keys, gap);
+    bool sure;
+    const uint64_t kept = keep_groups<double>(a, keys, 0.0f, sure);
     const int size = a.E / a.groups;
 #pragma unroll 1
     for (int e = lane; e < a.E; e += 64) {
@@ -400,20 +404,17 @@ __device__ __forceinline__ Choice pick(const RouterArgs& a, const float (&x)[PER
       if (64 * j + lane < a.E) keys[64 * j + lane] = key[j];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
-    float gap;
-    const uint64_t kept = keep_groups<float>(a, keys, gap);
+    const uint64_t kept = keep_groups<float>(a, keys, error, sure);
+    if (!SCORED) sure = true;  // logits have no error
     const float inverse = 1.0f / (float)(a.E / a.groups);
-    float most = 0.0f;  // the largest magnitude of a key, which bounds the errors of the groups' scores
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      if (SCORED && x[j] > NEG) most = fmaxf(most, fabsf(key[j]));
       if (SCORED && !a.bias) key[j] = x[j];
       // the group of e: e and the size are at most 2^12, so that (e + 1/2) / size falls on the right
       // side of every whole number
       const uint32_t g = (uint32_t)(((float)(64 * j + lane) + 0.5f) * inverse);
       if (!((kept >> (g & 63)) & 1) || 64 * j + lane >= a.E) key[j] = NEG;
     }
-    if (SCORED && a.group_topk < a.groups) sure = gap > 3.0f * key_gap(wave_max(most), error);
     __builtin_amdgcn_wave_barrier();
   }
   return choose<PER>(key, a.topk, near, error);
