@@ -356,11 +356,12 @@ int expert_route(const tq_router* R, const void* logits, int64_t T, int32_t* top
  *   renorm:  r_k = s_k / sum_j s_j,  g_k = scale * (dw_k - sum_j r_j dw_j) / sum_j s_j
  *   else     g_k = scale * dw_k;     G_e = the sum of g_k over the slots k with id e
  *   sigmoid: dlogits_e = G_e s_e (1 - s_e);  softmax: dlogits_e = s_e (G_e - sum_k s_k g_k)
- * computed in fp32, rounded once to the logits' type. Logits that no slot chose get exactly 0,
- * except under softmax without renorm.
+ * computed in fp32, rounded once to the logits' type. Logits that no slot chose get exactly 0 and
+ * are not looked at (a NaN among them makes expert_route's weights NaN, but not these gradients),
+ * except under softmax without renorm, where a NaN or +inf makes its row NaN.
  *   topk_ids  device int32 [T][topk]: expert_route's; -1 is an empty slot (its dw is not read);
  *             an expert that is named twice gets both slots' gradients. An id outside [-1, E)
- *             makes its row NaN.
+ *             makes its row NaN. A row of -1 alone is 0, whatever its logits.
  *   dw        device fp32 [T][topk].
  *   dlogits   device [T][E], of the logits' type; every entry is written. It may be the logits
  *             themselves.

@@ -70,7 +70,8 @@ def expert_route(x, topk, **kw):
 
 
 def expert_route_backward(x, ids, dw, score="softmax", renorm=True, scale=1.0, **_):
-    """dlogits [T, E] of the weights of the slots `ids`, the choice held fixed."""
+    """dlogits [T, E] of the weights of the slots `ids`, the choice held fixed. Weights that are
+    renormalised, and sigmoid's, are functions of the slots' logits alone, whatever the others are."""
     x, dw = np.asarray(x, dtype=np.float64), np.asarray(dw, dtype=np.float64)
     out = np.zeros_like(x)
     for t in range(len(x)):
@@ -78,18 +79,24 @@ def expert_route_backward(x, ids, dw, score="softmax", renorm=True, scale=1.0, *
         if not slots:
             continue
         e = [int(ids[t][k]) for k in slots]
-        s = router_scores(x[t], score)
         g = scale * dw[t][slots]
-        if renorm:
-            total = np.sum(s[e])
-            g = (g - np.sum(s[e] / total * g)) / total
-        G = np.zeros(x.shape[1])
-        for j, k in zip(e, g):
-            G[j] += k
-        if score == "sigmoid":
-            out[t] = G * s * (1.0 / (1.0 + np.exp(np.minimum(x[t], 700.0))))
-        else:
+        if score == "softmax" and not renorm:
+            with np.errstate(invalid="ignore"):
+                s = router_scores(x[t], score)
+            G = np.zeros(x.shape[1])
+            np.add.at(G, e, g)
             out[t] = s * (G - np.sum(s * G))
-            if renorm:  # the sum is 0: only chosen logits have a gradient
-                out[t][[j for j in range(x.shape[1]) if j not in e]] = 0.0
+            continue
+        v = x[t][e]
+        with np.errstate(invalid="ignore"):
+            if score == "softmax":
+                r, other = np.exp(v - np.max(v)), 1.0
+            else:
+                top = min(np.max(v), 0.0) if renorm and np.max(v) > -math.inf else 0.0
+                r = np.exp(np.minimum(v, 0.0) - top) / (1.0 + np.exp(-np.abs(v)))
+                other = 1.0 / (1.0 + np.exp(np.minimum(v, 700.0)))  # 1 - s
+            if renorm:
+                r = r / np.sum(r)
+                g = g - np.sum(r * g)
+            np.add.at(out[t], e, r * g * other)
     return out

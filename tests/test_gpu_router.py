@@ -488,3 +488,41 @@ def test_masked_experts_in_groups(score, group_top, value):
             for group_topk in (1, groups // 2, groups - 1):
                 check_route(x, topk=min(6, size * group_topk), score=score, bias=m, groups=groups, group_topk=group_topk,
                             group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [16, 65, 400, 1100])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_of_undefined_rows(score, renorm, E, dtype):
+    """NaN and infinities at experts that slots name and at ones that none does, among -inf alone, and in
+    rows without slots; the gradients may replace the logits."""
+    inf, nan = float("inf"), float("nan")
+    x = logits_for(440, 13, E, dtype)
+    x[1, E - 1], x[2, 0], x[3, E - 1], x[4, 1], x[5, E - 1] = nan, nan, inf, inf, -inf
+    x[6] = -inf
+    x[6, E - 2] = nan
+    x[7], x[8], x[9] = nan, inf, -inf
+    x[10, 5] = nan
+    x[11] = -inf
+    x[11, 0] = nan
+    ids = torch.tensor([[0, 1, 2]] * 13, dtype=torch.int32)
+    ids[9:11] = -1
+    ids[12] = torch.tensor([2, -1, 2])
+    kw = dict(topk=3, score=score, renorm=renorm, scale=1.5)
+    R = router_of(E, kw)
+    dw = torch.from_numpy(np.random.default_rng(9).standard_normal((13, 3)).astype(np.float32))
+    want = oracle.expert_route_backward(f64(x), ids.numpy(), f64(dw), **options(kw))
+    for target in (None, x.to(dev())):
+        z = x.to(dev()) if target is None else target
+        got = f64(ops().expert_route_backward(R, z, ids.to(dev()), dw.to(dev()), dlogits=target))
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        assert np.all(got[9:11] == 0)
+    rows = torch.from_numpy(~np.isnan(want).any(1))
+    rows[8] = False  # (infinities: no distance from a largest logit)
+    if renorm or score == "sigmoid":
+        assert rows[[0, 1, 3, 5, 9, 10, 12]].all()
+        x = torch.where(torch.isfinite(x), x, torch.zeros_like(x))  # logits that no slot of these rows names
+    else:
+        rows[9:11] = False
+    check_backward(R, x[rows], ids[rows].to(dev()), 10, **kw)

@@ -85,3 +85,23 @@ def test_groups_whose_scores_round_together(score, x):
         assert {e // 2 for e in ids} == set(order[:keep])
         ids, _ = oracle.route_row(x, 2 * keep, score=score, groups=n, group_topk=keep, group_top=2)
         assert {e // 2 for e in ids} == set(range(keep))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradients_of_undefined_rows(score, renorm):
+    """Logits that no slot names count under softmax without renorm alone."""
+    x = np.zeros((6, 6))
+    x[0, 4], x[1, 4], x[2, 4], x[3, 4], x[5, 1] = math.nan, math.inf, math.nan, -math.inf, math.nan
+    ids = np.array([[0, 1], [0, 1], [-1, -1], [0, 1], [0, 1], [0, 1]])
+    dw = np.array([[1.0, 3.0]] * 6)
+    got = oracle.expert_route_backward(x, ids, dw, score=score, renorm=renorm)
+    assert np.all(got[2] == 0) and np.all(np.isfinite(got[3:5]))
+    if score == "softmax" and not renorm:
+        assert np.all(np.isnan(got[[0, 1, 5]]))
+    else:
+        assert np.array_equal(got[0], got[4]) and np.array_equal(got[1], got[4])
+        assert np.isnan(got[5, 1]) and np.all(got[5, 2:] == 0)
+        # softmax and sigmoid of two equal logits, 1/2 each
+        want = [-0.5, 0.5] if score == "softmax" else [-0.25, 0.25] if renorm else [0.25, 0.75]
+        assert np.allclose(got[4, :2], want) and np.all(got[4, 2:] == 0)

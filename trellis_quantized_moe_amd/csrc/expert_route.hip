@@ -22,8 +22,10 @@
 // One row a wave: a chunk's rows fill the GPU eight times over, and a single row ends soonest.
 //
 // expert_route_backward: one wave per token; lane r holds slot r. Where the weights are
-// renormalised, and under sigmoid, only chosen logits have a gradient: the row is zeros in LDS
-// into which the lanes write theirs. Softmax without it has one for every logit.
+// renormalised, and under sigmoid, the weights are functions of the chosen logits alone: no other
+// is read (reading all of them, to find a NaN among those not chosen, made 8,192 rows of 384 in bf16
+// take 8.1 us instead of 6.0), and the row is zeros in LDS into which the lanes write their gradients.
+// Softmax without it has one for every logit.
 #include <algorithm>
 #include <type_traits>
 
@@ -511,6 +513,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
     int id = lane < a.topk ? a.chosen[t * a.topk + lane] : -1;
     const bool bad = __ballot(id < -1 || id >= a.E) != 0;
     if (bad) id = -1;
+    const bool some = __ballot(id >= 0) != 0;
     const float dw = id >= 0 ? a.dw[t * a.topk + lane] : 0.0f;
     const float xs = id >= 0 ? load_logit(row, id) : NEG;
     const float most = wave_max(xs);
@@ -525,9 +528,12 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
         top = fmaxf(top, x[j]);
       }
       top = wave_max(top);
+      top = top > NEG ? top : 0.0f;
+      // a NaN, or an infinity's, reaches the sum and so the whole row, also where all others are -inf
 #pragma unroll
-      for (int j = 0; j < PER; ++j) x[j] = top > NEG ? fast_exp(x[j] - top) : 0.0f;
-      rz = 1.0f / wave_sum(lane_sum<PER>([&](int j) { return x[j]; }));
+      for (int j = 0; j < PER; ++j) x[j] = fast_exp(x[j] - top);
+      const float sum = wave_sum(lane_sum<PER>([&](int j) { return x[j]; }));
+      rz = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row without experts has only scores of 0
     }
     // g: the gradient of the slot's score times the score, or (dense) the gradient alone
     float g = 0.0f, c = 0.0f;
@@ -571,7 +577,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void expert_route_backward_kernel
       const int e = 64 * j + lane;
       if (e < a.E) {
         float v = grad[e];
-        if (dense) v = top > NEG ? x[j] * rz * (v - c) : 0.0f;
+        if (dense) v = some ? x[j] * rz * (v - c) : 0.0f;
         store_grad(dst, t * a.E + e, bad ? __builtin_nanf("") : v);
       }
     }
