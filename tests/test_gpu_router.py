@@ -526,3 +526,61 @@ def test_gradients_of_undefined_rows(score, renorm, E, dtype):
     else:
         rows[9:11] = False
     check_backward(R, x[rows], ids[rows].to(dev()), 10, **kw)
+
+
+def near_ties(score, E, T, shape, spread, seed):
+    """Logits [T, E] and a bias that takes back the score of a base row, so that the keys of rows which
+    repeat it up to a few steps of fp32 are 0.75 up to about `spread` and the bias's rounding, 2^-25.
+    shape: scores that are alike (flat: a sum of softmax near E), of one or two dominant experts (a sum
+    near 1), or spread as logits are."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal(E).astype(np.float32)
+    if shape == "flat":
+        x *= np.float32(2.0 ** -6)
+    if shape == "dominant":
+        x[E // 3] += np.float32(12.0)
+        x[E // 2] += np.float32(11.0)
+    s = oracle.router_scores(x, score)
+    b = (0.75 - s + spread * rng.standard_normal(E)).astype(np.float32)
+    rows = np.tile(x, (T, 1)) + np.float32(2.0 ** -22) * rng.integers(-1, 2, (T, E)).astype(np.float32)
+    return torch.from_numpy(rows), torch.from_numpy(b)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [60, 64, 384, 1000, 4096])
+@pytest.mark.parametrize("shape", ["flat", "dominant", "normal"])
+@pytest.mark.parametrize("spread", [0.0, 2.0 ** -24, 2.0 ** -21])
+def test_keys_within_the_errors_of_each_other(score, E, shape, spread):
+    """All keys within some steps of fp32 of each other (more than 64 of them where E is larger), and a
+    spread at which some are told apart; without groups and in groups by one and two."""
+    rows, b = near_ties(score, E, 12, shape, spread, E)
+    assert np.ptp(oracle.router_scores(f64(rows)[0], score) + f64(b)) < 2.0 ** -22 + 12 * spread
+    for topk in (1, 8):
+        check_route(rows, topk=topk, score=score, bias=b)
+    for groups in (4, 20):
+        if E % groups == 0:
+            for group_top in (1, 2):
+                check_route(rows, topk=min(6, E // groups), score=score, bias=b, groups=groups, group_topk=3,
+                            group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 384, 1000])
+def test_pairs_of_keys_a_step_apart(score, E):
+    """The last expert chosen and the next differ by less than fp32 shows, on either side of a clear order
+    of the others; in the last lanes and values too."""
+    rng = np.random.default_rng(E)
+    T, topk = 40, 8
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    x[:, -1] = np.float32(0.5)
+    x[:, 5] = np.float32(0.5) + np.float32(2.0 ** -22) * rng.integers(-2, 3, T).astype(np.float32)
+    b = rng.uniform(-0.3, 0.3, E).astype(np.float32)
+    s = np.array([oracle.router_scores(r, score) for r in x.astype(np.float64)])
+    # the pair is put where the choice ends: seven others stay ahead, the rest behind
+    b[-1] = b[5] = np.float32(2.0)
+    ahead = rng.choice(np.arange(6, E - 1), 7, replace=False)
+    b[ahead] = np.float32(4.0) + np.float32(0.25) * np.arange(7, dtype=np.float32)
+    c = s + b.astype(np.float64)
+    gap = np.abs(c[:, 5] - c[:, -1])
+    assert np.median(gap) < 2.0 ** -22 and np.all((gap > 2.0 ** -50) | (x[:, 5] == x[:, -1]))
+    check_route(torch.from_numpy(x), topk=topk, score=score, bias=torch.from_numpy(b))
