@@ -335,7 +335,8 @@ typedef struct tq_router {
  * The choice is that of the scores in 64 bits. Without a bias it is that of the logits themselves,
  * which order where scores round together, of groups by their largest too; sums of two are of
  * scores. Weights are fp32, off by less than 2^-18 of themselves, and 2^-22 times how far the
- * logit lies below the row's largest (2^-23 in all where measured).
+ * logit lies below the row's largest (2^-23 in all where measured); where a weight, or what scale
+ * multiplies, is below 2^-126, by max(1, |scale|) * 2^-147 more.
  *   R         host: the router.
  *   logits    device [T][R->E]: fp32, or bf16 with TQ_LOGITS_BF16; aligned to an element.
  *   T         tokens (0 is a successful no-op); T * E at most 2^33.

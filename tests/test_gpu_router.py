@@ -584,3 +584,22 @@ def test_pairs_of_keys_a_step_apart(score, E):
     gap = np.abs(c[:, 5] - c[:, -1])
     assert np.median(gap) < 2.0 ** -22 and np.all((gap > 2.0 ** -50) | (x[:, 5] == x[:, -1]))
     check_route(torch.from_numpy(x), topk=topk, score=score, bias=torch.from_numpy(b))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scale", [1.0, 1e-6, 1e4])
+def test_weights_below_the_smallest_normal_number(score, renorm, scale):
+    """Logits 80 to 110 below the largest: a weight, or what the scale multiplies, is below 2^-126. Its terms
+    are then multiples of 2^-149: off by max(1, |scale|) 2^-147 on top of the relative bound."""
+    x = np.full((16, 24), -300.0, dtype=np.float32)
+    x[:, 3] = 0.0
+    x[:, 5:12] = -np.random.default_rng(450).uniform(80, 110, (16, 7)).astype(np.float32)
+    R = router_of(24, dict(topk=8, score=score, renorm=renorm, scale=scale))
+    ids, w = ops().expert_route(R, torch.from_numpy(x).to(dev()))
+    want_ids, want = oracle.expert_route(x, 8, score=score, renorm=renorm, scale=scale)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    far = -np.take_along_axis(x.astype(np.float64), want_ids, 1)
+    assert np.sum(want / scale < 2.0 ** -126) > 40 and np.sum(want / scale > 2.0 ** -126) > 40
+    bound = (2.0 ** -18 + 2.0 ** -22 * far) * want + max(1.0, scale) * 2.0 ** -147
+    assert np.all(np.abs(f64(w) - want) <= bound)
