@@ -229,7 +229,7 @@ struct Mx8GemmArgs {
   int layout;            // 0: codes in store order; 1: repacked
   const uint8_t* units;
   const uint8_t* xa;     // E4M3 codes [T][in]
-  uint32_t xa_bytes;     // < 2^29
+  uint32_t xa_bytes;     // < 2^30
   const uint8_t* xs;     // E8M0 scales [T][in / 32]
   uint32_t xs_bytes;
   const float* gates;
@@ -317,8 +317,9 @@ struct RouteArgs {
   uint8_t* qscales;
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
-// The same in one launch for few slots, without hist, rank and the placement of items: counts,
-// offsets, pairs and items (in expert order) as there, but an expert's slots in any order.
+// What a GEMM needs of it in one launch for few slots: pairs and items as there (in expert order, without
+// the placement of items by token range), but an expert's slots in any order. counts, offsets, hist and
+// rank are not written.
 constexpr int64_t ROUTE_SMALL_SLOTS = 4096;
 hipError_t launch_route_small(const RouteArgs& a, hipStream_t s);
 
