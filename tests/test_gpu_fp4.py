@@ -339,3 +339,22 @@ def test_offsets_past_32_bits():
         want = o.mxfp4_expert_gemm(last, x, torch.zeros((T, 1), dtype=torch.int32, device=dev()),
                                    flags=o.TQ_FP4 | (mode or o.TQ_GEMM))
         assert torch.equal(got, want) and bool(want.any())
+
+
+@pytest.mark.parametrize("repack", [False, True])
+def test_fp8_products_beside_the_flag(repack):
+    """TQ_FP8 over the same layer and workspace as TQ_FP4: the product of MXFP8 activations, before and
+    after, and the same bits both times."""
+    o = ops()
+    layer, x, ids, gates = case(943, 5, 60, 2, 128, 1024)
+    L = o.Mxfp4Layer.from_host(layer)
+    L = L.repacked() if repack else L
+    xq = oracle.dequantize_mxfp8_rows(*oracle.quantize_mxfp8_rows(oracle.bf16_bits_to_f64(x)))
+    ref = oracle.expert_gemm_values(xq, ids, gates, 5, mxfp4_weight_fn(layer))
+    ws = torch.zeros(max(o.workspace_bytes(60, 2, 5, 128, 1024, f) for f in (o.TQ_FP8, o.TQ_FP4)), dtype=torch.uint8,
+                     device=dev())
+    args = to_dev(x, np.int16), to_dev(ids), to_dev(gates)
+    first = o.mxfp4_expert_gemm(L, *args, flags=o.TQ_FP8, ws=ws)
+    o.mxfp4_expert_gemm(L, *args, flags=o.TQ_FP4, ws=ws)
+    assert torch.equal(o.mxfp4_expert_gemm(L, *args, flags=o.TQ_FP8, ws=ws), first)
+    assert np.linalg.norm(first.cpu().numpy() - ref) <= 1e-3 * np.linalg.norm(ref)
