@@ -123,11 +123,11 @@ bool fp4_decode_fits(int64_t N, int groups) {
   return N <= tq::FP4_DECODE_SLOTS && N * groups * 8 <= (int64_t)1 << 20;
 }
 
-// Its one launch saves the GEMM's routing (2.5 to 5 us) but reads weights less evenly, and an expert's
-// rows 16 at a time. Decode against route and GEMM in us, by slots and groups of 128 channels: 8 x 12
-// of 5,120 inputs 9.3 and 13.7; 512 x 1 22 and 25; 64 x 8 of 2,048 inputs 11.9 and 11.3; 64 x 12 over
-// 384 experts 56 and 53, over 8 experts 12.2 and 14; 1,024 x 1 30 and 27; 128 x 12 99 and 90; 512 x 20
-// 46 and 32; 1,024 x 12 132 and 108. Two launches cost a call a little more than one.
+// Its one launch saves the launch that routes and converts, but reads weights less evenly, and an expert's
+// rows 16 at a time. Decode against route and GEMM on the GPU in us, over 384 experts of 5,120 inputs, by
+// slots and groups of 128 channels: 8 x 12 9.1 and 13.8; 512 x 1 22.4 and 25.6; 64 x 8 of 2,048 inputs
+// 16.3 and 16.9; 64 x 12 51 and 59, over 8 experts 11.9 and 14.9; 1,024 x 1 28.9 and 28.5; 128 x 12 89
+// and 90; 1,024 x 12 296 and 262; 512 x 20 344 and 320.
 constexpr int64_t FP4_DECODE_PAIRS = 1024;
 
 bool use_gemm(int64_t T, int topk, int E, int groups, uint32_t flags) {
@@ -1035,9 +1035,10 @@ int mx_expert_gemm(const MxLayer* L, const void* x, int64_t T, const int32_t* to
     tq::RouteArgs r = route_args(W, ws, topk_ids, N, L->E, L->out, y_slots);
     r.item_rows = tq::fp4_item_rows(N, L->E, L->out);
     // Token ranges pay off where an expert's channels are one group (8,192 tokens x 8 of 384, 128 x
-    // 5,120: 64 us, without them 71). With more, items of one expert, which read the same weights, run
-    // together instead, and the scan is quicker (8,192 x 8 of 32, 1,536 x 5,120: 345 and 337; 2,048 x
-    // 8 of 64, 1,536 x 2,560: 73 and 70, with the scan 82 and 75).
+    // 5,120: GEMM 60.5 us, without them 67). With more, items of one expert, which read the same weights,
+    // run together instead, and the scan is quicker (with and without ranges: 2,048 x 8 of 64, 1,536 x
+    // 2,560: 58.6 and 55.0, the call 76 and 72; 8,192 x 2 of 64, 512 x 2,560: the call 44.5 and 42.9;
+    // 8,192 x 8 of 32, 1,536 x 5,120: 313 and 314).
     if (L->out > 128) r.split_rows = 0;
     r.max_items = (int)std::min(N, (N + r.item_rows - 1) / r.item_rows + L->E);  // <= W.max_items
     r.qx = xb;

@@ -15,8 +15,9 @@
 //      lane computes its expert's key in 64 bits, where the definition lies, and the lanes change
 //      places. Where the last group kept is not ahead of the next by more than the errors, or more
 //      than 64 experts are candidates, steps 2 to 4 run once more in 64 bits throughout. (All rows
-//      in 64 bits took 29 us for 8,192 rows of 384, one wave alone 8.5; now 12.2, in 8 groups 16.6, of
-//      which one row that runs again takes up to 9; rows that all tie 88.);
+//      in 64 bits took 29 us for 8,192 rows of 384, one wave alone 8.5; now 11.7 under sigmoid and 12.9
+//      under softmax, in 8 groups 16 and 17, or up to 26 where some rows run again, which is one chunk
+//      in two under sigmoid and most under softmax; rows that all tie 83 to 98.);
 //   6. weighs: lane r computes its score from its logit in fp32, relative to the largest
 //      chosen one where they are renormalised, so that no sum of scores can underflow.
 // One row a wave: a chunk's rows fill the GPU eight times over, and a single row ends soonest.

@@ -207,7 +207,8 @@ __device__ __forceinline__ void f4_item(const Fp4GemmArgs& a, F4Shared<WAVES>& s
   // The epilogue: element 4 j + i of lane (n, h) is channel 8 j + 4 h + i of a block, of the block's
   // row n. Each wave brings its rows together in LDS (its own part of the stages, once no load
   // writes them any more) and writes them in pieces of 128 NB bytes: stored from the lanes as they
-  // are, 16 bytes of 32 rows at a time, the results of 8,192 tokens x 8 of 32, 1,536 x 5,120, took 95 us of 352.
+  // are, 16 bytes of 32 rows at a time, the results of 8,192 tokens x 8 of 32, 1,536 x 5,120, took 95 us
+  // of the 352 that this kernel took then.
   wait_vmcnt<0>();
   bare_barrier();
   constexpr int kLine = 128 * NB + 16;  // the 16 bytes more put a row's pieces on other banks
@@ -288,16 +289,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp4_gemm_kernel(Fp4GemmArgs a) 
 
 // Items of 256 rows and channels read each operand half as often, but one fills a compute unit; they
 // are the faster ones where experts have many rows and their items (with half of an expert's last one
-// empty) are enough for most of the GPU. Measured, 256 against 128: 8,192 tokens x 8 of 32, 1,536 x
-// 5,120: 337 and 397 us; 2,048 x 8 of 64, 1,536 x 2,560: 70 and 85; 8,192 x 2 of 64, 512 x 2,560 (192
-// items): 26 and 30; 700 x 6 of 20, 1,424 x 7,168 (156): 61 and 61; 1,024 x 4 of 16, 1,536 x 5,120
-// (144): 38 and 35; 512 x 8 of 8 (120): 37 and 33.
+// empty) are enough for most of the GPU. The GEMM between events, 256 against 128: 8,192 tokens x 8 of
+// 32, 1,536 x 5,120: 314 and 378 us (256 in a trace that alternates between two sets of inputs: 325 to
+// 329); 2,048 x 8 of 64, 1,536 x 2,560: 55 and 61; 8,192 x 2 of 64, 512 x 2,560 (192 items): 26 and 28;
+// 700 x 6 of 20, 1,424 x 7,168 (156): 45 and 46; 1,024 x 4 of 16, 1,536 x 5,120 (144): 37 and 33; 512 x
+// 8 of 8 (120): 35 and 29.
 //
 // What an item of 256 x 256 x 5,120 spends: 91,000 clocks at 1.9 GHz, of which 67,000 in the loop (the
 // products alone need 41,000; the rest waits for loads that take up to 5,000 clocks beside the other
 // units' stores), 11,000 until its first stages are there and 12,000 on its stores. 4 waves of 128 x
-// 128, which read LDS a third less, take as long (329 us and 337; 29 and 26 in the third case above);
-// items of 128 x 256, two on a compute unit, 376.
+// 128, which read LDS a third less, take as long (2 % less there, 12 % more in the third case above);
+// items of 128 x 256, two on a compute unit, 12 % longer.
 int fp4_item_rows(int64_t N, int E, int out) {
   if (out <= 128 || N < 160 * (int64_t)E) return 128;
   const int64_t items = (N / 256 + E / 2) * ((out + 255) / 256);

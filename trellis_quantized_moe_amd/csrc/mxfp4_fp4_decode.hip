@@ -7,19 +7,19 @@
 // its waves looks through all route ids for the expert's slots, so every touched weight is read once
 // (per 16 rows). The four waves share out the inputs. Per window of 4 steps of 128 inputs a wave
 //   - has asked for the window's codes and scales of its channels one window ahead (two windows ahead
-//     were slower, one token 10.6 us instead of 9.3): lane (n, q)
+//     were 15 % slower for one token): lane (n, q)
 //     loads the 16 bytes of block q of a step of channel n, and 16 scale bytes (4 steps) of it;
 //   - converts the rows' inputs to MXFP4 (F29): lane p block p % 16 of row p / 16, loaded one
 //     conversion ahead, into LDS, from which lane (n, q) reads block q of row n;
 //   - multiplies: v_mfma_scale_f32_16x16x128_f8f6f4 per step and 16 channels.
 // The waves' sums are added in order, multiplied by the gate and written once.
 //
-// Bound by the weights' bytes where there are many (64 tokens x 8 of 384 experts, 128 x 5,120: 22.0 us
-// for about 98 MB), else by the latency of its dependent loads (one token, 1,536 x 5,120: 9.3 us; 128
-// x 5,120: 5.6). 32 channels a workgroup convert the rows half as often, 16 make twice as many
-// workgroups, which is faster until there are two for every compute unit (16 and 32 channels: one
-// token x 8 of 128 outputs 6.0 and 7.0 us, of 1,536 outputs 9.9 and 10.1; two tokens 17.0 and 14.3; 64
-// tokens x 8 of 128 outputs 25.4 and 22.7).
+// Bound by the weights' bytes where there are many (64 tokens x 8 of 384 experts, 128 x 5,120: 21.5 us
+// for about 98 MB), else by the latency of its dependent loads (one token, 1,536 x 5,120: 8.7 us; 128
+// x 5,120: 5.1). 32 channels a workgroup convert the rows half as often, 16 make twice as many
+// workgroups, which is faster until there are two for every compute unit (16 and 32 channels, of
+// 5,120 inputs: one token x 8 of 128 outputs 5.1 and 5.9 us, of 1,536 outputs 9.0 and 9.5; two tokens
+// 15.4 and 14.1; 64 tokens x 8 of 128 outputs over 128 experts 15.2 and 13.0).
 #include "gemm_core.h"
 #include "mx_unit.h"
 #include "mxfp4_quant.h"

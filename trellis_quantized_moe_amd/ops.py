@@ -635,7 +635,8 @@ def _check_logits(router, logits):
 
 def expert_route(router, logits, ids=None, w=None):
     """(topk_ids int32 [T, topk], topk_w fp32 [T, topk]) of fp32 or bf16 logits [T, E] (see
-    expert_route in include/tq.h)."""
+    expert_route in include/tq.h). The weights are not connected to logits that require a gradient:
+    expert_route_backward computes it."""
     T, dev, flags = _check_logits(router, logits)
     shape = (T, router.topk)
     if ids is None:
@@ -652,8 +653,9 @@ def expert_route(router, logits, ids=None, w=None):
 
 
 def expert_route_backward(router, logits, ids, dw, dlogits=None):
-    """The gradient [T, E] of expert_route's weights, of the logits' type, from dw [T, topk] (see
-    expert_route_backward in include/tq.h)."""
+    """The gradient [T, E] of expert_route's weights with respect to the logits, of their type, from
+    dw [T, topk], the gradient with respect to the weights (see expert_route_backward in
+    include/tq.h)."""
     T, dev, flags = _check_logits(router, logits)
     shape = (T, router.topk)
     _check_rows("ids", ids, _I32, dev, shape)
