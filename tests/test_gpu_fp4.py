@@ -358,3 +358,36 @@ def test_fp8_products_beside_the_flag(repack):
     o.mxfp4_expert_gemm(L, *args, flags=o.TQ_FP4, ws=ws)
     assert torch.equal(o.mxfp4_expert_gemm(L, *args, flags=o.TQ_FP8, ws=ws), first)
     assert np.linalg.norm(first.cpu().numpy() - ref) <= 1e-3 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("T", [3, 64, 300])
+@pytest.mark.parametrize("places", [(0,), (5,), (0, 2), tuple(range(0, 16, 2))])
+@pytest.mark.parametrize("ratio", [2, 9, 16, 18, 21, 25, 28])
+def test_large_blocks_that_cancel(T, places, ratio):
+    """Blocks whose products cancel, 2^ratio times as large as those of the others: the sum that is left
+    keeps to the bound of fp32 additions, and at a ratio whose sums all have 24 bits it is exact."""
+    o = ops()
+    out, in_ = 48, 512
+    rng = rng_for(944, ratio)
+    values = np.array([0.5, 1, 1.5, 2, 3, 4, 6])
+    codes = rng.integers(0, 16, (out, in_)).astype(np.uint8)
+    x = rng.choice(values, (T, in_)) * rng.choice([-1, 1], (T, in_))
+    for b in places:
+        s, h = slice(32 * b, 32 * b + 16), slice(32 * b + 16, 32 * b + 32)
+        x[:, s] = 2.0 ** ratio * rng.choice(values, (T, 16))
+        codes[:, s] = rng.integers(1, 8, (out, 16))
+        x[:, h], codes[:, h] = -x[:, s], codes[:, s]
+    bits = oracle.f32_to_bf16_bits_rne(x.astype(np.float32))
+    scales = np.full((out, in_ // 32), 127, np.uint8)
+    unit = np.concatenate([oracle.mxfp4_pack(codes).reshape(-1), scales.reshape(-1)])
+    layer = dict(E=1, out=out, units=unit, **{"in": in_})
+    L = o.Mxfp4Layer.from_host(layer)
+    ids = np.zeros((T, 1), np.int32)
+    y, a = reference(layer, bits, ids, None)
+    for mode in (o.TQ_GEMV, o.TQ_GEMM):
+        for l in (L, L.repacked()):
+            got = o.mxfp4_expert_gemm(l, to_dev(bits, np.int16), to_dev(ids), flags=o.TQ_FP4 | mode)
+            compare(got, y, a, in_, 1, 0)
+            if ratio <= 9:  # sums are multiples of 2^-2 below 16 * 36 * 32 * 2^9 = 2^23.2: exact up to 2^22
+                exact = a[:, 0] <= 2.0 ** 22
+                assert exact.any() and np.array_equal(got.cpu().numpy()[:, 0][exact], y[:, 0][exact])
