@@ -340,7 +340,8 @@ typedef struct tq_router {
  *   R         host: the router.
  *   logits    device [T][R->E]: fp32, or bf16 with TQ_LOGITS_BF16; aligned to an element.
  *   T         tokens (0 is a successful no-op); T * E at most 2^33.
- *   topk_ids  device int32 [T][topk].   topk_w  device fp32 [T][topk].
+ *   topk_ids  device int32 [T][topk].   topk_w  device fp32 [T][topk]. Neither may overlap the
+ *             logits, the bias or the other.
  *   flags     0 or TQ_LOGITS_BF16.
  * A logit of -inf (or a bias of -inf) takes its expert out of the choice; a token with fewer
  * than topk experts left gets id -1 and weight 0 in the slots that remain, so a padded token's
@@ -365,7 +366,7 @@ int expert_route(const tq_router* R, const void* logits, int64_t T, int32_t* top
  *             makes its row NaN. A row of -1 alone is 0, whatever its logits.
  *   dw        device fp32 [T][topk].
  *   dlogits   device [T][E], of the logits' type; every entry is written. It may be the logits
- *             themselves.
+ *             themselves; other overlap with an input is not allowed.
  * Other arguments as expert_route.
  */
 int expert_route_backward(const tq_router* R, const void* logits, int64_t T,
